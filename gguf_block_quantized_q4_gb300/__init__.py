@@ -24,6 +24,8 @@ LIB_PATH = os.path.join(HERE, "libmq.so")
 
 Q4_0, Q4_1, Q5_0, Q5_1, Q8_0, Q4_K, Q5_K, Q6_K = 2, 3, 6, 7, 8, 12, 13, 14
 F16, BF16 = 1, 30  # unquantised weights: decode matvec only
+F32 = 0  # activations of rope_store / attn_decode; not a weight type
+ATTN_TRACK = 1
 REG_DEFAULT, REG_NO_MMQ_PLANE, REG_MMQ_FROM_DECODE_PLANE = 0, 1, 2
 # (elements, bytes) per block; f16 / bf16 rows count in units of 32 elements (K % 32 == 0)
 BLOCK = {Q4_0: (32, 18), Q4_1: (32, 20), Q5_0: (32, 22), Q5_1: (32, 24), Q8_0: (32, 34),
@@ -31,7 +33,7 @@ BLOCK = {Q4_0: (32, 18), Q4_1: (32, 20), Q5_0: (32, 22), Q5_1: (32, 24), Q8_0: (
 
 STATUS = ["MQ_OK", "MQ_ERR_ARG", "MQ_ERR_TYPE", "MQ_ERR_SHAPE", "MQ_ERR_PAYLOAD",
           "MQ_ERR_ALIGN", "MQ_ERR_CUDA", "MQ_ERR_OOM", "MQ_ERR_LAUNCH", "MQ_ERR_TIMEOUT",
-          "MQ_ERR_STATE"]
+          "MQ_ERR_STATE", "MQ_ERR_INDEX"]
 
 # The C ABI: name -> (restype, argtypes)
 _P, _I64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
@@ -57,6 +59,12 @@ ABI = {
                                  ctypes.POINTER(_P)]),
     "mq_ffn_gu_matvec": (_ST, [ctypes.c_int, _P, _P, _P, _I64, _I64, ctypes.c_int, _P]),
     "mq_ffn_gu_mmq": (_ST, [ctypes.c_int, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "mq_rope_store": (_ST, [_P, _P, ctypes.c_int, _P, _I64, _P, _P, _P, _P, _I64, ctypes.c_int,
+                            _P]),
+    "mq_attn_workspace_bytes": (_SZ, [_P, _I64, ctypes.c_int, _I64, ctypes.c_uint32]),
+    "mq_attn_decode": (_ST, [_P, ctypes.c_int, _P, _P, _P, _I64, _P, _I64, ctypes.c_int, _I64,
+                             ctypes.c_float, _I64, ctypes.c_uint32, _P, _SZ, _P]),
+    "mq_kv_evict": (_ST, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
     "mq_stream_status": (_ST, [_P]),
     "mq_last_error": (ctypes.c_char_p, []),
     "mq_status_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -384,6 +392,253 @@ def mmq_blockdots(W: Weight, xq, M: int, D=None, stream=None):
     _check(lib().mq_mmq_blockdots(W.qtype, W.handle, _ptr(xq), _ptr(D), M, W.N, W.K,
                                   _stream(stream)))
     return D
+
+
+# ---- decode attention over a paged key-value cache ------------------------------------------
+
+
+class _KVCacheStruct(ctypes.Structure):  # mq_kv_cache
+    _fields_ = [("type", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_pages", _I64), ("page_stride", _I64),
+                ("head_stride", _I64), ("slot_stride", _I64), ("k", _P), ("v", _P),
+                ("k_scale", _P), ("v_scale", _P), ("weight_sum", _P)]
+
+
+class _RopeStruct(ctypes.Structure):  # mq_rope
+    _fields_ = [("table", _P), ("max_pos", _I64), ("rot_dim", ctypes.c_int),
+                ("pairs", ctypes.c_int), ("n_axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 128)]
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _io(t):
+    """The C type code of an activation tensor."""
+    code = _IO.get(str(t.dtype))
+    _need(code is not None and t.is_cuda, f"a CUDA tensor of f32, f16 or bf16 is required, got "
+          f"{t.dtype} on {t.device}")
+    return code
+
+
+_IO = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+
+
+class KVCache:
+    """A paged cache over the caller's planes (mq_kv_cache): k, v [page][head][slot][head_dim]
+    (layout "hnd") or [page][slot][head][head_dim] ("nhd") of f16, bf16, or int8 with f16
+    scales k_scale, v_scale of the same axes and head_dim / 32; sums f32 of the same axes
+    without head_dim (the weight each row has gathered), or None.  The planes may be views with
+    larger outer strides, the same in rows for all of them."""
+
+    def __init__(self, kind, k, v, k_scale=None, v_scale=None, sums=None, layout="hnd"):
+        _need(layout in ("hnd", "nhd"), f"layout {layout!r} is neither 'hnd' nor 'nhd'")
+        want = {F16: "torch.float16", BF16: "torch.bfloat16", Q8_0: "torch.int8"}.get(kind)
+        _need(want is not None, f"cache type {kind} is not F16, BF16 or Q8_0")
+        _need(k.dim() == 4 and k.shape == v.shape, "k and v are [page][...][...][head_dim]")
+        d = k.shape[3]
+        planes = [("k", k, want, d), ("v", v, want, d)]
+        if kind == Q8_0:
+            _need(k_scale is not None and v_scale is not None, "a Q8_0 cache needs its scales")
+            planes += [("k_scale", k_scale, "torch.float16", d // 32),
+                       ("v_scale", v_scale, "torch.float16", d // 32)]
+        if sums is not None:
+            planes.append(("sums", sums, "torch.float32", 1))
+        # strides in rows (that of an axis of one element says nothing)
+        rows = [k.stride(i) // max(d, 1) if k.shape[i] > 1 else 1 for i in range(3)]
+        for name, t, dtype, width in planes:
+            _need(t.is_cuda and str(t.dtype) == dtype, f"{name} must be a CUDA tensor of {dtype}")
+            _need(tuple(t.shape[:3]) == tuple(k.shape[:3]) and
+                  (t.dim() == 3 if name == "sums" else t.dim() == 4 and t.shape[3] == width),
+                  f"{name} has shape {tuple(t.shape)}")
+            _need(all(t.shape[i] == 1 or t.stride(i) == rows[i] * width for i in range(3)) and
+                  (t.dim() == 3 or width == 1 or t.stride(3) == 1),
+                  f"{name}: rows are not contiguous, or its strides differ from k's")
+        head, slot = (1, 2) if layout == "hnd" else (2, 1)
+        self.kind, self.k, self.v, self.k_scale, self.v_scale = kind, k, v, k_scale, v_scale
+        self.sums, self.layout = sums, layout
+        self.n_pages, self.n_kv_heads, self.page_size = k.shape[0], k.shape[head], k.shape[slot]
+        self.head_dim = d
+
+        def ptr(t):
+            return None if t is None else t.data_ptr()
+        self._c = _KVCacheStruct(kind, self.n_kv_heads, d, self.page_size, self.n_pages, rows[0],
+                                 rows[head], rows[slot], ptr(k), ptr(v),
+                                 ptr(k_scale) if kind == Q8_0 else None,
+                                 ptr(v_scale) if kind == Q8_0 else None, ptr(sums))
+        self._ref = ctypes.addressof(self._c)
+
+
+def kv_cache(kind, n_pages, page_size, n_kv_heads, head_dim, sums=False, layout="hnd",
+             device="cuda") -> KVCache:
+    """A KVCache over new zeroed planes."""
+    import torch
+    _need(kind in (F16, BF16, Q8_0), f"cache type {kind} is not F16, BF16 or Q8_0")
+    outer = ((n_pages, n_kv_heads, page_size) if layout == "hnd"
+             else (n_pages, page_size, n_kv_heads))
+    dtype = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8}[kind]
+
+    def plane(*shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=device)
+    k, v = (plane(*outer, head_dim, dtype=dtype) for _ in range(2))
+    ks, vs = ((plane(*outer, head_dim // 32, dtype=torch.float16) for _ in range(2))
+              if kind == Q8_0 else (None, None))
+    return KVCache(kind, k, v, ks, vs, plane(*outer, dtype=torch.float32) if sums else None,
+                   layout)
+
+
+def rope_table(max_pos, inv_freq, scale=1.0, device="cuda"):
+    """The f32 table [max_pos][len(inv_freq)][2] of scale * (cos, sin)(position * inv_freq),
+    computed in 64 bits."""
+    import torch
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * f
+    return (torch.stack([a.cos(), a.sin()], -1) * scale).float()
+
+
+def rope_axes(sections, weave=False):
+    """The axis of each pair for sections[a] pairs on axis a: contiguous, or woven (pair i on
+    the axes in turn while they have pairs left)."""
+    if not weave:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] -= 1
+    return out
+
+
+class Rope:
+    """A rotation (mq_rope): table f32 [max_pos][pairs of a head][2] (rope_table), axis: the
+    position axis of each pair (default: all on axis 0); pairs: dims (2i, 2i+1) instead of
+    (i, i + rot_dim/2)."""
+
+    def __init__(self, table, axis=None, pairs=False):
+        _need(table.dim() == 3 and table.shape[2] == 2 and table.is_contiguous() and table.is_cuda
+              and str(table.dtype) == "torch.float32",
+              "table must be a contiguous CUDA f32 tensor [max_pos][rot_dim/2][2]")
+        half = table.shape[1]
+        axis = [0] * half if axis is None else [int(a) for a in axis]
+        _need(len(axis) == half and half <= 128 and all(0 <= a < 4 for a in axis),
+              "axis names one of up to 4 axes for each of at most 128 pairs")
+        self.table, self.axis, self.n_axes = table, axis, max(axis, default=0) + 1
+        self._c = _RopeStruct(table.data_ptr(), table.shape[0], 2 * half, int(pairs), self.n_axes,
+                              (ctypes.c_uint8 * 128)(*axis))
+        self._ref = ctypes.addressof(self._c)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+def rope_store(cache: KVCache, rope: Rope, qkv, pos, slot, n_heads, bias=None, q=None,
+               stream=None):
+    """Rotate and store T tokens: qkv [T][(n_heads + 2 n_kv_heads) head_dim] (f32, f16 or bf16;
+    rows may be strided), pos int32 [n_axes][T] (or [T] for one axis), slot int64 [T].  Returns
+    the rotated queries [T][n_heads][head_dim]."""
+    import torch
+    T, width = qkv.shape
+    io = _io(qkv)
+    _need(width == (n_heads + 2 * cache.n_kv_heads) * cache.head_dim and
+          (qkv.stride(1) == 1 or T == 0), f"qkv has shape {tuple(qkv.shape)}")
+    _need(pos.dtype == torch.int32 and pos.numel() >= rope.n_axes * T and pos.shape[-1] == T and
+          pos.is_contiguous(), "pos must be contiguous int32 [n_axes][T]")
+    _need(slot.dtype == torch.int64 and slot.shape == (T,) and slot.is_contiguous(),
+          "slot must be contiguous int64 [T]")
+    if bias is not None:
+        _need(bias.dtype == torch.float32 and bias.shape == (width,) and bias.is_contiguous(),
+              "bias must be contiguous f32, one per column of qkv")
+    if q is None:
+        q = torch.empty((T, n_heads, cache.head_dim), dtype=qkv.dtype, device=qkv.device)
+    else:
+        _need(q.dtype == qkv.dtype and q.is_contiguous() and
+              q.numel() == T * n_heads * cache.head_dim, "q must be contiguous, of qkv's type")
+    _check(lib().mq_rope_store(cache._ref, rope._ref, io, qkv.data_ptr(),
+                               qkv.stride(0) if T > 1 else width,
+                               None if bias is None else bias.data_ptr(), pos.data_ptr(),
+                               slot.data_ptr(), q.data_ptr(), T, n_heads, _raw_stream(stream)))
+    return q
+
+
+def attn_workspace(cache: KVCache, n_seqs, n_heads, max_len, track=False):
+    """A zeroed workspace for attn_decode calls of up to this size."""
+    import torch
+    n = lib().mq_attn_workspace_bytes(cache._ref, n_seqs, n_heads, max_len, int(bool(track)))
+    if n == 0:
+        raise MQError(STATUS.index("MQ_ERR_ARG"), lib().mq_last_error().decode(errors="replace"))
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def _check_pages(name, pages, n_seqs):
+    _need(str(pages.dtype) == "torch.int32" and pages.dim() == 2 and pages.shape[0] == n_seqs and
+          (pages.stride(1) == 1 or pages.shape[1] == 1), f"{name} must be int32 [S][pages]")
+    return pages.stride(0) if n_seqs > 1 else max(pages.shape[1], 1)
+
+
+def attn_decode(cache: KVCache, q, pages, lens, max_len, scale=None, window=0, track=False,
+                ws=None, o=None, stream=None):
+    """Attention of one new token per sequence: q [S][n_heads][head_dim] (f32, f16 or bf16),
+    pages int32 [S][max pages], lens int32 [S] (at most max_len).  scale defaults to
+    head_dim ** -0.5.  ws: a workspace kept from attn_workspace (else one is made for the
+    call).  Returns o, of q's shape and type."""
+    import torch
+    S, n_heads, d = q.shape
+    io = _io(q)
+    _need(d == cache.head_dim and q.is_contiguous(), f"q has shape {tuple(q.shape)} or strides")
+    pages_ld = _check_pages("pages", pages, S)
+    _need(lens.dtype == torch.int32 and lens.shape == (S,) and lens.is_contiguous(),
+          "lens must be contiguous int32 [S]")
+    _need(max_len <= pages.shape[1] * cache.page_size,
+          f"max_len={max_len} is more than {pages.shape[1]} pages hold")
+    _need(not track or cache.sums is not None, "the cache keeps no weight sums")
+    if ws is None:
+        ws = attn_workspace(cache, S, n_heads, max_len, track)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _need(o.dtype == q.dtype and o.shape == q.shape and o.is_contiguous(),
+              "o must be contiguous, of q's shape and type")
+    _check(lib().mq_attn_decode(cache._ref, io, q.data_ptr(), o.data_ptr(), pages.data_ptr(),
+                                pages_ld, lens.data_ptr(), S, n_heads, max_len,
+                                d ** -0.5 if scale is None else scale, window, int(bool(track)),
+                                ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+    return o
+
+
+def kv_evict(cache: KVCache, pages, lens, max_len, new_pages, keep, sink=0, recent=0, kept=None,
+             new_lens=None, stream=None):
+    """Copy the rows that stay (the first sink, the last recent and the heaviest of the rest, keep
+    in all) to new_pages.  Returns (kept int32 [S][n_kv_heads][keep], new_lens int32 [S])."""
+    import torch
+    S = lens.shape[0]
+    pages_ld = _check_pages("pages", pages, S)
+    new_ld = _check_pages("new_pages", new_pages, S)
+    _need(lens.dtype == torch.int32 and lens.dim() == 1 and lens.is_contiguous(),
+          "lens must be contiguous int32 [S]")
+    _need(max_len <= pages.shape[1] * cache.page_size and
+          keep <= new_pages.shape[1] * cache.page_size,
+          f"max_len={max_len} or keep={keep} is more than the pages hold")
+    _need(cache.sums is not None, "the cache keeps no weight sums")
+    if kept is None:
+        kept = torch.empty((S, cache.n_kv_heads, keep), dtype=torch.int32, device=lens.device)
+    else:
+        _need(kept.dtype == torch.int32 and kept.is_contiguous() and
+              kept.numel() == S * cache.n_kv_heads * keep, "kept must be int32 [S][heads][keep]")
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    else:
+        _need(new_lens.dtype == torch.int32 and new_lens.shape == lens.shape and
+              new_lens.is_contiguous(), "new_lens must be contiguous int32 [S]")
+    _check(lib().mq_kv_evict(cache._ref, pages.data_ptr(), pages_ld, lens.data_ptr(), S, max_len,
+                             new_pages.data_ptr(), new_ld, keep, sink, recent, kept.data_ptr(),
+                             new_lens.data_ptr(), _raw_stream(stream)))
+    return kept, new_lens
 
 
 def stream_status(stream=None):

@@ -13,6 +13,7 @@
 #include <mutex>
 #include <vector>
 
+#include "kv.cuh"
 #include "mq_common.cuh"
 
 namespace mq {
@@ -77,6 +78,7 @@ extern "C" const char *mq_status_name(mq_status s) {
     case MQ_ERR_LAUNCH: return "MQ_ERR_LAUNCH";
     case MQ_ERR_TIMEOUT: return "MQ_ERR_TIMEOUT";
     case MQ_ERR_STATE: return "MQ_ERR_STATE";
+    case MQ_ERR_INDEX: return "MQ_ERR_INDEX";
   }
   return "MQ_ERR_UNKNOWN";
 }
@@ -423,8 +425,8 @@ extern "C" mq_status mq_weight_unpack(const mq_weight *w, void *host_bytes, size
 }
 
 // A pointer the device can read/write as global memory.
-static mq_status check_dev_ptr(const char *site, const char *name, const void *p, int dev,
-                               size_t align) {
+mq_status mq::check_dev_ptr(const char *site, const char *name, const void *p, int dev,
+                            size_t align) {
   if (!p) return fail(MQ_ERR_ARG, "%s: %s is NULL", site, name);
   if (reinterpret_cast<uintptr_t>(p) % align)
     return fail(MQ_ERR_ALIGN, "%s: %s=%p is not %zu-byte aligned", site, name, p, align);
@@ -436,7 +438,7 @@ static mq_status check_dev_ptr(const char *site, const char *name, const void *p
                 cudaGetErrorName(e));
   }
   if (a.type == cudaMemoryTypeDevice && a.device != dev)
-    return fail(MQ_ERR_ARG, "%s: %s=%p lives on device %d, the weight on device %d", site, name,
+    return fail(MQ_ERR_ARG, "%s: %s=%p lives on device %d, the call is on device %d", site, name,
                 p, a.device, dev);
   if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
     return fail(MQ_ERR_ARG, "%s: %s=%p is host memory (type %d); a device pointer is required",
@@ -718,12 +720,17 @@ extern "C" mq_status mq_stream_status(mq_stream stream) {
   mq_status s;
   if ((s = current_state(&st, site)) != MQ_OK) return s;
   CK(cudaStreamSynchronize((cudaStream_t)stream), site);
-  int h[2] = {0, 0};
+  int h[4] = {0, 0, 0, 0};
   CK(cudaMemcpy(h, st->status, sizeof(h), cudaMemcpyDeviceToHost), site);
   if (h[0] != 0) {
-    CK(cudaMemset(st->status, 0, 64), site);
+    CK(cudaMemset(st->status, 0, 8), site);
     return fail(MQ_ERR_TIMEOUT, "%s: a bounded device-side wait expired (code %d, kernel id %d)",
                 site, h[0], h[1]);
+  }
+  if (h[kStatusIndexWord] != 0) {
+    CK(cudaMemset(st->status + kStatusIndexWord, 0, 8), site);
+    return fail(MQ_ERR_INDEX, "%s: %s %d is outside its range; what it stands for was left out",
+                site, index_error_name(h[kStatusIndexWord]), h[kStatusIndexWord + 1]);
   }
   return MQ_OK;
 }

@@ -91,6 +91,9 @@ constexpr int kMaxB = 8;
 constexpr int kRowGroup = 128; // decode-plane row group (rows per matvec CTA)
 constexpr int kChunk = 256;    // decode-plane K chunk
 constexpr int kStatusTimeout = 1;
+// words of the device status: 0, 1 a timeout's code and site; 2, 3 an index error's code
+// (IndexError) and the value met
+constexpr int kStatusIndexWord = 2;
 
 // ---- per-thread error reporting ------------------------------------------
 mq_status fail(mq_status s, const char *fmt, ...);
@@ -101,7 +104,7 @@ struct DeviceState {
   bool ready = false;
   int sms = 0;
   int smem_optin = 0;
-  int *status = nullptr;  // device status word for bounded waits (code, kernel id)
+  int *status = nullptr;  // device status words (timeout code, site; index code, value)
   cudaStream_t reg_stream = nullptr;
   uint8_t *static_xq = nullptr;  // mq_mmq_fused_static's scratch (device symbol address)
   // mq_mmq_host: the stream that copies y back while the MMQ's next rows run, and its events
@@ -117,6 +120,9 @@ struct DeviceState {
 };
 DeviceState *device_state(int dev);  // nullptr if mq_init(dev) was not called
 mq_status current_state(DeviceState **st, const char *site);
+
+// A pointer the device can read/write as global memory, aligned to `align` bytes.
+mq_status check_dev_ptr(const char *site, const char *name, const void *p, int dev, size_t align);
 
 // ---- kernel launchers (defined per translation unit) ----------------------
 mq_status repack_weight(mq_weight *w, const uint8_t *raw_dev, bool mmq, cudaStream_t s);

@@ -80,6 +80,7 @@ extern "C" {
  * Q5_0, Q5_1 and Q5_K are among the types its matmul whitelist and weight gate admit
  * (§4.3, §4.6). */
 typedef enum {
+    MQ_F32 = 0, /* the type of activations in mq_rope_store / mq_attn_decode; not a weight type */
     MQ_F16 = 1, MQ_Q4_0 = 2, MQ_Q4_1 = 3, MQ_Q5_0 = 6, MQ_Q5_1 = 7, MQ_Q8_0 = 8,
     MQ_Q4_K = 12, MQ_Q5_K = 13, MQ_Q6_K = 14, MQ_BF16 = 30
 } mq_type;
@@ -95,7 +96,9 @@ typedef enum {
     MQ_ERR_OOM = 7,      /* device allocation failed at registration */
     MQ_ERR_LAUNCH = 8,   /* a kernel launch or smem opt-in was refused (message names the kernel) */
     MQ_ERR_TIMEOUT = 9,  /* a bounded device-side wait expired (reported by mq_stream_status) */
-    MQ_ERR_STATE = 10    /* mq_init was not called for the current device */
+    MQ_ERR_STATE = 10,   /* mq_init was not called for the current device */
+    MQ_ERR_INDEX = 11    /* a kernel met a position, slot, page or length outside its range, and
+                            left out what it stands for (reported by mq_stream_status) */
 } mq_status;
 
 /* Opaque weight handle: library-owned device planes built at registration. */
@@ -119,8 +122,8 @@ typedef void *mq_stream;
  * the calling thread).  Queries the SM count and the shared-memory opt-in
  * limit, opts every kernel that needs more than 48 KiB of dynamic shared
  * memory in (once per device, outside any stream capture: "CUDA Backend
- * Design" §2.4, the eager pre-warm), allocates the per-device status word
- * used by bounded waits and looks up the address of mq_mmq_fused_static's
+ * Design" §2.4, the eager pre-warm), allocates the per-device status words
+ * of bounded waits and index checks and looks up the address of mq_mmq_fused_static's
  * scratch.  Idempotent.  Must precede every other call for that device.  Each
  * call also reads the tests' switches MQ_TEST_FAIL_LAUNCH, MQ_TEST_EXPIRE_WAIT and
  * MQ_TEST_NO_XPLANE from the environment (no hot-path call reads it).
@@ -318,10 +321,132 @@ mq_status mq_ffn_gu_matvec(mq_type type, const mq_weight *W, const float *x, flo
 mq_status mq_ffn_gu_mmq(mq_type type, const mq_weight *W, const void *xq, float *h, int64_t M,
                         int64_t N, int64_t K, mq_stream stream);
 
+/* ---- decode attention over a paged key-value cache ("minfer CUDA Backend Design" §4.3 and
+ * §4.7: the attention, RoPE and KV-store nodes around the quantised matmuls; "Architecture
+ * Execution Plan" C4: cells of f16 or Q8_0 rows; C8: paged sharing).  The pages name these
+ * operations without writing them out; the formulas stand at each call. */
+
+/* A paged cache: planes the caller owns, described by value (nothing is kept between calls).
+ * A row is head_dim consecutive elements: the key (or value) of one cached token and kv head.
+ * Row (page p, kv head h, slot j) has the index
+ *     r = p*page_stride + h*head_stride + j*slot_stride
+ * in every plane: k and v at element r*head_dim, their scales at element r*(head_dim/32),
+ * weight_sum at element r.  Any strides that keep the rows apart will do:
+ * [page][head][slot] is page_stride = n_kv_heads*page_size, head_stride = page_size,
+ * slot_stride = 1; [page][slot][head] is page_stride = page_size*n_kv_heads,
+ * head_stride = 1, slot_stride = n_kv_heads.
+ *   type       MQ_F16, MQ_BF16, or MQ_Q8_0: int8 quants in k / v and one f16 scale d per 32
+ *              elements in k_scale / v_scale, value = d*q.  The scales have planes of their own
+ *              because a 34-byte block would leave every row unaligned.
+ *   head_dim   64, 96, 128, 192 or 256
+ *   page_size  slots of a page, 1..65536 (any number; not only powers of two)
+ *   weight_sum f32, the attention weight each row has gathered (MQ_ATTN_TRACK adds,
+ *              mq_rope_store clears a row it stores, mq_kv_evict selects by it and moves it);
+ *              NULL if not kept
+ * Planes 16-byte aligned.  Position i of a sequence lives in slot i % page_size of the page
+ * pages[s*pages_ld + i / page_size] (int32 entries; only the entries below the sequence's
+ * length are read). */
+typedef struct {
+    mq_type type;
+    int n_kv_heads, head_dim, page_size;
+    int64_t n_pages;
+    int64_t page_stride, head_stride, slot_stride;
+    void *k, *v;
+    void *k_scale, *v_scale;
+    float *weight_sum;
+} mq_kv_cache;
+
+/* A rotation with up to four position axes (time, height, width, ...).  Pair i of a head
+ * (i < rot_dim/2) turns by the angle of the row table[p][i], p the token's position on axis
+ * axis[i]: contiguous sections, axes woven through the pairs or any other map.
+ *   table     device f32 [max_pos][rot_dim/2][2]: cosine and sine (any frequency scaling and
+ *             attention factor are the table's)
+ *   rot_dim   multiple of 8, <= head_dim; dims from rot_dim on are passed through
+ *   pairs     0: pair i is dims (i, i + rot_dim/2); 1: dims (2i, 2i + 1)
+ *   n_axes    1..4; axis[i] < n_axes */
+typedef struct {
+    const float *table;
+    int64_t max_pos;
+    int rot_dim, pairs, n_axes;
+    uint8_t axis[128];
+} mq_rope;
+
+/* mq_rope_store -- rotate the queries and keys of T tokens and store keys and values in the
+ * cache.  qkv: device [T] rows of ld elements of type io (MQ_F32, MQ_F16 or MQ_BF16), of which
+ * the first (n_heads + 2*n_kv_heads)*head_dim are read: query heads, key heads, value heads
+ * (the fused attn_qkv product, "CUDA Backend Design" §4.6).  bias: f32, one per element of a
+ * row, or NULL.  pos: int32 [n_axes][T].  slot: int64 [T], page*page_size + offset; a negative
+ * slot stores nothing for its token.  q: device [T][n_heads*head_dim] of type io, written.
+ * In binary32, every step rounded to nearest even and none contracted:
+ *     a = x + bias;  r0 = a0*c - a1*s;  r1 = a0*s + a1*c
+ * then rounded to io (queries) or to the cache's type (keys, and the values, which are not
+ * rotated).  Q8_0 rows: per 32 elements d = f16(amax/127) (at most 65504), q = a/d rounded half
+ * to even and clamped to [-127, 127], 0 where d is 0 ("Execution Plan" C4 S2b, decision 4).
+ * The slots of one call are distinct.  A token with a position outside [0, max_pos) gets a zero
+ * q and stores nothing; a slot past the cache stores nothing; both are reported by
+ * mq_stream_status.  ld*sizeof(io) is a multiple of 16.  T = 0 does nothing. */
+mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope, mq_type io,
+                        const void *qkv, int64_t ld, const float *bias, const int32_t *pos,
+                        const int64_t *slot, void *q, int64_t T, int n_heads, mq_stream stream);
+
+/* mq_attn_decode: also add the attention weights to the cache's weight_sum. */
+#define MQ_ATTN_TRACK 1u
+
+/* mq_attn_workspace_bytes -- size of mq_attn_decode's workspace for up to S sequences of up to
+ * max_len cached tokens (0 for arguments mq_attn_decode would refuse).  Zero it once before its
+ * first call (a count in it must start at zero; every call leaves it so).  A workspace serves
+ * calls of any shape that fits, one at a time. */
+size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads, int64_t max_len,
+                               uint32_t flags);
+
+/* mq_attn_decode -- attention of one new token per sequence over its cached rows:
+ *     s_i = scale * sum_d q[d]*k_i[d],   w = softmax(s),   o[d] = sum_i w_i*v_i[d]
+ * over the positions i in [max(0, len - window), len) (window 0: all of them), for every query
+ * head; query head a reads kv head a / (n_heads / n_kv_heads).  A sequence of length 0 gives
+ * o = 0.  Sums, softmax statistics and accumulators are binary32; f16 and Q8_0 keys meet the
+ * query as two f16 parts (22 bits), bf16 keys as three bf16 parts (24 bits), and the weights
+ * likewise.
+ *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned
+ *   len     device int32 [S], the rows to read, the new token's own among them; <= max_len
+ *   max_len bound of the lengths on the host, <= pages_ld*page_size: it sizes the workspace
+ *           and the launch, not the work
+ *   flags   MQ_ATTN_TRACK: weight_sum of each row read += its w summed over the kv head's
+ *           query heads (two sequences of one call must then share no page)
+ *   ws      device workspace of ws_bytes >= mq_attn_workspace_bytes, 256-byte aligned
+ * Several new tokens of one sequence (speculative verification) are several sequences with the
+ * same pages and their own lengths.  Results do not depend on the order in which thread blocks
+ * run.  A length outside [0, max_len] is clamped, a page outside the cache is left out; both
+ * are reported by mq_stream_status.  S = 0 does nothing. */
+mq_status mq_attn_decode(const mq_kv_cache *cache, mq_type io, const void *q, void *o,
+                         const int32_t *pages, int64_t pages_ld, const int32_t *len, int64_t S,
+                         int n_heads, int64_t max_len, float scale, int64_t window,
+                         uint32_t flags, void *ws, size_t ws_bytes, mq_stream stream);
+
+/* mq_kv_evict -- bring each sequence down to at most `keep` rows per kv head.  With n = len[s]
+ * <= keep all rows stay.  Otherwise positions [0, sink), [n - recent, n) and, of those between,
+ * the keep - sink - recent with the largest weight_sum stay (equal sums: the lower position; a
+ * NaN counts as larger than every number; -0 equals 0).  Each kv head chooses for itself.  The
+ * rows that stay are copied in ascending order of position (keys, values, scales, weight sums)
+ * to positions 0, 1, ... of new_pages; the old pages are only read.  No page of new_pages may
+ * appear in pages or twice.
+ *   kept     device int32 [S][n_kv_heads][keep]: the positions that stayed, then -1; written
+ *   new_len  device int32 [S]: min(n, keep); written
+ *   sink, recent >= 0, sink + recent <= keep, 1 <= keep <= new_pages_ld*page_size
+ *   max_len  bound of the lengths, <= pages_ld*page_size
+ * A length outside [0, max_len] is clamped; a row whose old or new page lies outside the cache is
+ * not copied; both are reported by mq_stream_status.  S = 0 does nothing. */
+mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages, int64_t pages_ld,
+                      const int32_t *len, int64_t S, int64_t max_len, const int32_t *new_pages,
+                      int64_t new_pages_ld, int64_t keep, int64_t sink, int64_t recent,
+                      int32_t *kept, int32_t *new_len, mq_stream stream);
+
 /* mq_stream_status -- synchronise `stream`, then read and clear the current
- * device's status word written by bounded device-side waits.  Returns MQ_OK,
- * or MQ_ERR_TIMEOUT if a wait expired since the last call (the message names
- * the kernel), or MQ_ERR_CUDA if the synchronisation failed. */
+ * device's status words.  Returns MQ_OK, or MQ_ERR_TIMEOUT if a bounded
+ * device-side wait expired since the last call (the message names the
+ * kernel), or MQ_ERR_INDEX if a kernel left out a position, slot, page or
+ * length outside its range (the message says which; a timeout is reported
+ * first, and an index error then by the next call), or MQ_ERR_CUDA if the
+ * synchronisation failed. */
 mq_status mq_stream_status(mq_stream stream);
 
 /* mq_last_error -- message of the last failing call on this thread: the call,
