@@ -70,10 +70,10 @@ __device__ __forceinline__ int clamped_len(int len, int max_len) {
 }
 
 // The row of (head, position), or -1 where its page lies outside the cache.
-__device__ __forceinline__ int64_t kv_row(const KvView &c, const int32_t *__restrict__ pages,
+__device__ __forceinline__ int64_t kv_row(const KvView &c, const int32_t *pages,
                                           int head, int pos) {
   const uint32_t pi = quotient((uint32_t)pos, c.page);
-  const int64_t page = __ldg(pages + pi);
+  const int64_t page = pages[pi];
   if (page < 0 || page >= c.n_pages) return -1;
   return page * c.page_stride + head * c.head_stride +
          int64_t((uint32_t)pos - pi * c.page.d) * c.slot_stride;

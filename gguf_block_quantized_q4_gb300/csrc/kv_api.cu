@@ -47,6 +47,9 @@ mq_status check_cache(const char *site, const mq_kv_cache *c) {
                   site, a.name, (long long)a.stride, (long long)extent);
     extent = a.stride * (a.n - 1) + extent;
   }
+  if (extent > int64_t(0xfffffffe))  // the kernels keep row indexes in 32 bits
+    return fail(MQ_ERR_SHAPE, "%s: the strides span %lld rows; at most 2^32 - 2 are supported", site,
+                (long long)extent);
   return MQ_OK;
 }
 
