@@ -8,20 +8,25 @@
 //
 // What bounds it: the bytes of K and V, each read once.  A group of query heads shares them, so
 // both products are matrix products with 8 (or 16) columns: S^T = K Q^T and O^T = V^T P^T on
-// mma.sync m16n8k16, the rows of K (keys) and of V^T (dims) as the 16-row operand, the query
-// rows as the 8 columns.  (A tcgen05 tile has 64 or 128 rows and its operands in shared memory;
-// eight columns leave it idle, and the products take a fifth of the tensor time here anyway.)
-// Because a key is used by one warp only, K and V go from global memory straight into the
-// operand registers: the order of the dims in a product is free, so a lane's 16 bytes of a key
-// row are its operand words, and V's pairs of keys are put together by byte permutes.  No
-// shared memory, no alignment of pages to tiles, and a row past the end is simply not loaded.
+// mma.sync m16n8k16, keys (and dims of V^T) as the 16-row operand, the query rows as the 8
+// columns.  (A tcgen05 tile has 64 or 128 rows and at least 8 columns of its own accumulator
+// memory; here the softmax between the products lives in registers and the products take a
+// fifth of the time that the bytes need.)
+//
+// Loads: one thread block per SM.  Each warp takes 16 or 32 keys at a time and has a ring of its
+// own in shared memory, filled row by row with 16-byte asynchronous copies that follow the page
+// table (a page may end anywhere; a row past the end is filled with zeros, nothing is read for
+// it), so no barrier stands between the loads and the products and about 128 KB are in flight
+// per SM; 44 KB cover the memory's latency.  ldmatrix, transposing for V, reads the operands;
+// rows are padded by 16 bytes, which puts the eight rows of a matrix on different banks.
 //
 // Work: (sequence, kv head, row group) units of tiles of TK keys, laid end to end; thread block b
 // of the `parts` that have work takes the tiles [b T / parts, (b + 1) T / parts) of all T.  The
 // split is made on the device from the lengths, so unlike lengths load all SMs alike.  A unit
 // whole in one block is written at once; the pieces of the others go to the workspace, and the
-// last block of a unit to arrive joins them in the order of the blocks (a counter per unit's
-// first block, back to zero afterwards), so results do not depend on the order of execution.
+// last block of a unit to arrive joins them in a fixed order (a counter per unit's first block,
+// back to zero afterwards), so results do not depend on the order of execution.  The rings run
+// on across pieces.
 //
 // Precision: f16 operands are multiplied exactly and summed in binary32.  q (scaled by a power
 // of two per row) and the weights are carried as two f16 parts (22 bits), against bf16 keys and
@@ -35,29 +40,35 @@
 namespace mq {
 namespace {
 
-constexpr int kWarps = 4;           // per thread block
 constexpr int kMaxParts = 1024;     // thread blocks with work (counters in the workspace)
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // ---- device helpers ---------------------------------------------------------------------
-__device__ __forceinline__ uint4 load16(const uint8_t *p, bool on) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (on)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// 16 bytes to shared memory; zeros, and no read, where !on.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
 }
-__device__ __forceinline__ uint2 load8(const uint8_t *p, bool on) {
-  uint2 v = make_uint2(0, 0);
-  if (on)
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t load4(const uint8_t *p, bool on) {
-  uint32_t v = 0;
-  if (on) asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the N newest groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements; lane 8 i + r gives the address of row r of matrix i.
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
 }
 template <bool BF>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -142,6 +153,8 @@ __device__ __forceinline__ void store_io4(void *p, int io, int64_t i, float4 v) 
 }
 
 // ---- the shape of a kernel ----------------------------------------------------------------
+constexpr int kSmemMax = 227 * 1024;  // per thread block
+
 template <int TYPE, int D, int NT>
 struct Shape {
   static constexpr bool kQ8 = TYPE == MQ_Q8_0;
@@ -150,21 +163,27 @@ struct Shape {
   static constexpr int kPartsK = kBfK ? 3 : 2, kPartsV = kBfV ? 3 : 2;
   static constexpr int kRow = kQ8 ? D : 2 * D;  // bytes of a key row
   static constexpr int kNG = D / 32;            // groups of 32 dims
-  // 16-key groups a warp takes at a time: about 4 KB of K (and of V) in flight per warp
-  static constexpr int kMT = kRow * 16 >= 3072 ? 1 : 2;
-  static constexpr int kKeys = 16 * kMT, kTK = kKeys * kWarps;
+  static constexpr int kMT = kRow <= 128 ? 2 : 1;  // 16-key groups a warp takes at a time
+  static constexpr int kKeys = 16 * kMT;
   static constexpr int kRows = 8 * NT;          // query rows of a unit
-  static constexpr int kKWords = kQ8 ? 2 : 4;   // a lane's words of a key row, per group
-  static constexpr int kVWords = kQ8 ? 1 : 2;
+  // shared memory: the rings, Q8_0 scales of a ring's keys, query parts, the warps' results
+  static constexpr int kStride = kRow + 16;     // an odd number of 16-byte steps
+  static constexpr int kStage = 2 * kKeys * kStride;
+  static constexpr int kScales = kQ8 ? 2 * kKeys * kNG * 4 : 0;  // per stage, binary32
+  static constexpr int kLdO = D + 4;
+  static constexpr int kQuery = kPartsK * NT * kNG * 32 * 16;
+  static constexpr int smem(int warps, int stages) {
+    return warps * (stages * (kStage + kScales) + kRows * (kLdO + 2) * 4) + kQuery + kRows * 4 + 16;
+  }
+  static constexpr int kWarps = smem(8, 2) <= kSmemMax ? 8 : smem(6, 2) <= kSmemMax ? 6 : 4;
+  static constexpr int kStages = smem(kWarps, 3) <= kSmemMax ? 3 : 2;
+  static constexpr int kSmem = smem(kWarps, kStages), kThreads = 32 * kWarps;
+  static constexpr int kTK = kKeys * kWarps;    // keys of a tile
+  static_assert(smem(kWarps, kStages) <= kSmemMax, "shared memory");
   // exp2 of a weight's exponent in the f16 parts: weights in (0, 2^15], so that the second part
   // of all but negligible weights is a normal f16
   static constexpr float kBias = kBfV ? 0.f : 15.f;
 };
-// thread blocks per SM that the registers are sized for
-template <int TYPE, int D, int NT>
-constexpr int blocks_per_sm() {
-  return D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2;
-}
 
 struct Params {
   AttnArgs a;
@@ -227,16 +246,43 @@ __device__ __forceinline__ void next_tile(Cursor &c, const AttnArgs &a, int unit
   } while (c.span.tiles == 0);
 }
 
+// Joins the results that the warps left in shared memory: so[w][row][dim], sm / sl the maxima and
+// sums.  Calls put(row, dim, o, m, l) with four dims of o (not normalised) for the first `rows`.
+template <class C, class Put>
+__device__ __forceinline__ void join_warps(const float *so, const float *sm, const float *sl, int D,
+                                           int rows, Put put) {
+  for (int i = threadIdx.x; i < rows * (D / 4); i += C::kThreads) {
+    const int r = i / (D / 4), d = 4 * (i % (D / 4));
+    float m = sm[r], l = 0.f;
+#pragma unroll
+    for (int w = 1; w < C::kWarps; ++w) m = fmaxf(m, sm[w * C::kRows + r]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      const float f = exp2_fast(sm[w * C::kRows + r] - base);
+      const float4 y = *reinterpret_cast<const float4 *>(so + (w * C::kRows + r) * C::kLdO + d);
+      l = fmaf(sl[w * C::kRows + r], f, l);
+      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y);
+      x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+    }
+    put(r, d, x, m, l);
+  }
+}
+
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<TYPE, D, NT>())
+__global__ void __launch_bounds__(Shape<TYPE, D, NT>::kThreads, 1)
 attn_decode_kernel(const __grid_constant__ Params p) {
   using C = Shape<TYPE, D, NT>;
-  constexpr int NG = C::kNG, MT = C::kMT, LDO = D + 4;
-  __shared__ uint4 sq[C::kPartsK][NT][NG][32];          // query parts as operand words
-  __shared__ float sfac[C::kRows];                      // per row: scale * log2 e * 2^-e
-  __shared__ float sm[kWarps][C::kRows], sl[kWarps][C::kRows];
-  __shared__ __align__(16) float so[kWarps][C::kRows][LDO];
-  __shared__ int slast;
+  constexpr int NG = C::kNG, MT = C::kMT, KS = D / 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t *const ring = smem;                                               // [warp][stage][K, V]
+  float *const scales = reinterpret_cast<float *>(ring + C::kWarps * C::kStages * C::kStage);
+  uint4 *const sq = reinterpret_cast<uint4 *>(scales + C::kWarps * C::kStages * (C::kScales / 4));
+  float *const so = reinterpret_cast<float *>(sq) + C::kQuery / 4;          // [warp][row][kLdO]
+  float *const sm = so + C::kWarps * C::kRows * C::kLdO, *const sl = sm + C::kWarps * C::kRows;
+  float *const sfac = sl + C::kWarps * C::kRows;  // per row: scale * log2 e * 2^-e
+  int *const slast = reinterpret_cast<int *>(sfac + C::kRows);
   const AttnArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   grid_dependency();
@@ -246,7 +292,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     const int raw = a.len[s];
     if (raw != clamped_len(raw, a.max_len) && tid == 0) index_error(a.status, kIdxAttnLen, raw);
     if (raw <= 0)
-      for (int i = tid; i < a.hq * (D / 4); i += kWarps * 32)
+      for (int i = tid; i < a.hq * (D / 4); i += C::kThreads)
         store_io4(a.o, a.io, int64_t(s) * a.hq * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   }
 
@@ -276,7 +322,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     cur.left = end - at;
   }
 
-  // Rows of a tile's keys: lane i holds key i's.  Its page entry is read one tile ahead.
+  // ---- the ring ----
+  // Rows of a tile's keys: lane i holds key i's.  The page entry is read one tile ahead.
   int32_t page = -1;
   uint32_t slot = 0;
   int page_unit = 0;
@@ -294,90 +341,77 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       }
     }
   };
-  auto row_of_lane = [&]() -> uint32_t {
-    if (page < 0) return kNoRow;
-    return (uint32_t)(page * a.c.page_stride + (page_unit / p.row_groups) * a.c.head_stride +
-                      slot * a.c.slot_stride);
+  const uint32_t ring0 = smem_addr(ring) + warp * C::kStages * C::kStage;
+  float *const scale0 = scales + warp * C::kStages * (C::kScales / 4);
+  uint32_t valid_bits[C::kStages] = {};  // per tile in flight (oldest first): keys that are there
+  // Q8_0 scales of the newest tile, on their way: lane i has key i % 16 (+ 16), of K or V
+  uint16_t pend[MT][NG];
+  int pend_stage = -1;
+  auto store_scales = [&]() {
+    if (!C::kQ8 || pend_stage < 0) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+        scale0[pend_stage * (C::kScales / 4) + ((lane >> 4) * C::kKeys + 16 * m + (lane & 15)) * NG + j] =
+            __half2float(__ushort_as_half(pend[m][j]));
   };
-
-  uint32_t kr[MT][2][NG][C::kKWords], vr[MT][4][NG][C::kVWords];  // K, V in flight
-  uint32_t kscale[MT][2][(NG + 1) / 2], vscale[MT][4][(NG + 1) / 2];  // Q8_0 scales, two a word
-  uint32_t row = kNoRow;                                            // lane i: key i's row
-  uint32_t valid = 0;                                               // bit i: key i is there
-  auto load_scales = [&](const __half *plane, uint32_t r, bool on, uint32_t (&w)[(NG + 1) / 2]) {
-    const uint8_t *q = reinterpret_cast<const uint8_t *>(plane) + size_t(r) * (NG * 2);
-    if (NG == 8) {
-      const uint4 v = load16(q, on);
-      w[0] = v.x, w[1 % ((NG + 1) / 2)] = v.y, w[2 % ((NG + 1) / 2)] = v.z, w[3 % ((NG + 1) / 2)] = v.w;
-    } else if (NG == 4) {
-      const uint2 v = load8(q, on);
-      w[0] = v.x, w[1 % ((NG + 1) / 2)] = v.y;
-    } else if (NG % 2 == 0) {
+  auto issue = [&](int stage) {  // the tile looked up last, into a stage; then the next look-up
+    const uint32_t row =
+        page < 0 ? kNoRow
+                 : (uint32_t)(page * a.c.page_stride +
+                              (page_unit / p.row_groups) * a.c.head_stride + slot * a.c.slot_stride);
 #pragma unroll
-      for (int i = 0; i < NG / 2; ++i) w[i] = load4(q + 4 * i, on);
-    } else {  // rows of an odd number of scales are 2-byte aligned
+    for (int i = 0; i + 1 < C::kStages; ++i) valid_bits[i] = valid_bits[i + 1];
+    valid_bits[C::kStages - 1] = __ballot_sync(0xffffffffu, row != kNoRow);
+    constexpr int CH = C::kRow / 16;  // 16-byte chunks of a row
+    const uint32_t dst = ring0 + stage * C::kStage;
 #pragma unroll
-      for (int i = 0; i < (NG + 1) / 2; ++i) {
-        uint16_t x = 0, y = 0;
-        if (on) {
-          x = *reinterpret_cast<const uint16_t *>(q + 4 * i);
-          if (2 * i + 1 < NG) y = *reinterpret_cast<const uint16_t *>(q + 4 * i + 2);
-        }
-        w[i] = x | uint32_t(y) << 16;
-      }
+    for (int i = 0; i < C::kKeys * CH / 32; ++i) {
+      const int key = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+      const uint32_t r = __shfl_sync(0xffffffffu, row, key);
+      const bool on = r != kNoRow;
+      const size_t off = on ? size_t(r) * C::kRow + ch * 16 : 0;
+      copy16(dst + key * C::kStride + ch * 16, a.c.k + off, on);
+      copy16(dst + (C::kKeys + key) * C::kStride + ch * 16, a.c.v + off, on);
     }
-  };
-  auto load_k = [&]() {
+    copies_commit();
+    if (C::kQ8) {
+      store_scales();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * m + (lane & 15));
+        const __half *q = (lane < 16 ? a.c.ks : a.c.vs) + size_t(r == kNoRow ? 0 : r) * NG;
+        if constexpr (NG % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * m + 8 * i + g);
-        const bool on = r != kNoRow;
-        const uint8_t *q = a.c.k + size_t(r) * C::kRow + t * (C::kKWords * 4);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          if (C::kQ8) {
-            const uint2 v = load8(q + 32 * j, on);
-            kr[m][i][j][0] = v.x, kr[m][i][j][1] = v.y;
-          } else {
-            const uint4 v = load16(q + 64 * j, on);
-            kr[m][i][j][0] = v.x, kr[m][i][j][1] = v.y;
-            kr[m][i][j][2 % C::kKWords] = v.z, kr[m][i][j][3 % C::kKWords] = v.w;
+          for (int j = 0; j < NG; j += 4) {
+            uint2 v = make_uint2(0, 0);
+            if (r != kNoRow) v = *reinterpret_cast<const uint2 *>(q + j);
+            pend[m][j] = v.x, pend[m][j + 1] = v.x >> 16;
+            pend[m][j + 2] = v.y, pend[m][j + 3] = v.y >> 16;
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NG; ++j) pend[m][j] = r != kNoRow ? __half_as_ushort(q[j]) : 0;
         }
-        if (C::kQ8) load_scales(a.c.ks, r, on, kscale[m][i]);
       }
-  };
-  auto load_v = [&]() {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * m + 8 * (i >> 1) + 2 * t + (i & 1));
-        const bool on = r != kNoRow;
-        const uint8_t *q = a.c.v + size_t(r) * C::kRow + g * (C::kVWords * 4);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          if (C::kQ8) {
-            vr[m][i][j][0] = load4(q + 32 * j, on);
-          } else {
-            const uint2 v = load8(q + 64 * j, on);
-            vr[m][i][j][0] = v.x, vr[m][i][j][1 % C::kVWords] = v.y;
-          }
-        }
-        if (C::kQ8) load_scales(a.c.vs, r, on, vscale[m][i]);
-      }
+      pend_stage = stage;
+    }
+    next_tile(cur, a, p.units, C::kTK);
+    look_up();
   };
 
   Cursor now = cur;  // the tile being multiplied (its piece's unit)
   look_up();
-  row = row_of_lane();
-  valid = __ballot_sync(0xffffffffu, row != kNoRow);
-  load_k();
-  load_v();
-  next_tile(cur, a, p.units, C::kTK);
-  look_up();
+#pragma unroll
+  for (int i = 0; i < C::kStages; ++i) issue(i);
+  int stage = 0;
+
+  // operand addresses of this lane within a stage: matrix lane >> 3, row lane & 7
+  const uint32_t k_lane = ((lane & 7) + (lane & 8)) * C::kStride + (lane >> 4) * 16;
+  const uint32_t v_lane = (C::kKeys + (lane & 7) + (lane >> 4) * 8) * C::kStride + (lane >> 3 & 1) * 16;
+  // Q8_0: the two chunks of 16 dims side by side, keys 0-7 and 8-15 each
+  const uint32_t v_lane8 = (C::kKeys + (lane & 7) + (lane & 8)) * C::kStride + (lane >> 4) * 16;
 
   while (at < end) {
     // ---- one piece: tiles of one unit ----
@@ -389,16 +423,18 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     const int64_t head0 = int64_t(now.s) * a.hq + hk * p.group + rg * C::kRows;
     const int64_t unit_id = int64_t(now.s) * p.units + now.unit;
 
-    // the query's parts
-    for (int r = warp; r < C::kRows; r += kWarps) {
+    // the query's parts as operand words: lane 4 r + t' of (part, 8-row group, 32 dims) has the
+    // words of two 16-dim steps.  f16 and bf16 rows: dims 2t', 2t' + 1 and 8 more of a step;
+    // Q8_0 rows: dims 4t' .. 4t' + 3 (a chunk's four bytes)
+    for (int r = warp; r < C::kRows; r += C::kWarps) {
       float x[8];
-      float top = 0.f;
       const bool on = r < rows && lane < D / 8;
       const float4 u = on ? load_io4(a.q, a.io, (head0 + r) * D + lane * 8) : make_float4(0, 0, 0, 0);
       const float4 v = on ? load_io4(a.q, a.io, (head0 + r) * D + lane * 8 + 4) : make_float4(0, 0, 0, 0);
       x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
       int e = 0;
       if (!C::kBfK) {  // a power of two that puts the row's largest element in [2^14, 2^15)
+        float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -410,10 +446,19 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         uint32_t w[4][C::kPartsK];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split2<C::kBfK>(x[2 * i] * up, x[2 * i + 1] * up, w[i]);
+        // the lane's 8 dims are half `lane & 1` of step lane >> 1
+        uint32_t *q = reinterpret_cast<uint32_t *>(sq + ((r >> 3) * NG + (lane >> 2)) * 32 + (r & 7) * 4);
+        const int step = lane >> 1 & 1, half = lane & 1;
 #pragma unroll
         for (int k = 0; k < C::kPartsK; ++k)
-          sq[k][r >> 3][lane >> 2][(r & 7) * 4 + (lane & 3)] =
-              make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t *const to = q + k * NT * NG * 128;
+            if (C::kQ8)
+              to[(2 * half + (i >> 1)) * 4 + 2 * step + (i & 1)] = w[i][k];
+            else
+              to[i * 4 + 2 * step + half] = w[i][k];
+          }
       }
     }
     __syncthreads();
@@ -421,188 +466,185 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) fac[n][0] = sfac[8 * n + 2 * t], fac[n][1] = sfac[8 * n + 2 * t + 1];
 
-    float o[NG][2][NT][4] = {}, mx[NT][2], ls[NT][2] = {};
+    float o[KS][NT][4] = {}, mx[NT][2], ls[NT][2] = {};
 #pragma unroll
     for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
 
     for (int i = 0; i < count; ++i) {
-      const uint32_t here = valid;
-      const int key0 = now.span.lo + (now.tile + i) * C::kTK + warp * C::kKeys;
-      // ---- S^T = K Q^T ----
-      float s[MT][NT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float c0[4] = {}, c1[4] = {}, total[4] = {};
-#pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            uint32_t ka[4], kb[4];
-            if (C::kQ8) {
-              const uint32_t x0 = kr[m][0][j][0] ^ 0x80808080u, x1 = kr[m][0][j][1] ^ 0x80808080u;
-              const uint32_t y0 = kr[m][1][j][0] ^ 0x80808080u, y1 = kr[m][1][j][1] ^ 0x80808080u;
-              ka[0] = int8_f16<0x4140>(x0), ka[1] = int8_f16<0x4342>(x0);
-              ka[2] = int8_f16<0x4140>(x1), ka[3] = int8_f16<0x4342>(x1);
-              kb[0] = int8_f16<0x4140>(y0), kb[1] = int8_f16<0x4342>(y0);
-              kb[2] = int8_f16<0x4140>(y1), kb[3] = int8_f16<0x4342>(y1);
-            } else {
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                ka[w] = kr[m][0][j][w % C::kKWords], kb[w] = kr[m][1][j][w % C::kKWords];
-            }
-#pragma unroll
-            for (int k = 0; k < C::kPartsK; ++k) {
-              const uint4 b = sq[k][n][j][lane];
-              mma<C::kBfK>(k ? c1 : c0, ka[0], kb[0], ka[1], kb[1], b.x, b.y);
-              mma<C::kBfK>(k ? c1 : c0, ka[2], kb[2], ka[3], kb[3], b.z, b.w);
-            }
-            if (C::kQ8) {  // the block's scales: keys g (elements 0, 1) and g + 8 (2, 3)
-              const float2 d0 = unpack2<false>(kscale[m][0][j / 2]);
-              const float2 d1 = unpack2<false>(kscale[m][1][j / 2]);
-              const float da = j & 1 ? d0.y : d0.x, db = j & 1 ? d1.y : d1.x;
-              total[0] = fmaf(c0[0] + c1[0], da, total[0]);
-              total[1] = fmaf(c0[1] + c1[1], da, total[1]);
-              total[2] = fmaf(c0[2] + c1[2], db, total[2]);
-              total[3] = fmaf(c0[3] + c1[3], db, total[3]);
-#pragma unroll
-              for (int w = 0; w < 4; ++w) c0[w] = c1[w] = 0.f;
-            }
-          }
-#pragma unroll
-          for (int w = 0; w < 4; ++w) s[m][n][w] = C::kQ8 ? total[w] : c0[w] + c1[w];
-        }
-      // the next tile's rows; K's registers are free
-      const bool more = at + i + 1 < end;
-      if (more) {
-        row = row_of_lane();
-        valid = __ballot_sync(0xffffffffu, row != kNoRow);
-        load_k();
-      }
-      // ---- softmax ----
-      float al[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float top[2] = {mx[n][0], mx[n][1]};
+      copies_wait<C::kStages - 1>();
+      __syncwarp();
+      const uint32_t here = valid_bits[0];
+      const uint32_t base = ring0 + stage * C::kStage;
+      const float *const sc = scale0 + stage * (C::kScales / 4);
+      if (here) {
+        // ---- S^T = K Q^T ----
+        float s[MT][NT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const bool ga = here >> (16 * m + g) & 1, gb = here >> (16 * m + 8 + g) & 1;
-          s[m][n][0] = ga ? s[m][n][0] * fac[n][0] : -INFINITY;
-          s[m][n][1] = ga ? s[m][n][1] * fac[n][1] : -INFINITY;
-          s[m][n][2] = gb ? s[m][n][2] * fac[n][0] : -INFINITY;
-          s[m][n][3] = gb ? s[m][n][3] * fac[n][1] : -INFINITY;
-          top[0] = fmaxf(top[0], fmaxf(s[m][n][0], s[m][n][2]));
-          top[1] = fmaxf(top[1], fmaxf(s[m][n][1], s[m][n][3]));
-          if (p.logits && 8 * n + 2 * t < p.logit_width) {
-            float *q = p.logits + (unit_id * a.max_len + key0 + 16 * m + g) * p.logit_width + 8 * n + 2 * t;
-            const int ka = key0 + 16 * m + g;
-            if (ka < now.span.len) *reinterpret_cast<float2 *>(q) = make_float2(s[m][n][0], s[m][n][1]);
-            if (ka + 8 < now.span.len)
-              *reinterpret_cast<float2 *>(q + 8 * p.logit_width) = make_float2(s[m][n][2], s[m][n][3]);
+          float c0[NT][4] = {}, c1[NT][4] = {}, total[NT][4] = {};
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            uint32_t ka[2][4];  // two steps of 16 dims
+            if (C::kQ8) {
+              uint32_t x[4];  // keys g (0, 2) and g + 8 (1, 3), chunks 0 and 1
+              ldmatrix4<false>(x, base + k_lane + 16 * m * C::kStride + j * 32);
+#pragma unroll
+              for (int st = 0; st < 2; ++st) {
+                const uint32_t xa = x[2 * st] ^ 0x80808080u, xb = x[2 * st + 1] ^ 0x80808080u;
+                ka[st][0] = int8_f16<0x4140>(xa), ka[st][1] = int8_f16<0x4140>(xb);
+                ka[st][2] = int8_f16<0x4342>(xa), ka[st][3] = int8_f16<0x4342>(xb);
+              }
+            } else {
+              ldmatrix4<false>(ka[0], base + k_lane + 16 * m * C::kStride + j * 64);
+              ldmatrix4<false>(ka[1], base + k_lane + 16 * m * C::kStride + j * 64 + 32);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < C::kPartsK; ++k) {
+                const uint4 b = sq[((k * NT + n) * NG + j) * 32 + lane];
+                mma<C::kBfK>(k ? c1[n] : c0[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], b.x, b.y);
+                mma<C::kBfK>(k ? c1[n] : c0[n], ka[1][0], ka[1][1], ka[1][2], ka[1][3], b.z, b.w);
+              }
+            if (C::kQ8) {  // the block's scales: keys g (elements 0, 1) and g + 8 (2, 3)
+              const float da = sc[(16 * m + g) * NG + j], db = sc[(16 * m + g + 8) * NG + j];
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  total[n][w] = fmaf(c0[n][w] + c1[n][w], w < 2 ? da : db, total[n][w]);
+                  c0[n][w] = c1[n][w] = 0.f;
+                }
+            }
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) s[m][n][w] = C::kQ8 ? total[n][w] : c0[n][w] + c1[n][w];
         }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], 4));
-          top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], 8));
-          top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], 16));
-          const float base = top[w] == -INFINITY ? 0.f : top[w];  // no key yet: all weights 0
-          al[n][w] = exp2_fast(mx[n][w] - base);
-          mx[n][w] = top[w];
-          float sum = 0.f;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            s[m][n][w] = exp2_fast(s[m][n][w] - base + C::kBias);
-            s[m][n][w + 2] = exp2_fast(s[m][n][w + 2] - base + C::kBias);
-            sum += s[m][n][w] + s[m][n][w + 2];
-          }
-          ls[n][w] = fmaf(ls[n][w], al[n][w], sum);
-        }
-      }
-      // the weights transposed, as binary32 in two halves: lane (g, t) gets row g's weights of
-      // the keys 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
+        // ---- softmax ----
+        const int key0 = now.span.lo + (now.tile + i) * C::kTK + warp * C::kKeys;
+        float al[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int w = 0; w < 4; w += 2) {
-            const uint32_t x = __float_as_uint(s[m][n][w]), y = __float_as_uint(s[m][n][w + 1]);
-            const uint32_t hi = transpose8x8(__byte_perm(x, y, 0x7632));
-            const uint32_t lo = transpose8x8(__byte_perm(x, y, 0x5410));
-            s[m][n][w] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
-            s[m][n][w + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+          for (int m = 0; m < MT; ++m) {
+            const bool ga = here >> (16 * m + g) & 1, gb = here >> (16 * m + 8 + g) & 1;
+            s[m][n][0] = ga ? s[m][n][0] * fac[n][0] : -INFINITY;
+            s[m][n][1] = ga ? s[m][n][1] * fac[n][1] : -INFINITY;
+            s[m][n][2] = gb ? s[m][n][2] * fac[n][0] : -INFINITY;
+            s[m][n][3] = gb ? s[m][n][3] * fac[n][1] : -INFINITY;
           }
-      uint32_t pw[MT][NT][2][C::kPartsV];  // the weights' parts (for Q8_0: made per block)
-      if (!C::kQ8)
+        if (p.logits) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              if (8 * n + 2 * t < p.logit_width) {
+                const int ka = key0 + 16 * m + g;
+                float *q = p.logits + (unit_id * a.max_len + ka) * p.logit_width + 8 * n + 2 * t;
+                if (ka < now.span.len) *reinterpret_cast<float2 *>(q) = make_float2(s[m][n][0], s[m][n][1]);
+                if (ka + 8 < now.span.len)
+                  *reinterpret_cast<float2 *>(q + 8 * p.logit_width) = make_float2(s[m][n][2], s[m][n][3]);
+              }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float top = mx[n][w];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][w], s[m][n][w + 2]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float low = top == -INFINITY ? 0.f : top;  // no key yet: all weights 0
+            al[n][w] = exp2_fast(mx[n][w] - low);
+            mx[n][w] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              s[m][n][w] = exp2_fast(s[m][n][w] - low + C::kBias);
+              s[m][n][w + 2] = exp2_fast(s[m][n][w + 2] - low + C::kBias);
+              sum += s[m][n][w] + s[m][n][w + 2];
+            }
+            ls[n][w] = fmaf(ls[n][w], al[n][w], sum);
+          }
+        // the weights transposed: lane (g, t) gets row g's of the keys 2t, 2t + 1, 2t + 8, 2t + 9;
+        // their parts, or for Q8_0 (whose blocks' scales come first) as binary32 in two halves
+        uint32_t pw[MT][NT][2][C::kPartsV];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            split2<C::kBfV>(s[m][n][0], s[m][n][1], pw[m][n][0]);
-            split2<C::kBfV>(s[m][n][2], s[m][n][3], pw[m][n][1]);
-          }
-      // ---- O^T = O^T alpha + V^T P^T ----
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        float c[2][NT][4] = {};
+            for (int h = 0; h < 2; ++h) {
+              if (C::kQ8) {
+                const uint32_t x = __float_as_uint(s[m][n][2 * h]), y = __float_as_uint(s[m][n][2 * h + 1]);
+                const uint32_t hi = transpose8x8(__byte_perm(x, y, 0x7632));
+                const uint32_t lo = transpose8x8(__byte_perm(x, y, 0x5410));
+                s[m][n][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+                s[m][n][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+              } else {
+                split2<C::kBfV>(s[m][n][2 * h], s[m][n][2 * h + 1], pw[m][n][h]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t va[2][4];  // [16 dims][operand word]
-          if (C::kQ8) {
-#pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2) {  // keys 2t, 2t + 1; then 2t + 8, 2t + 9
-              const uint32_t x = vr[m][2 * i2][j][0], y = vr[m][2 * i2 + 1][j][0];
-              const uint32_t d01 = __byte_perm(x, y, 0x5140), d23 = __byte_perm(x, y, 0x7362);
-              va[0][2 * i2] = int8_bf16(__byte_perm(d01, 0x43434343u, 0x4140));
-              va[0][2 * i2 + 1] = int8_bf16(__byte_perm(d01, 0x43434343u, 0x4342));
-              va[1][2 * i2] = int8_bf16(__byte_perm(d23, 0x43434343u, 0x4140));
-              va[1][2 * i2 + 1] = int8_bf16(__byte_perm(d23, 0x43434343u, 0x4342));
+                for (int k = 0; k < C::kPartsV; ++k) pw[m][n][h][k] = transpose8x8(pw[m][n][h][k]);
+              }
             }
-            float dv[4];  // the four keys' scales of this block
+        // ---- O^T = O^T alpha + V^T P^T ----
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 d = unpack2<false>(vscale[m][k][j / 2]);
-              dv[k] = j & 1 ? d.y : d.x;
-            }
+        for (int j = 0; j < NG; ++j) {
+          float c[2][NT][4] = {};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              split2<C::kBfV>(s[m][n][0] * dv[0], s[m][n][1] * dv[1], pw[m][n][0]);
-              split2<C::kBfV>(s[m][n][2] * dv[2], s[m][n][3] * dv[3], pw[m][n][1]);
+          for (int m = 0; m < MT; ++m) {
+            uint32_t va[2][4];  // [16 dims][operand word]
+            if (C::kQ8) {
+              uint32_t x[4];  // dims 2g, 2g + 1 of the keys 2t, 2t + 1: chunk 0, 1 of keys 0-7, 8-15
+              ldmatrix4<true>(x, base + v_lane8 + 16 * m * C::kStride + j * 32);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  va[h][2 * q] = int8_bf16(__byte_perm(x[2 * h + q], 0x43434343u, 0x4240));
+                  va[h][2 * q + 1] = int8_bf16(__byte_perm(x[2 * h + q], 0x43434343u, 0x4341));
+                }
+              float dv[4];  // the scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                dv[q] = sc[(C::kKeys + 16 * m + 8 * (q >> 1) + 2 * t + (q & 1)) * NG + j];
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                split2<C::kBfV>(s[m][n][0] * dv[0], s[m][n][1] * dv[1], pw[m][n][0]);
+                split2<C::kBfV>(s[m][n][2] * dv[2], s[m][n][3] * dv[3], pw[m][n][1]);
+              }
+            } else {
+              ldmatrix4<true>(va[0], base + v_lane + 16 * m * C::kStride + j * 64);
+              ldmatrix4<true>(va[1], base + v_lane + 16 * m * C::kStride + j * 64 + 32);
             }
-          } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                const uint32_t x = vr[m][2 * i2][j][h % C::kVWords], y = vr[m][2 * i2 + 1][j][h % C::kVWords];
-                va[h][2 * i2] = __byte_perm(x, y, 0x5410);
-                va[h][2 * i2 + 1] = __byte_perm(x, y, 0x7632);
-              }
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < C::kPartsV; ++k)
+                  mma<C::kBfV>(c[h][n], va[h][0], va[h][1], va[h][2], va[h][3], pw[m][n][0][k],
+                               pw[m][n][1][k]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int k = 0; k < C::kPartsV; ++k)
-                mma<C::kBfV>(c[h][n], va[h][0], va[h][1], va[h][2], va[h][3], pw[m][n][0][k],
-                             pw[m][n][1][k]);
+              for (int w = 0; w < 4; ++w)
+                o[2 * j + h][n][w] = fmaf(o[2 * j + h][n][w], al[n][w & 1], c[h][n][w]);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) o[j][h][n][w] = fmaf(o[j][h][n][w], al[n][w & 1], c[h][n][w]);
       }
-      if (more) {
-        load_v();
-        next_tile(cur, a, p.units, C::kTK);
-        look_up();
-      }
+      __syncwarp();  // the stage has been read
+      issue(stage);
+      if (++stage == C::kStages) stage = 0;
     }
 
-    // ---- the warps' parts of the piece joined ----
+    // ---- the piece's result ----
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -611,42 +653,34 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int r = 8 * n + 2 * t + w;
-        if (g == 0) sm[warp][r] = mx[n][w], sl[warp][r] = l;
+        const int r = warp * C::kRows + 8 * n + 2 * t + w;
+        if (g == 0) sm[r] = mx[n][w], sl[r] = l;
 #pragma unroll
-        for (int j = 0; j < NG; ++j)
-          *reinterpret_cast<float4 *>(&so[warp][r][32 * j + 4 * g]) =
-              make_float4(o[j][0][n][w], o[j][0][n][w + 2], o[j][1][n][w], o[j][1][n][w + 2]);
+        for (int j = 0; j < KS; ++j)
+          if (C::kQ8) {  // dims 16 j + 2g, 2g + 1
+            *reinterpret_cast<float2 *>(so + r * C::kLdO + 16 * j + 2 * g) =
+                make_float2(o[j][n][w], o[j][n][w + 2]);
+          } else {
+            so[r * C::kLdO + 16 * j + g] = o[j][n][w];
+            so[r * C::kLdO + 16 * j + 8 + g] = o[j][n][w + 2];
+          }
       }
     __syncthreads();
-    const bool whole = now.tile == 0 && count == tiles;
-    const int64_t slot_id = me * 2 + (now.tile == 0);
-    for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
-      const int r = i / (D / 4), d = 4 * (i % (D / 4));
-      float m = sm[0][r], l = 0.f;
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm[w][r]);
-      const float base = m == -INFINITY ? 0.f : m;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(sm[w][r] - base);
-        const float4 y = *reinterpret_cast<const float4 *>(&so[w][r][d]);
-        l = fmaf(sl[w][r], f, l);
-        x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-      }
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        store_io4(a.o, a.io, (head0 + r) * D + d,
-                  make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-        if (d == 0 && p.stats) p.stats[unit_id * C::kRows + r] = make_float2(base - C::kBias, inv);
-      } else {
-        *reinterpret_cast<float4 *>(p.piece_o + (slot_id * C::kRows + r) * D + d) = x;
+    auto finish = [&](int r, int d, float4 x, float m, float l) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      store_io4(a.o, a.io, (head0 + r) * D + d,
+                make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+      if (d == 0 && p.stats) p.stats[unit_id * C::kRows + r] = make_float2((m == -INFINITY ? 0.f : m) - C::kBias, inv);
+    };
+    if (now.tile == 0 && count == tiles) {
+      join_warps<C>(so, sm, sl, D, rows, finish);
+    } else {
+      const int64_t mine = me * 2 + (now.tile == 0);  // a block leaves at most two pieces
+      join_warps<C>(so, sm, sl, D, rows, [&](int r, int d, float4 x, float m, float l) {
+        *reinterpret_cast<float4 *>(p.piece_o + (mine * C::kRows + r) * D + d) = x;
         if (d == 0)
-          *reinterpret_cast<float2 *>(p.piece_ml + (slot_id * C::kRows + r) * 2) = make_float2(m, l);
-      }
-    }
-    if (!whole) {
+          *reinterpret_cast<float2 *>(p.piece_ml + (mine * C::kRows + r) * 2) = make_float2(m, l);
+      });
       // blocks of the unit's first and last tile: block b has the tiles from T b / parts on
       const int64_t b0 = ((unit_first + 1) * parts - 1) / T;
       const int64_t b1 = ((unit_first + tiles) * parts - 1) / T;
@@ -654,37 +688,49 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       __syncthreads();
       if (tid == 0) {
         const int before = atomicAdd(p.count + b0, 1);
-        slast = before == (int)(b1 - b0);
-        if (slast) p.count[b0] = 0;
+        *slast = before == (int)(b1 - b0);
+        if (*slast) p.count[b0] = 0;
       }
       __syncthreads();
-      if (slast) {
+      if (*slast) {  // warp w joins the pieces w, w + kWarps, ...; then the warps' results
         __threadfence();
-        for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
-          const int r = i / (D / 4), d = 4 * (i % (D / 4));
-          float m = -INFINITY, l = 0.f;
-          auto ml = [&](int64_t b) {
-            return __ldcg(reinterpret_cast<const float2 *>(
-                p.piece_ml + ((b * 2 + (b == b0)) * C::kRows + r) * 2));
-          };
-#pragma unroll 4
-          for (int64_t b = b0; b <= b1; ++b) m = fmaxf(m, ml(b).x);
-          const float base = m == -INFINITY ? 0.f : m;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int64_t b = b0; b <= b1; ++b) {
-            const float2 v = ml(b);
-            const float f = exp2_fast(v.x - base);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(
-                p.piece_o + ((b * 2 + (b == b0)) * C::kRows + r) * D + d));
-            l = fmaf(v.y, f, l);
-            x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+        constexpr int Q = C::kRows * D / 128;  // a lane's groups of four dims
+        float4 x[Q];
+        float m[Q], l[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f), m[q] = -INFINITY, l[q] = 0.f;
+        for (int64_t b = b0 + warp; b <= b1; b += C::kWarps) {
+          const int64_t from = (b * 2 + (b == b0)) * C::kRows;
+          float4 y[Q];
+          float2 ml[Q];
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const int it = 32 * q + lane;
+            const bool on = it / (D / 4) < rows;
+            y[q] = make_float4(0.f, 0.f, 0.f, 0.f), ml[q] = make_float2(-INFINITY, 0.f);
+            if (on) {
+              y[q] = __ldcg(reinterpret_cast<const float4 *>(p.piece_o + from * D) + it);
+              ml[q] = __ldcg(reinterpret_cast<const float2 *>(p.piece_ml) + from + it / (D / 4));
+            }
           }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          store_io4(a.o, a.io, (head0 + r) * D + d,
-                    make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-          if (d == 0 && p.stats) p.stats[unit_id * C::kRows + r] = make_float2(base - C::kBias, inv);
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const float top = fmaxf(m[q], ml[q].x), low = top == -INFINITY ? 0.f : top;
+            const float f = exp2_fast(m[q] - low), h = exp2_fast(ml[q].x - low);
+            m[q] = top;
+            l[q] = l[q] * f + ml[q].y * h;
+            x[q].x = x[q].x * f + y[q].x * h, x[q].y = x[q].y * f + y[q].y * h;
+            x[q].z = x[q].z * f + y[q].z * h, x[q].w = x[q].w * f + y[q].w * h;
+          }
         }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int it = 32 * q + lane, r = warp * C::kRows + it / (D / 4), d = 4 * (it % (D / 4));
+          *reinterpret_cast<float4 *>(so + r * C::kLdO + d) = x[q];
+          if (d == 0) sm[r] = m[q], sl[r] = l[q];
+        }
+        __syncthreads();
+        join_warps<C>(so, sm, sl, D, rows, finish);
       }
     }
     // the next piece
@@ -725,17 +771,13 @@ __global__ void __launch_bounds__(256) attn_track_kernel(const __grid_constant__
 // them and the accumulators (D/8 registers per 8 columns) leave room for K and V in flight.
 int rows_of(int group, int dim) { return group > 8 && dim <= 128 ? 16 : 8; }
 
-int grid_of(int dim, int rows, const DeviceState *st) {
-  const int per_sm = dim * (rows / 8) <= 64 ? 4 : dim * (rows / 8) <= 128 ? 3 : 2;
-  return std::min(st->sms * per_sm, kMaxParts);
-}
 struct Workspace {
   size_t piece_o, piece_ml, stats, logits, total;
   int logit_width;
 };
 Workspace workspace_of(int64_t S, int hq, int hkv, int dim, int64_t max_len, bool track,
                        const DeviceState *st) {
-  const int group = hq / hkv, rows = rows_of(group, dim), grid = grid_of(dim, rows, st);
+  const int group = hq / hkv, rows = rows_of(group, dim), grid = std::min(st->sms, kMaxParts);
   const size_t units = size_t(hkv) * ((group + rows - 1) / rows);
   Workspace w;
   w.logit_width = std::min(rows, (group + 1) & ~1);
@@ -748,13 +790,38 @@ Workspace workspace_of(int64_t S, int hq, int hkv, int dim, int64_t max_len, boo
 }
 
 template <int TYPE, int D, int NT>
-mq_status launch_shape(Params p, cudaStream_t s, const DeviceState *st) {
+mq_status launch_shape(const Params &p, cudaStream_t s, const DeviceState *st) {
   using C = Shape<TYPE, D, NT>;
-  static_assert(blocks_per_sm<TYPE, D, NT>() * 152 <= kMaxParts, "counters");
   const int64_t tiles = (p.a.max_len + C::kTK - 1) / C::kTK * p.a.S * p.units;
-  const int64_t grid = std::min<int64_t>(grid_of(D, C::kRows, st), tiles);
+  const int64_t grid = std::min<int64_t>(std::min(st->sms, kMaxParts), tiles);
   return launch_dependent("attn_decode_kernel", attn_decode_kernel<TYPE, D, NT>,
-                          dim3((unsigned)grid, 1, 1), dim3(kWarps * 32, 1, 1), 0, s, p);
+                          dim3((unsigned)grid, 1, 1), dim3(C::kThreads, 1, 1), C::kSmem, s, p);
+}
+template <int TYPE, int D, int NT>
+mq_status opt_in_shape(const DeviceState *st) {
+  using C = Shape<TYPE, D, NT>;
+  if (C::kSmem > st->smem_optin)
+    return fail(MQ_ERR_LAUNCH, "attn_decode_kernel needs %d bytes of shared memory, the device allows %d",
+                C::kSmem, st->smem_optin);
+  const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<TYPE, D, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  return e == cudaSuccess ? MQ_OK : cuda_fail(e, "cudaFuncSetAttribute", "attn_decode_kernel");
+}
+template <int TYPE, int D>
+mq_status opt_in_rows(const DeviceState *st) {
+  mq_status r = opt_in_shape<TYPE, D, 1>(st);
+  if constexpr (D <= 128)
+    if (r == MQ_OK) r = opt_in_shape<TYPE, D, 2>(st);
+  return r;
+}
+template <int TYPE>
+mq_status opt_in(const DeviceState *st) {
+  mq_status r = opt_in_rows<TYPE, 64>(st);
+  if (r == MQ_OK) r = opt_in_rows<TYPE, 96>(st);
+  if (r == MQ_OK) r = opt_in_rows<TYPE, 128>(st);
+  if (r == MQ_OK) r = opt_in_rows<TYPE, 192>(st);
+  if (r == MQ_OK) r = opt_in_rows<TYPE, 256>(st);
+  return r;
 }
 template <int TYPE, int D>
 mq_status launch_rows(const Params &p, int rows, cudaStream_t s, const DeviceState *st) {
@@ -774,6 +841,13 @@ mq_status launch_dim(const Params &p, int rows, cudaStream_t s, const DeviceStat
 }
 
 }  // namespace
+
+mq_status init_attn_decode(const DeviceState *st) {
+  mq_status r = opt_in<MQ_F16>(st);
+  if (r == MQ_OK) r = opt_in<MQ_BF16>(st);
+  if (r == MQ_OK) r = opt_in<MQ_Q8_0>(st);
+  return r;
+}
 
 size_t attn_ws_bytes(int64_t S, int hq, int hkv, int dim, int64_t max_len, bool track,
                      const DeviceState *st) {

@@ -144,6 +144,7 @@ struct AttnArgs {
 size_t attn_ws_bytes(int64_t S, int hq, int hkv, int dim, int64_t max_len, bool track,
                      const DeviceState *st);
 mq_status launch_attn_decode(const AttnArgs &a, cudaStream_t s, const DeviceState *st);
+mq_status init_attn_decode(const DeviceState *st);  // shared-memory opt-ins
 
 // ---- kv_evict.cu ----
 struct EvictArgs {
@@ -160,6 +161,5 @@ struct EvictArgs {
   int *status;
 };
 mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *st);
-mq_status init_kv(DeviceState *st);  // shared-memory opt-ins of the three files' kernels
 
 }  // namespace mq

@@ -129,6 +129,4 @@ mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState 
   return r;
 }
 
-mq_status init_kv(DeviceState *) { return MQ_OK; }
-
 }  // namespace mq
