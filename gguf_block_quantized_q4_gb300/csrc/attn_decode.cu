@@ -30,8 +30,10 @@
 //
 // Precision: f16 operands are multiplied exactly and summed in binary32.  q (scaled by a power
 // of two per row) and the weights are carried as two f16 parts (22 bits), against bf16 keys and
-// values as three bf16 parts (24 bits); Q8_0 quants are exact in f16 and bf16, the keys' scales
-// multiply the 32-element block sums in binary32, the values' scales the weights.  Each tile's
+// values as three bf16 parts (24 bits); Q8_0 quants are exact in f16, the keys' scales multiply
+// the 32-element block sums in binary32, the values' scales the weights (both first scaled by
+// powers of two that put the largest weight at 2^15 and a tile's largest scale in [1/2, 1), so
+// that the second f16 part is a normal number for all but negligible products).  Each tile's
 // product is added to o by a binary32 fma (the tensor cores' own long sums may truncate).
 #include <algorithm>
 
@@ -126,14 +128,6 @@ __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
   __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&u), *reinterpret_cast<const __half2 *>(&c));
   return *reinterpret_cast<uint32_t *>(&r);
 }
-// Two int8 in the low bytes of 0x43vv 0x43vv as bf16x2: (128 + low seven bits) less (128, or
-// 256 where the sign bit is set).
-__device__ __forceinline__ uint32_t int8_bf16(uint32_t u) {
-  uint32_t a = u & 0x437f437fu, b = u & 0x43804380u;
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a),
-                             *reinterpret_cast<__nv_bfloat162 *>(&b));
-  return *reinterpret_cast<uint32_t *>(&r);
-}
 // 4 elements of an activation row.
 __device__ __forceinline__ float4 load_io4(const void *p, int io, int64_t i) {
   if (io == MQ_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
@@ -158,9 +152,8 @@ constexpr int kSmemMax = 227 * 1024;  // per thread block
 template <int TYPE, int D, int NT>
 struct Shape {
   static constexpr bool kQ8 = TYPE == MQ_Q8_0;
-  static constexpr bool kBfK = TYPE == MQ_BF16;                   // operand type of K Q^T
-  static constexpr bool kBfV = TYPE == MQ_BF16 || TYPE == MQ_Q8_0;  // of V^T P^T
-  static constexpr int kPartsK = kBfK ? 3 : 2, kPartsV = kBfV ? 3 : 2;
+  static constexpr bool kBf = TYPE == MQ_BF16;  // operands bf16, else f16
+  static constexpr int kParts = kBf ? 3 : 2;    // of the query and of the weights
   static constexpr int kRow = kQ8 ? D : 2 * D;  // bytes of a key row
   static constexpr int kNG = D / 32;            // groups of 32 dims
   static constexpr int kMT = kRow <= 128 ? 2 : 1;  // 16-key groups a warp takes at a time
@@ -169,9 +162,11 @@ struct Shape {
   // shared memory: the rings, Q8_0 scales of a ring's keys, query parts, the warps' results
   static constexpr int kStride = kRow + 16;     // an odd number of 16-byte steps
   static constexpr int kStage = 2 * kKeys * kStride;
-  static constexpr int kScales = kQ8 ? 2 * kKeys * kNG * 4 : 0;  // per stage, binary32
+  // Q8_0 scales of a stage in binary32, K's then V's, [32-element block][key]; then the power of
+  // two that V's were divided by
+  static constexpr int kScales = kQ8 ? (2 * kNG * kKeys + 4) * 4 : 0;
   static constexpr int kLdO = D + 4;
-  static constexpr int kQuery = kPartsK * NT * kNG * 32 * 16;
+  static constexpr int kQuery = kParts * NT * kNG * 32 * 16;
   static constexpr int smem(int warps, int stages) {
     return warps * (stages * (kStage + kScales) + kRows * (kLdO + 2) * 4) + kQuery + kRows * 4 + 16;
   }
@@ -182,7 +177,7 @@ struct Shape {
   static_assert(smem(kWarps, kStages) <= kSmemMax, "shared memory");
   // exp2 of a weight's exponent in the f16 parts: weights in (0, 2^15], so that the second part
   // of all but negligible weights is a normal f16
-  static constexpr float kBias = kBfV ? 0.f : 15.f;
+  static constexpr float kBias = kBf ? 0.f : 15.f;
 };
 
 struct Params {
@@ -349,12 +344,23 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   int pend_stage = -1;
   auto store_scales = [&]() {
     if (!C::kQ8 || pend_stage < 0) return;
+    uint32_t top = 0;  // the largest of V's (f16 bits of non-negative scales order as numbers)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < NG; ++j)
-        scale0[pend_stage * (C::kScales / 4) + ((lane >> 4) * C::kKeys + 16 * m + (lane & 15)) * NG + j] =
-            __half2float(__ushort_as_half(pend[m][j]));
+        if (lane >= 16) top = max(top, uint32_t(pend[m][j]) & 0x7fffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int e = top == 0 || top >= 0x7c00u ? 126 : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+    const float down = lane < 16 ? 1.f : __uint_as_float(uint32_t(253 - e) << 23);
+    float *const to = scale0 + pend_stage * (C::kScales / 4);
+    if (lane == 0) to[2 * NG * C::kKeys] = __uint_as_float(uint32_t(e + 1) << 23);  // 2^(e - 126)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+        to[((lane >> 4) * NG + j) * C::kKeys + 16 * m + (lane & 15)] =
+            __half2float(__ushort_as_half(pend[m][j])) * down;
   };
   auto issue = [&](int stage) {  // the tile looked up last, into a stage; then the next look-up
     const uint32_t row =
@@ -433,7 +439,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       const float4 v = on ? load_io4(a.q, a.io, (head0 + r) * D + lane * 8 + 4) : make_float4(0, 0, 0, 0);
       x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
       int e = 0;
-      if (!C::kBfK) {  // a power of two that puts the row's largest element in [2^14, 2^15)
+      if (!C::kBf) {  // a power of two that puts the row's largest element in [2^14, 2^15)
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
@@ -443,14 +449,14 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       const float up = __uint_as_float(uint32_t(127 + e) << 23);
       if (lane == 0) sfac[r] = p.scale_log2 * __uint_as_float(uint32_t(127 - e) << 23);
       if (lane < D / 8) {
-        uint32_t w[4][C::kPartsK];
+        uint32_t w[4][C::kParts];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split2<C::kBfK>(x[2 * i] * up, x[2 * i + 1] * up, w[i]);
+        for (int i = 0; i < 4; ++i) split2<C::kBf>(x[2 * i] * up, x[2 * i + 1] * up, w[i]);
         // the lane's 8 dims are half `lane & 1` of step lane >> 1
         uint32_t *q = reinterpret_cast<uint32_t *>(sq + ((r >> 3) * NG + (lane >> 2)) * 32 + (r & 7) * 4);
         const int step = lane >> 1 & 1, half = lane & 1;
 #pragma unroll
-        for (int k = 0; k < C::kPartsK; ++k)
+        for (int k = 0; k < C::kParts; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t *const to = q + k * NT * NG * 128;
@@ -477,51 +483,60 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       const uint32_t base = ring0 + stage * C::kStage;
       const float *const sc = scale0 + stage * (C::kScales / 4);
       if (here) {
-        // ---- S^T = K Q^T ----
-        float s[MT][NT][4];
+        // ---- S^T = K Q^T ----  (c0: the first part of the query, c1: the others)
+        float s[MT][NT][4], c0[MT][NT][4] = {}, c1[MT][NT][4] = {};
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          float c0[NT][4] = {}, c1[NT][4] = {}, total[NT][4] = {};
+        for (int j = 0; j < NG; ++j) {
+          uint4 b[C::kParts][NT];
 #pragma unroll
-          for (int j = 0; j < NG; ++j) {
+          for (int k = 0; k < C::kParts; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[k][n] = sq[((k * NT + n) * NG + j) * 32 + lane];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t at_k = base + k_lane + 16 * m * C::kStride;
             uint32_t ka[2][4];  // two steps of 16 dims
             if (C::kQ8) {
               uint32_t x[4];  // keys g (0, 2) and g + 8 (1, 3), chunks 0 and 1
-              ldmatrix4<false>(x, base + k_lane + 16 * m * C::kStride + j * 32);
+              ldmatrix4<false>(x, at_k + j * 32);
 #pragma unroll
               for (int st = 0; st < 2; ++st) {
                 const uint32_t xa = x[2 * st] ^ 0x80808080u, xb = x[2 * st + 1] ^ 0x80808080u;
                 ka[st][0] = int8_f16<0x4140>(xa), ka[st][1] = int8_f16<0x4140>(xb);
                 ka[st][2] = int8_f16<0x4342>(xa), ka[st][3] = int8_f16<0x4342>(xb);
               }
-            } else {
-              ldmatrix4<false>(ka[0], base + k_lane + 16 * m * C::kStride + j * 64);
-              ldmatrix4<false>(ka[1], base + k_lane + 16 * m * C::kStride + j * 64 + 32);
-            }
+              const float da = sc[j * C::kKeys + 16 * m + g], db = sc[j * C::kKeys + 16 * m + g + 8];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n) {  // the block's sum times the scales of keys g, g + 8
+                float c[4] = {};
 #pragma unroll
-              for (int k = 0; k < C::kPartsK; ++k) {
-                const uint4 b = sq[((k * NT + n) * NG + j) * 32 + lane];
-                mma<C::kBfK>(k ? c1[n] : c0[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], b.x, b.y);
-                mma<C::kBfK>(k ? c1[n] : c0[n], ka[1][0], ka[1][1], ka[1][2], ka[1][3], b.z, b.w);
+                for (int k = 0; k < C::kParts; ++k) {
+                  mma<C::kBf>(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[k][n].x, b[k][n].y);
+                  mma<C::kBf>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[k][n].z, b[k][n].w);
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) c0[m][n][w] = fmaf(c[w], w < 2 ? da : db, c0[m][n][w]);
               }
-            if (C::kQ8) {  // the block's scales: keys g (elements 0, 1) and g + 8 (2, 3)
-              const float da = sc[(16 * m + g) * NG + j], db = sc[(16 * m + g + 8) * NG + j];
+            } else {
+              ldmatrix4<false>(ka[0], at_k + j * 64);
+              ldmatrix4<false>(ka[1], at_k + j * 64 + 32);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  total[n][w] = fmaf(c0[n][w] + c1[n][w], w < 2 ? da : db, total[n][w]);
-                  c0[n][w] = c1[n][w] = 0.f;
+                for (int k = 0; k < C::kParts; ++k) {
+                  float(&c)[4] = k ? c1[m][n] : c0[m][n];
+                  mma<C::kBf>(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[k][n].x, b[k][n].y);
+                  mma<C::kBf>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[k][n].z, b[k][n].w);
                 }
             }
           }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) s[m][n][w] = C::kQ8 ? total[n][w] : c0[n][w] + c1[n][w];
-        }
+            for (int w = 0; w < 4; ++w) s[m][n][w] = C::kQ8 ? c0[m][n][w] : c0[m][n][w] + c1[m][n][w];
         // ---- softmax ----
         const int key0 = now.span.lo + (now.tile + i) * C::kTK + warp * C::kKeys;
         float al[NT][2];
@@ -572,7 +587,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           }
         // the weights transposed: lane (g, t) gets row g's of the keys 2t, 2t + 1, 2t + 8, 2t + 9;
         // their parts, or for Q8_0 (whose blocks' scales come first) as binary32 in two halves
-        uint32_t pw[MT][NT][2][C::kPartsV];
+        uint32_t pw[MT][NT][2][C::kParts];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -586,12 +601,13 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                 s[m][n][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
                 s[m][n][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
               } else {
-                split2<C::kBfV>(s[m][n][2 * h], s[m][n][2 * h + 1], pw[m][n][h]);
+                split2<C::kBf>(s[m][n][2 * h], s[m][n][2 * h + 1], pw[m][n][h]);
 #pragma unroll
-                for (int k = 0; k < C::kPartsV; ++k) pw[m][n][h][k] = transpose8x8(pw[m][n][h][k]);
+                for (int k = 0; k < C::kParts; ++k) pw[m][n][h][k] = transpose8x8(pw[m][n][h][k]);
               }
             }
         // ---- O^T = O^T alpha + V^T P^T ----
+        const float unit = C::kQ8 ? sc[2 * NG * C::kKeys] : 1.f;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           float c[2][NT][4] = {};
@@ -605,17 +621,17 @@ attn_decode_kernel(const __grid_constant__ Params p) {
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                  va[h][2 * q] = int8_bf16(__byte_perm(x[2 * h + q], 0x43434343u, 0x4240));
-                  va[h][2 * q + 1] = int8_bf16(__byte_perm(x[2 * h + q], 0x43434343u, 0x4341));
+                  const uint32_t u = x[2 * h + q] ^ 0x80808080u;
+                  va[h][2 * q] = int8_f16<0x4240>(u), va[h][2 * q + 1] = int8_f16<0x4341>(u);
                 }
-              float dv[4];  // the scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                dv[q] = sc[(C::kKeys + 16 * m + 8 * (q >> 1) + 2 * t + (q & 1)) * NG + j];
+              // the scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9
+              const float *const dv = sc + (NG + j) * C::kKeys + 16 * m + 2 * t;
+              const float2 d0 = *reinterpret_cast<const float2 *>(dv);
+              const float2 d1 = *reinterpret_cast<const float2 *>(dv + 8);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                split2<C::kBfV>(s[m][n][0] * dv[0], s[m][n][1] * dv[1], pw[m][n][0]);
-                split2<C::kBfV>(s[m][n][2] * dv[2], s[m][n][3] * dv[3], pw[m][n][1]);
+                split2<C::kBf>(s[m][n][0] * d0.x, s[m][n][1] * d0.y, pw[m][n][0]);
+                split2<C::kBf>(s[m][n][2] * d1.x, s[m][n][3] * d1.y, pw[m][n][1]);
               }
             } else {
               ldmatrix4<true>(va[0], base + v_lane + 16 * m * C::kStride + j * 64);
@@ -626,17 +642,19 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < C::kPartsV; ++k)
-                  mma<C::kBfV>(c[h][n], va[h][0], va[h][1], va[h][2], va[h][3], pw[m][n][0][k],
-                               pw[m][n][1][k]);
+                for (int k = 0; k < C::kParts; ++k)
+                  mma<C::kBf>(c[h][n], va[h][0], va[h][1], va[h][2], va[h][3], pw[m][n][0][k],
+                              pw[m][n][1][k]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int w = 0; w < 4; ++w)
-                o[2 * j + h][n][w] = fmaf(o[2 * j + h][n][w], al[n][w & 1], c[h][n][w]);
+              for (int w = 0; w < 4; ++w) {
+                const float old = o[2 * j + h][n][w] * al[n][w & 1];
+                o[2 * j + h][n][w] = C::kQ8 ? fmaf(c[h][n][w], unit, old) : fmaf(o[2 * j + h][n][w], al[n][w & 1], c[h][n][w]);
+              }
         }
       }
       __syncwarp();  // the stage has been read
@@ -742,29 +760,44 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 }
 
 // The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
-// head in their order.
+// head in their order.  Four keys a thread, their loads side by side (a chain of page, logits and
+// sum per key, one after the other, took 75.8 us with the attention at 32 sequences of up to 4001
+// keys).
 constexpr int kTrackKeys = 1024;
 __global__ void __launch_bounds__(256) attn_track_kernel(const __grid_constant__ Params p, int rows) {
   grid_dependency();
   const AttnArgs &a = p.a;
   const int s = blockIdx.z, h = blockIdx.y;
   const Span sp = span_of(a, s, 1);
-  for (int j = sp.lo + blockIdx.x * kTrackKeys + threadIdx.x, k = 0; k < kTrackKeys && j < sp.len;
-       j += 256, k += 256) {
-    const int64_t r = kv_row(a.c, a.pages + s * a.pages_ld, h, j);
-    if (r < 0) continue;
-    float w = 0.f;
-    for (int rg = 0; rg < p.row_groups; ++rg) {
-      const int64_t unit = int64_t(s) * p.units + h * p.row_groups + rg;
-      const float *x = p.logits + (unit * a.max_len + j) * p.logit_width;
-      const int n = min(rows, p.group - rg * rows);
-      for (int i = 0; i < n; ++i) {
-        const float2 st = p.stats[unit * rows + i];
-        w += exp2_fast(x[i] - st.x) * st.y;
-      }
-    }
-    a.c.sums[r] += w;
+  const int j0 = sp.lo + blockIdx.x * kTrackKeys + threadIdx.x;
+  if (j0 >= sp.len) return;
+  int64_t r[4];
+  float old[4], w[4] = {};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = j0 + 256 * k;
+    r[k] = j < sp.len ? kv_row(a.c, a.pages + s * a.pages_ld, h, j) : -1;
+    old[k] = r[k] < 0 ? 0.f : a.c.sums[r[k]];
   }
+  for (int rg = 0; rg < p.row_groups; ++rg) {
+    const int64_t unit = int64_t(s) * p.units + h * p.row_groups + rg;
+    const float *x = p.logits + (unit * a.max_len + j0) * p.logit_width;
+    const int n = min(rows, p.group - rg * rows);
+    for (int i = 0; i < n; i += 2) {  // (an odd group's last pair holds a row that is not there)
+      const float2 s0 = p.stats[unit * rows + i];
+      const float2 s1 = i + 1 < n ? p.stats[unit * rows + i + 1] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r[k] >= 0) {
+          const float2 v = *reinterpret_cast<const float2 *>(x + 256 * k * p.logit_width + i);
+          w[k] += exp2_fast(v.x - s0.x) * s0.y;
+          if (i + 1 < n) w[k] += exp2_fast(v.y - s1.x) * s1.y;
+        }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (r[k] >= 0) a.c.sums[r[k]] = old[k] + w[k];
 }
 
 // Query rows of a unit: 8 columns of the products, or 16 where the group fills more than 8 of
