@@ -128,24 +128,6 @@ __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
   __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&u), *reinterpret_cast<const __half2 *>(&c));
   return *reinterpret_cast<uint32_t *>(&r);
 }
-// 4 elements of an activation row.
-__device__ __forceinline__ float4 load_io4(const void *p, int io, int64_t i) {
-  if (io == MQ_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-  const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
-  const float2 a = io == MQ_F16 ? unpack2<false>(v.x) : unpack2<true>(v.x);
-  const float2 b = io == MQ_F16 ? unpack2<false>(v.y) : unpack2<true>(v.y);
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void store_io4(void *p, int io, int64_t i, float4 v) {
-  if (io == MQ_F32) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
-  } else {
-    const uint2 u = io == MQ_F16 ? make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w))
-                                 : make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w));
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = u;
-  }
-}
-
 // ---- the shape of a kernel ----------------------------------------------------------------
 constexpr int kSmemMax = 227 * 1024;  // per thread block
 
@@ -225,19 +207,21 @@ __device__ __forceinline__ int64_t all_tiles(const AttnArgs &a, int tk, int64_t 
 
 // Where a warp's next tile lies.
 struct Cursor {
-  int s, unit, tile;  // sequence, (kv head, row group), tile
+  int s, hk, rg, tile;  // sequence, kv head, row group, tile
   Span span;
-  int64_t left;       // tiles of this block from here on
+  int64_t left;         // tiles of this block from here on
 };
-__device__ __forceinline__ void next_tile(Cursor &c, const AttnArgs &a, int units, int tk) {
+__device__ __forceinline__ void next_tile(Cursor &c, const Params &p, int tk) {
   --c.left;
   if (++c.tile < c.span.tiles) return;
   c.tile = 0;
-  if (++c.unit < units) return;
-  c.unit = 0;
+  if (++c.rg < p.row_groups) return;
+  c.rg = 0;
+  if (++c.hk < p.a.c.hkv) return;
+  c.hk = 0;
   if (c.left <= 0) return;
   do {
-    c.span = span_of(a, ++c.s, tk);
+    c.span = span_of(p.a, ++c.s, tk);
   } while (c.span.tiles == 0);
 }
 
@@ -312,44 +296,45 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       cur.span = span_of(a, ++s, C::kTK);
     }
     cur.s = s;
-    cur.unit = (int)((at - first) / cur.span.tiles);
+    const int unit = (int)((at - first) / cur.span.tiles);
+    cur.hk = unit / p.row_groups;
+    cur.rg = unit % p.row_groups;
     cur.tile = (int)((at - first) % cur.span.tiles);
     cur.left = end - at;
   }
 
   // ---- the ring ----
-  // Rows of a tile's keys: lane i holds key i's.  The page entry is read one tile ahead.
-  int32_t page = -1;
+  // Rows of a tile's keys: lane i holds key i's.  The page entry is read one tile ahead, and looked
+  // at only then.
+  int32_t page = 0;
   uint32_t slot = 0;
-  int page_unit = 0;
+  int page_head = 0;
+  bool there = false;
   auto look_up = [&]() {  // at cur
     const int key = cur.span.lo + cur.tile * C::kTK + warp * C::kKeys + lane;
-    page = -1;
-    page_unit = cur.unit;
-    if (cur.left > 0 && lane < C::kKeys && key < cur.span.len) {
+    there = cur.left > 0 && lane < C::kKeys && key < cur.span.len;
+    page_head = cur.hk;
+    if (there) {
       const uint32_t pi = quotient((uint32_t)key, a.c.page);
       slot = (uint32_t)key - pi * a.c.page.d;
       page = a.pages[cur.s * a.pages_ld + pi];
-      if (page < 0 || page >= a.c.n_pages) {
-        index_error(a.status, kIdxAttnPage, page);
-        page = -1;
-      }
     }
   };
   const uint32_t ring0 = smem_addr(ring) + warp * C::kStages * C::kStage;
   float *const scale0 = scales + warp * C::kStages * (C::kScales / 4);
   uint32_t valid_bits[C::kStages] = {};  // per tile in flight (oldest first): keys that are there
   // Q8_0 scales of the newest tile, on their way: lane i has key i % 16 (+ 16), of K or V
-  uint16_t pend[MT][NG];
+  constexpr int SW = (NG + 1) / 2;  // words of a row's scales, two each
+  uint32_t pend[MT][SW];
   int pend_stage = -1;
   auto store_scales = [&]() {
     if (!C::kQ8 || pend_stage < 0) return;
-    uint32_t top = 0;  // the largest of V's (f16 bits of non-negative scales order as numbers)
+    uint32_t top = 0;  // the largest of V's (f16 bits of magnitudes order as numbers)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < NG; ++j)
-        if (lane >= 16) top = max(top, uint32_t(pend[m][j]) & 0x7fffu);
+      for (int j = 0; j < SW; ++j)
+        if (lane >= 16) top = max(top, max(pend[m][j] & 0x7fffu, pend[m][j] >> 16 & 0x7fffu));
     top = __reduce_max_sync(0xffffffffu, top);
     const int e = top == 0 || top >= 0x7c00u ? 126 : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
     const float down = lane < 16 ? 1.f : __uint_as_float(uint32_t(253 - e) << 23);
@@ -358,15 +343,19 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < NG; ++j)
-        to[((lane >> 4) * NG + j) * C::kKeys + 16 * m + (lane & 15)] =
-            __half2float(__ushort_as_half(pend[m][j])) * down;
+      for (int j = 0; j < NG; ++j) {
+        const float2 d = unpack2<false>(pend[m][j / 2]);
+        to[((lane >> 4) * NG + j) * C::kKeys + 16 * m + (lane & 15)] = (j & 1 ? d.y : d.x) * down;
+      }
   };
   auto issue = [&](int stage) {  // the tile looked up last, into a stage; then the next look-up
-    const uint32_t row =
-        page < 0 ? kNoRow
-                 : (uint32_t)(page * a.c.page_stride +
-                              (page_unit / p.row_groups) * a.c.head_stride + slot * a.c.slot_stride);
+    uint32_t row = kNoRow;
+    if (there) {
+      if (page >= 0 && page < a.c.n_pages)
+        row = (uint32_t)(page * a.c.page_stride + page_head * a.c.head_stride + slot * a.c.slot_stride);
+      else
+        index_error(a.status, kIdxAttnPage, page);
+    }
 #pragma unroll
     for (int i = 0; i + 1 < C::kStages; ++i) valid_bits[i] = valid_bits[i + 1];
     valid_bits[C::kStages - 1] = __ballot_sync(0xffffffffu, row != kNoRow);
@@ -388,22 +377,32 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       for (int m = 0; m < MT; ++m) {
         const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * m + (lane & 15));
         const __half *q = (lane < 16 ? a.c.ks : a.c.vs) + size_t(r == kNoRow ? 0 : r) * NG;
+        const bool on = r != kNoRow;
         if constexpr (NG % 4 == 0) {
 #pragma unroll
-          for (int j = 0; j < NG; j += 4) {
+          for (int j = 0; j < SW; j += 2) {
             uint2 v = make_uint2(0, 0);
-            if (r != kNoRow) v = *reinterpret_cast<const uint2 *>(q + j);
-            pend[m][j] = v.x, pend[m][j + 1] = v.x >> 16;
-            pend[m][j + 2] = v.y, pend[m][j + 3] = v.y >> 16;
+            if (on) v = *reinterpret_cast<const uint2 *>(q + 2 * j);
+            pend[m][j] = v.x, pend[m][j + 1] = v.y;
           }
-        } else {
+        } else if constexpr (NG % 2 == 0) {
 #pragma unroll
-          for (int j = 0; j < NG; ++j) pend[m][j] = r != kNoRow ? __half_as_ushort(q[j]) : 0;
+          for (int j = 0; j < SW; ++j) pend[m][j] = on ? *reinterpret_cast<const uint32_t *>(q + 2 * j) : 0;
+        } else {  // rows of an odd number of scales are 2-byte aligned
+#pragma unroll
+          for (int j = 0; j < SW; ++j) {
+            uint32_t x = 0, y = 0;
+            if (on) {
+              x = __half_as_ushort(q[2 * j]);
+              if (2 * j + 1 < NG) y = __half_as_ushort(q[2 * j + 1]);
+            }
+            pend[m][j] = x | y << 16;
+          }
         }
       }
       pend_stage = stage;
     }
-    next_tile(cur, a, p.units, C::kTK);
+    next_tile(cur, p, C::kTK);
     look_up();
   };
 
@@ -424,10 +423,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     const int64_t unit_first = at - now.tile;  // the unit's first tile, of all
     const int tiles = now.span.tiles;
     const int count = (int)min(end - at, int64_t(tiles - now.tile));
-    const int hk = now.unit / p.row_groups, rg = now.unit % p.row_groups;
-    const int rows = min(C::kRows, p.group - rg * C::kRows);  // query rows that exist
-    const int64_t head0 = int64_t(now.s) * a.hq + hk * p.group + rg * C::kRows;
-    const int64_t unit_id = int64_t(now.s) * p.units + now.unit;
+    const int rows = min(C::kRows, p.group - now.rg * C::kRows);  // query rows that exist
+    const int64_t head0 = int64_t(now.s) * a.hq + now.hk * p.group + now.rg * C::kRows;
+    const int64_t unit_id = int64_t(now.s) * p.units + now.hk * p.row_groups + now.rg;
 
     // the query's parts as operand words: lane 4 r + t' of (part, 8-row group, 32 dims) has the
     // words of two 16-dim steps.  f16 and bf16 rows: dims 2t', 2t' + 1 and 8 more of a step;
@@ -755,7 +753,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     at += count;
     now.left = end - at + 1;
     now.tile += count - 1;
-    next_tile(now, a, p.units, C::kTK);
+    next_tile(now, p, C::kTK);
   }
 }
 

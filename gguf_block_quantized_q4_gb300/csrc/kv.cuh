@@ -107,6 +107,35 @@ mq_status launch_dependent(const char *name, void (*kernel)(P...), dim3 grid, di
   return MQ_OK;
 }
 
+// Four elements of an activation row of type io (MQ_F32, MQ_F16, MQ_BF16), as binary32.
+__device__ __forceinline__ float4 load_io4(const void *p, int io, int64_t i) {
+  if (io == MQ_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+  const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+  if (io == MQ_BF16)
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ uint2 pack4(float4 v, bool bf16) {  // rounded to nearest even
+  uint2 u;
+  if (bf16) {
+    *reinterpret_cast<__nv_bfloat162 *>(&u.x) = __floats2bfloat162_rn(v.x, v.y);
+    *reinterpret_cast<__nv_bfloat162 *>(&u.y) = __floats2bfloat162_rn(v.z, v.w);
+  } else {
+    *reinterpret_cast<__half2 *>(&u.x) = __floats2half2_rn(v.x, v.y);
+    *reinterpret_cast<__half2 *>(&u.y) = __floats2half2_rn(v.z, v.w);
+  }
+  return u;
+}
+__device__ __forceinline__ void store_io4(void *p, int io, int64_t i, float4 v) {
+  if (io == MQ_F32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
+  else
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = pack4(v, io == MQ_BF16);
+}
+
 // ---- rope_store.cu ----
 struct RopeArgs {
   KvView c;
