@@ -8,9 +8,10 @@
 // What bounds it: the bytes of qkv, q and the rows stored, each moved once.  A thread keeps one
 // place in the head, four pairs (two groups of four dims, 16 bytes of f32 each), for all heads
 // that it visits: the cosines and sines of a token are read once and stay in registers, and
-// every access is 8 or 16 bytes wide.  A thread block takes a token, its threads as many heads
-// at a time as divide the heads evenly; few tokens are spread over more blocks, a round of heads
-// each.  Q8_0 rows: the largest magnitude of a 32-element block meets in shared memory as an
+// every access is 8 or 16 bytes wide.  A thread block takes one token after another, its threads
+// as many heads at a time as divide the heads evenly (a block per token pays the threads' places,
+// axes and divisions for each: 652 instructions a warp, 131 us for 16384 bf16 tokens); few tokens
+// are spread over more blocks, a round of heads each.  Q8_0 rows: the largest magnitude of a 32-element block meets in shared memory as an
 // integer maximum (the halves of a partial rotation may end inside a block, so no fixed lanes
 // share one), then the quants as in quant_row.cuh.
 #include <algorithm>
@@ -49,97 +50,131 @@ __device__ __forceinline__ uint32_t quants4(float4 v, float d) {
                      __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040), 0x5410);
 }
 
-// per_pass: heads that the block's threads take at once; passes: their rounds; gridDim.y blocks
-// share the rounds of a token.
-template <bool Q8>
+// per_pass: heads that the block's threads take at once; passes: the rounds of a token, of which NP
+// are loaded at a time; gridDim.y blocks share them.  A token's first loads need nothing but its
+// number, its positions and slot were read with the token before, so one latency covers a token.
+template <bool Q8, int NP, int IO>
 __global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_constant__ RopeArgs a,
                                                               int per_pass, int passes) {
-  __shared__ uint32_t amax[kThreads];  // [head of the round][32-element block]
-  grid_dependency();
-  const int64_t t = blockIdx.x;
-  const int dim = a.c.dim, units = dim / 8, hkv = a.c.hkv, heads = a.hq + 2 * hkv;
+  __shared__ uint32_t amax[Q8 ? NP : 1][kThreads];  // [round][head of the round][32-element block]
+  const int dim = a.c.dim, units = dim / 8, hkv = a.c.hkv, heads = a.hq + 2 * hkv, nb = dim / 32;
   const int u = threadIdx.x % units, sub = threadIdx.x / units;
   const int half = a.rope.rot_dim / 2;
   const bool turns = 4 * u < half;
   const bool apart = turns && !a.rope.pairs;
   const int d0 = apart ? 4 * u : 8 * u, d1 = apart ? half + 4 * u : 8 * u + 4;
+  const uint32_t axes = turns && a.rope.n_axes > 1 ? *reinterpret_cast<const uint32_t *>(a.rope.axis + 4 * u) : 0;
+  grid_dependency();
 
-  bool known = true;  // every position of the token lies in the table
-  for (int ax = 0; ax < a.rope.n_axes; ++ax) {
-    const int p = a.pos[ax * a.T + t];
-    if (p < 0 || p >= a.rope.max_pos) {
-      known = false;
-      if (blockIdx.y == 0 && threadIdx.x == 0) index_error(a.status, kIdxPosition, p);
-    }
-  }
-  float2 cs[4];
+  float4 x[NP], y[NP];
+  auto load = [&](int64_t t, int pass0) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    cs[k] = make_float2(1.f, 0.f);
-    if (turns && known) {
-      const int64_t p = a.pos[a.rope.axis[4 * u + k] * a.T + t];
-      cs[k] = reinterpret_cast<const float2 *>(a.rope.table)[p * half + 4 * u + k];
-    }
-  }
-  int64_t slot = a.slot[t], row0 = -1;  // the row of kv head 0, or -1: nothing is stored
-  if (known && slot >= 0) {
-    const int64_t page = slot / a.c.page.d;
-    if (page < a.c.n_pages)
-      row0 = page * a.c.page_stride + (slot - page * a.c.page.d) * a.c.slot_stride;
-    else if (blockIdx.y == 0 && threadIdx.x == 0)
-      index_error(a.status, kIdxSlot, slot);
-  }
-
-  for (int pass = blockIdx.y; pass < passes; pass += gridDim.y) {
-    const int head = pass * per_pass + sub;
-    const bool on = sub < per_pass && head < heads;
-    const int64_t col = int64_t(head) * dim;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    if (on) {
-      x = load_io4(a.qkv, a.io, t * a.ld + col + d0);
-      y = load_io4(a.qkv, a.io, t * a.ld + col + d1);
-      if (a.bias) {
-        x = add4(x, *reinterpret_cast<const float4 *>(a.bias + col + d0));
-        y = add4(y, *reinterpret_cast<const float4 *>(a.bias + col + d1));
+    for (int k = 0; k < NP; ++k) {
+      const int head = (pass0 + k) * per_pass + sub;
+      x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sub < per_pass && head < heads) {
+        x[k] = load_io4(a.qkv, IO, t * a.ld + head * dim + d0);
+        y[k] = load_io4(a.qkv, IO, t * a.ld + head * dim + d1);
       }
-      if (turns && head < a.hq + hkv) {
-        if (apart) {
-          turn(x.x, y.x, cs[0]), turn(x.y, y.y, cs[1]), turn(x.z, y.z, cs[2]), turn(x.w, y.w, cs[3]);
+    }
+  };
+  int next_pos[4];
+  int64_t next_slot;
+  auto look_up = [&](int64_t t) {
+#pragma unroll
+    for (int ax = 0; ax < 4; ++ax) next_pos[ax] = ax < a.rope.n_axes ? a.pos[ax * a.T + t] : 0;
+    next_slot = a.slot[t];
+  };
+  look_up(blockIdx.x);
+
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    load(t, blockIdx.y * NP);
+    bool known = true;  // every position of the token lies in the table
+#pragma unroll
+    for (int ax = 0; ax < 4; ++ax)
+      if (next_pos[ax] < 0 || next_pos[ax] >= a.rope.max_pos) {
+        known = false;
+        if (blockIdx.y == 0 && threadIdx.x == 0) index_error(a.status, kIdxPosition, next_pos[ax]);
+      }
+    float2 cs[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      cs[k] = make_float2(1.f, 0.f);
+      if (turns && known) {
+        const uint32_t ax = axes >> 8 * k & 3;
+        const int64_t p = ax & 2 ? (ax & 1 ? next_pos[3] : next_pos[2]) : (ax & 1 ? next_pos[1] : next_pos[0]);
+        cs[k] = reinterpret_cast<const float2 *>(a.rope.table)[p * half + 4 * u + k];
+      }
+    }
+    const int64_t slot = next_slot;
+    int64_t row0 = -1;  // the row of kv head 0, or -1: nothing is stored
+    if (known && slot >= 0) {
+      const int64_t page = slot < (int64_t(1) << 31) ? quotient((uint32_t)slot, a.c.page) : slot / a.c.page.d;
+      if (page < a.c.n_pages)
+        row0 = page * a.c.page_stride + (slot - page * a.c.page.d) * a.c.slot_stride;
+      else if (blockIdx.y == 0 && threadIdx.x == 0)
+        index_error(a.status, kIdxSlot, slot);
+    }
+    if (t + gridDim.x < a.T) look_up(t + gridDim.x);
+
+    for (int pass0 = blockIdx.y * NP; pass0 < passes; pass0 += gridDim.y * NP) {
+      if (pass0 != blockIdx.y * NP) load(t, pass0);
+      const bool quantises = Q8 && (pass0 + NP) * per_pass > a.hq;  // (the same for the whole block)
+      if (quantises) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) amax[Q8 ? k : 0][threadIdx.x] = 0;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int head = (pass0 + k) * per_pass + sub;
+        if (sub >= per_pass || head >= heads) continue;
+        const int col = head * dim;
+        if (a.bias) {
+          x[k] = add4(x[k], *reinterpret_cast<const float4 *>(a.bias + col + d0));
+          y[k] = add4(y[k], *reinterpret_cast<const float4 *>(a.bias + col + d1));
+        }
+        if (turns && head < a.hq + hkv) {
+          if (apart) {
+            turn(x[k].x, y[k].x, cs[0]), turn(x[k].y, y[k].y, cs[1]);
+            turn(x[k].z, y[k].z, cs[2]), turn(x[k].w, y[k].w, cs[3]);
+          } else {
+            turn(x[k].x, x[k].y, cs[0]), turn(x[k].z, x[k].w, cs[1]);
+            turn(y[k].x, y[k].y, cs[2]), turn(y[k].z, y[k].w, cs[3]);
+          }
+        }
+        if (head < a.hq) {
+          if (!known) x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          store_io4(a.q, IO, t * a.hq * dim + col + d0, x[k]);
+          store_io4(a.q, IO, t * a.hq * dim + col + d1, y[k]);
+          continue;
+        }
+        if (row0 < 0) continue;
+        const bool key = head < a.hq + hkv;
+        const int64_t r = row0 + (key ? head - a.hq : head - a.hq - hkv) * a.c.head_stride;
+        if (key && a.c.sums && u == 0) a.c.sums[r] = 0.f;
+        if (Q8) {
+          atomicMax(&amax[Q8 ? k : 0][sub * nb + d0 / 32], top4(x[k]));
+          atomicMax(&amax[Q8 ? k : 0][sub * nb + d1 / 32], top4(y[k]));
         } else {
-          turn(x.x, x.y, cs[0]), turn(x.z, x.w, cs[1]), turn(y.x, y.y, cs[2]), turn(y.z, y.w, cs[3]);
+          uint8_t *const to = (key ? a.c.k : a.c.v) + r * dim * 2;
+          *reinterpret_cast<uint2 *>(to + d0 * 2) = pack4(x[k], a.c.type == MQ_BF16);
+          *reinterpret_cast<uint2 *>(to + d1 * 2) = pack4(y[k], a.c.type == MQ_BF16);
         }
       }
-    }
-    if (on && head < a.hq) {
-      if (!known) x = y = make_float4(0.f, 0.f, 0.f, 0.f);
-      store_io4(a.q, a.io, t * a.hq * dim + col + d0, x);
-      store_io4(a.q, a.io, t * a.hq * dim + col + d1, y);
-    }
-    // keys and values
-    const bool stores = on && head >= a.hq && row0 >= 0;
-    const bool key = head < a.hq + hkv;
-    const int64_t r = row0 + (key ? head - a.hq : head - a.hq - hkv) * a.c.head_stride;
-    uint8_t *const plane = key ? a.c.k : a.c.v;
-    if (stores && key && a.c.sums && u == 0) a.c.sums[r] = 0.f;
-    if (!Q8) {
-      if (stores) {
-        *reinterpret_cast<uint2 *>(plane + (r * dim + d0) * 2) = pack4(x, a.c.type == MQ_BF16);
-        *reinterpret_cast<uint2 *>(plane + (r * dim + d1) * 2) = pack4(y, a.c.type == MQ_BF16);
-      }
-    } else if ((pass + 1) * per_pass > a.hq) {  // (the same for the whole block)
-      const int nb = dim / 32;
-      amax[threadIdx.x] = 0;
+      if (!quantises) continue;
       __syncthreads();
-      if (stores) {
-        atomicMax(&amax[sub * nb + d0 / 32], top4(x));
-        atomicMax(&amax[sub * nb + d1 / 32], top4(y));
-      }
-      __syncthreads();
-      if (stores) {
-        const __half s0 = block_scale(amax[sub * nb + d0 / 32]);
-        const __half s1 = d1 / 32 == d0 / 32 ? s0 : block_scale(amax[sub * nb + d1 / 32]);
-        *reinterpret_cast<uint32_t *>(plane + r * dim + d0) = quants4(x, __half2float(s0));
-        *reinterpret_cast<uint32_t *>(plane + r * dim + d1) = quants4(y, __half2float(s1));
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int head = (pass0 + k) * per_pass + sub;
+        if (sub >= per_pass || head >= heads || head < a.hq || row0 < 0) continue;
+        const bool key = head < a.hq + hkv;
+        const int64_t r = row0 + (key ? head - a.hq : head - a.hq - hkv) * a.c.head_stride;
+        const __half s0 = block_scale(amax[Q8 ? k : 0][sub * nb + d0 / 32]);
+        const __half s1 = block_scale(amax[Q8 ? k : 0][sub * nb + d1 / 32]);
+        uint8_t *const to = (key ? a.c.k : a.c.v) + r * dim;
+        *reinterpret_cast<uint32_t *>(to + d0) = quants4(x[k], __half2float(s0));
+        *reinterpret_cast<uint32_t *>(to + d1) = quants4(y[k], __half2float(s1));
         // the thread that holds a block's first dims writes its scale
         __half *const scale = (key ? a.c.ks : a.c.vs) + r * nb;
         if (d0 % 32 == 0) scale[d0 / 32] = s0;
@@ -147,6 +182,25 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_const
       }
       __syncthreads();
     }
+  }
+}
+
+// (IO is a template argument so that the loads of a group stand together, without a branch on the
+// type at each)
+template <bool Q8, int NP>
+mq_status launch_io(const RopeArgs &a, dim3 grid, dim3 block, int per_pass, int passes, cudaStream_t s) {
+  auto *kernel = a.io == MQ_F32   ? rope_store_kernel<Q8, NP, MQ_F32>
+                 : a.io == MQ_F16 ? rope_store_kernel<Q8, NP, MQ_F16>
+                                  : rope_store_kernel<Q8, NP, MQ_BF16>;
+  return launch_dependent("rope_store_kernel", kernel, grid, block, 0, s, a, per_pass, passes);
+}
+template <bool Q8>
+mq_status launch_rounds(const RopeArgs &a, int np, dim3 grid, dim3 block, int per_pass, int passes,
+                        cudaStream_t s) {
+  switch (np) {
+    case 1: return launch_io<Q8, 1>(a, grid, block, per_pass, passes, s);
+    case 2: return launch_io<Q8, 2>(a, grid, block, per_pass, passes, s);
+    default: return launch_io<Q8, 3>(a, grid, block, per_pass, passes, s);
   }
 }
 
@@ -158,13 +212,13 @@ mq_status launch_rope_store(const RopeArgs &a, cudaStream_t s, const DeviceState
   const int passes = (heads + most - 1) / most, per_pass = (heads + passes - 1) / passes;
   const unsigned threads = (per_pass * units + 31) / 32 * 32;
   // fewer tokens than fill the SMs: the rounds go to blocks of their own
-  const unsigned split = a.T * passes <= 8 * st->sms ? passes : 1;
-  const dim3 grid((unsigned)a.T, split, 1), block(threads, 1, 1);
-  return a.c.type == MQ_Q8_0
-             ? launch_dependent("rope_store_kernel", rope_store_kernel<true>, grid, block, 0, s, a,
-                                per_pass, passes)
-             : launch_dependent("rope_store_kernel", rope_store_kernel<false>, grid, block, 0, s, a,
-                                per_pass, passes);
+  const bool split = a.T * passes <= 8 * st->sms;
+  const int np = split ? 1 : std::min(passes, 3);
+  // blocks of up to 256 threads with about 70 registers: as many as are resident at once
+  const int64_t resident = int64_t(st->sms) * std::max(1, std::min(2048 / (int)threads, 65536 / (72 * (int)threads)));
+  const dim3 grid((unsigned)std::min(a.T, resident), split ? passes : 1, 1), block(threads, 1, 1);
+  return a.c.type == MQ_Q8_0 ? launch_rounds<true>(a, np, grid, block, per_pass, passes, s)
+                             : launch_rounds<false>(a, np, grid, block, per_pass, passes, s);
 }
 
 }  // namespace mq
