@@ -15,6 +15,7 @@
 // integer maximum (the halves of a partial rotation may end inside a block, so no fixed lanes
 // share one), then the quants as in quant_row.cuh.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.cuh"
 #include "quant_row.cuh"
@@ -66,59 +67,85 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_const
   const uint32_t axes = turns && a.rope.n_axes > 1 ? *reinterpret_cast<const uint32_t *>(a.rope.axis + 4 * u) : 0;
   grid_dependency();
 
+  // this thread's places: the element offset of its first group in a row of qkv (and of q), its
+  // kv head's rows from the token's first, by round of a group
+  using E = typename std::conditional<IO == MQ_F32, float, uint16_t>::type;
+  const int gap = d1 - d0;
+  auto head_of = [&](int pass) { return sub < per_pass ? pass * per_pass + sub : heads; };
+
   float4 x[NP], y[NP];
-  auto load = [&](int64_t t, int pass0) {
+  auto load = [&](const E *row, int pass0) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int head = (pass0 + k) * per_pass + sub;
+      const int head = head_of(pass0 + k);
       x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (sub < per_pass && head < heads) {
-        x[k] = load_io4(a.qkv, IO, t * a.ld + head * dim + d0);
-        y[k] = load_io4(a.qkv, IO, t * a.ld + head * dim + d1);
+      if (head < heads) {
+        const E *const from = row + (head * dim + d0);
+        x[k] = load_io4(from, IO, 0);
+        y[k] = load_io4(from + gap, IO, 0);
       }
     }
   };
-  int next_pos[4];
-  int64_t next_slot;
+  int next_pos[4] = {};
+  int64_t next_slot = -1;
   auto look_up = [&](int64_t t) {
+    next_pos[0] = a.pos[t];
+    if (a.rope.n_axes > 1) {
 #pragma unroll
-    for (int ax = 0; ax < 4; ++ax) next_pos[ax] = ax < a.rope.n_axes ? a.pos[ax * a.T + t] : 0;
+      for (int ax = 1; ax < 4; ++ax)
+        if (ax < a.rope.n_axes) next_pos[ax] = a.pos[ax * a.T + t];
+    }
     next_slot = a.slot[t];
   };
+  const uint32_t max_pos = (uint32_t)a.rope.max_pos;  // (<= 2^31)
   look_up(blockIdx.x);
 
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    load(t, blockIdx.y * NP);
+    const E *const row = static_cast<const E *>(a.qkv) + t * a.ld;
+    load(row, blockIdx.y * NP);
     bool known = true;  // every position of the token lies in the table
 #pragma unroll
     for (int ax = 0; ax < 4; ++ax)
-      if (next_pos[ax] < 0 || next_pos[ax] >= a.rope.max_pos) {
+      if ((uint32_t)next_pos[ax] >= max_pos) {
         known = false;
         if (blockIdx.y == 0 && threadIdx.x == 0) index_error(a.status, kIdxPosition, next_pos[ax]);
       }
     float2 cs[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      cs[k] = make_float2(1.f, 0.f);
-      if (turns && known) {
-        const uint32_t ax = axes >> 8 * k & 3;
-        const int64_t p = ax & 2 ? (ax & 1 ? next_pos[3] : next_pos[2]) : (ax & 1 ? next_pos[1] : next_pos[0]);
-        cs[k] = reinterpret_cast<const float2 *>(a.rope.table)[p * half + 4 * u + k];
+    for (int k = 0; k < 4; ++k) cs[k] = make_float2(1.f, 0.f);
+    if (turns && known) {
+      const float2 *const table = reinterpret_cast<const float2 *>(a.rope.table) + 4 * u;
+      if (a.rope.n_axes == 1) {
+        const float4 *const from = reinterpret_cast<const float4 *>(table + (uint64_t)(uint32_t)next_pos[0] * half);
+        const float4 v = from[0], w = from[1];
+        cs[0] = make_float2(v.x, v.y), cs[1] = make_float2(v.z, v.w);
+        cs[2] = make_float2(w.x, w.y), cs[3] = make_float2(w.z, w.w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t ax = axes >> 8 * k & 3;
+          const int p = ax & 2 ? (ax & 1 ? next_pos[3] : next_pos[2]) : (ax & 1 ? next_pos[1] : next_pos[0]);
+          cs[k] = table[(uint64_t)(uint32_t)p * half + k];
+        }
       }
     }
     const int64_t slot = next_slot;
-    int64_t row0 = -1;  // the row of kv head 0, or -1: nothing is stored
-    if (known && slot >= 0) {
+    bool stores = known && slot >= 0;
+    uint32_t row0 = 0;  // the row of kv head 0 (the cache spans less than 2^32 rows)
+    if (stores) {
       const int64_t page = slot < (int64_t(1) << 31) ? quotient((uint32_t)slot, a.c.page) : slot / a.c.page.d;
-      if (page < a.c.n_pages)
-        row0 = page * a.c.page_stride + (slot - page * a.c.page.d) * a.c.slot_stride;
+      stores = page < a.c.n_pages;
+      if (stores)
+        row0 = (uint32_t)page * (uint32_t)a.c.page_stride +
+               (uint32_t)(slot - page * a.c.page.d) * (uint32_t)a.c.slot_stride;
       else if (blockIdx.y == 0 && threadIdx.x == 0)
         index_error(a.status, kIdxSlot, slot);
     }
     if (t + gridDim.x < a.T) look_up(t + gridDim.x);
+    E *const q = static_cast<E *>(a.q) + t * (a.hq * dim);
 
     for (int pass0 = blockIdx.y * NP; pass0 < passes; pass0 += gridDim.y * NP) {
-      if (pass0 != blockIdx.y * NP) load(t, pass0);
+      if (pass0 != blockIdx.y * NP) load(row, pass0);
       const bool quantises = Q8 && (pass0 + NP) * per_pass > a.hq;  // (the same for the whole block)
       if (quantises) {
 #pragma unroll
@@ -127,12 +154,12 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_const
       }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const int head = (pass0 + k) * per_pass + sub;
-        if (sub >= per_pass || head >= heads) continue;
-        const int col = head * dim;
+        const int head = head_of(pass0 + k);
+        if (head >= heads) continue;
+        const int at = head * dim + d0;
         if (a.bias) {
-          x[k] = add4(x[k], *reinterpret_cast<const float4 *>(a.bias + col + d0));
-          y[k] = add4(y[k], *reinterpret_cast<const float4 *>(a.bias + col + d1));
+          x[k] = add4(x[k], *reinterpret_cast<const float4 *>(a.bias + at));
+          y[k] = add4(y[k], *reinterpret_cast<const float4 *>(a.bias + at + gap));
         }
         if (turns && head < a.hq + hkv) {
           if (apart) {
@@ -145,38 +172,38 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_const
         }
         if (head < a.hq) {
           if (!known) x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          store_io4(a.q, IO, t * a.hq * dim + col + d0, x[k]);
-          store_io4(a.q, IO, t * a.hq * dim + col + d1, y[k]);
+          store_io4(q + at, IO, 0, x[k]);
+          store_io4(q + at + gap, IO, 0, y[k]);
           continue;
         }
-        if (row0 < 0) continue;
+        if (!stores) continue;
         const bool key = head < a.hq + hkv;
-        const int64_t r = row0 + (key ? head - a.hq : head - a.hq - hkv) * a.c.head_stride;
+        const uint32_t r = row0 + (uint32_t)(key ? head - a.hq : head - a.hq - hkv) * (uint32_t)a.c.head_stride;
         if (key && a.c.sums && u == 0) a.c.sums[r] = 0.f;
         if (Q8) {
           atomicMax(&amax[Q8 ? k : 0][sub * nb + d0 / 32], top4(x[k]));
           atomicMax(&amax[Q8 ? k : 0][sub * nb + d1 / 32], top4(y[k]));
         } else {
-          uint8_t *const to = (key ? a.c.k : a.c.v) + r * dim * 2;
-          *reinterpret_cast<uint2 *>(to + d0 * 2) = pack4(x[k], a.c.type == MQ_BF16);
-          *reinterpret_cast<uint2 *>(to + d1 * 2) = pack4(y[k], a.c.type == MQ_BF16);
+          uint16_t *const to = reinterpret_cast<uint16_t *>(key ? a.c.k : a.c.v) + ((uint64_t)r * dim + d0);
+          *reinterpret_cast<uint2 *>(to) = pack4(x[k], a.c.type == MQ_BF16);
+          *reinterpret_cast<uint2 *>(to + gap) = pack4(y[k], a.c.type == MQ_BF16);
         }
       }
       if (!quantises) continue;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const int head = (pass0 + k) * per_pass + sub;
-        if (sub >= per_pass || head >= heads || head < a.hq || row0 < 0) continue;
+        const int head = head_of(pass0 + k);
+        if (head >= heads || head < a.hq || !stores) continue;
         const bool key = head < a.hq + hkv;
-        const int64_t r = row0 + (key ? head - a.hq : head - a.hq - hkv) * a.c.head_stride;
+        const uint32_t r = row0 + (uint32_t)(key ? head - a.hq : head - a.hq - hkv) * (uint32_t)a.c.head_stride;
         const __half s0 = block_scale(amax[Q8 ? k : 0][sub * nb + d0 / 32]);
         const __half s1 = block_scale(amax[Q8 ? k : 0][sub * nb + d1 / 32]);
-        uint8_t *const to = (key ? a.c.k : a.c.v) + r * dim;
-        *reinterpret_cast<uint32_t *>(to + d0) = quants4(x[k], __half2float(s0));
-        *reinterpret_cast<uint32_t *>(to + d1) = quants4(y[k], __half2float(s1));
+        uint8_t *const to = (key ? a.c.k : a.c.v) + ((uint64_t)r * dim + d0);
+        *reinterpret_cast<uint32_t *>(to) = quants4(x[k], __half2float(s0));
+        *reinterpret_cast<uint32_t *>(to + gap) = quants4(y[k], __half2float(s1));
         // the thread that holds a block's first dims writes its scale
-        __half *const scale = (key ? a.c.ks : a.c.vs) + r * nb;
+        __half *const scale = (key ? a.c.ks : a.c.vs) + (uint64_t)r * nb;
         if (d0 % 32 == 0) scale[d0 / 32] = s0;
         if (d1 % 32 == 0) scale[d1 / 32] = s1;
       }
