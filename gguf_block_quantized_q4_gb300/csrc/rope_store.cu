@@ -55,7 +55,7 @@ __device__ __forceinline__ uint32_t quants4(float4 v, float d) {
 // are loaded at a time; gridDim.y blocks share them.  A token's first loads need nothing but its
 // number, its positions and slot were read with the token before, so one latency covers a token.
 template <bool Q8, int NP, int IO>
-__global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_constant__ RopeArgs a,
+__global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_constant__ RopeArgs a,
                                                               int per_pass, int passes) {
   __shared__ uint32_t amax[Q8 ? NP : 1][kThreads];  // [round][head of the round][32-element block]
   const int dim = a.c.dim, units = dim / 8, hkv = a.c.hkv, heads = a.hq + 2 * hkv, nb = dim / 32;
@@ -241,8 +241,8 @@ mq_status launch_rope_store(const RopeArgs &a, cudaStream_t s, const DeviceState
   // fewer tokens than fill the SMs: the rounds go to blocks of their own
   const bool split = a.T * passes <= 8 * st->sms;
   const int np = split ? 1 : std::min(passes, 3);
-  // blocks of up to 256 threads with about 70 registers: as many as are resident at once
-  const int64_t resident = int64_t(st->sms) * std::max(1, std::min(2048 / (int)threads, 65536 / (72 * (int)threads)));
+  // blocks of up to 256 threads with 64 registers: as many as are resident at once
+  const int64_t resident = int64_t(st->sms) * std::max(1, std::min(2048 / (int)threads, 65536 / (64 * (int)threads)));
   const dim3 grid((unsigned)std::min(a.T, resident), split ? passes : 1, 1), block(threads, 1, 1);
   return a.c.type == MQ_Q8_0 ? launch_rounds<true>(a, np, grid, block, per_pass, passes, s)
                              : launch_rounds<false>(a, np, grid, block, per_pass, passes, s);
