@@ -85,19 +85,22 @@ __device__ __forceinline__ void grid_dependency() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// cluster: thread blocks of a cluster, along x (grid.x a multiple of it).
 template <class... P, class... A>
-mq_status launch_dependent(const char *name, void (*kernel)(P...), dim3 grid, dim3 block,
-                           size_t smem, cudaStream_t s, A... args) {
+mq_status launch_cluster(const char *name, void (*kernel)(P...), dim3 grid, dim3 block,
+                         size_t smem, cudaStream_t s, unsigned cluster, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = test_fail_launch() ? dim3(0, 1, 1) : grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
@@ -105,6 +108,12 @@ mq_status launch_dependent(const char *name, void (*kernel)(P...), dim3 grid, di
                 grid.x, grid.y, grid.z, block.x, cudaGetErrorName(e));
   }
   return MQ_OK;
+}
+
+template <class... P, class... A>
+mq_status launch_dependent(const char *name, void (*kernel)(P...), dim3 grid, dim3 block,
+                           size_t smem, cudaStream_t s, A... args) {
+  return launch_cluster(name, kernel, grid, block, smem, s, 1, args...);
 }
 
 // Four elements of an activation row of type io (MQ_F32, MQ_F16, MQ_BF16), as binary32.
@@ -190,5 +199,6 @@ struct EvictArgs {
   int *status;
 };
 mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *st);
+mq_status init_kv_evict(const DeviceState *st);  // shared-memory opt-in
 
 }  // namespace mq

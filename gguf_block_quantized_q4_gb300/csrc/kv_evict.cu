@@ -1,15 +1,32 @@
-// kv_evict.cu -- mq_kv_evict: the rows that stay are chosen per (sequence, kv head) by one CTA,
-// then copied in order.
+// kv_evict.cu -- mq_kv_evict: the rows that stay are chosen per (sequence, kv head), then copied
+// in order.
 //
 // Choice: a weight sum maps to an unsigned key in the order of the values (NaN above all, -0 as
-// 0); the smallest key of the rows that stay is found bit by bit from the top, counting the
-// candidates at or above each trial key; rows equal to it stay from the lowest position on.
+// 0).  A thread block cluster of up to 8 blocks holds the candidates' keys of one kv head in
+// shared memory (a part of the positions each) and finds the smallest key that stays by a radix
+// selection from the top: histograms of 11, 11 and 10 bits, summed over the cluster through
+// distributed shared memory.  Rows equal to that key stay from the lowest position on; ballots
+// and the cluster's counts give every row its place.  What bounds it: latency, three rounds of
+// histogram and cluster barrier (it reads 4 bytes per row; counting bit by bit from global
+// memory, one block per head, took 5.2 ms for 131072 rows).
+//
+// Copy: bounded by the bytes of the kept rows, read and written once.  A warp looks up 32 (or,
+// when there are few, 16) rows, one per lane, then moves them 16 bytes a lane, eight loads in
+// flight.
+#include <algorithm>
+#include <cooperative_groups.h>
+
 #include "kv.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace mq {
 namespace {
 
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeysHeld = 48 * 1024;  // per block, in shared memory; further keys are read again
+constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0xffffffffu;
@@ -17,116 +34,243 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Sum over the CTA (every thread gets it); buf: one int per warp.
-__device__ int block_sum(int v, int *buf) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int s = 0;
-  for (int w = 0; w < kSelThreads / 32; ++w) s += buf[w];
-  return s;
-}
-// Threads before this one whose flag is set, and the CTA's count of them.
-__device__ int block_rank(bool f, int *buf, int *total) {
-  const unsigned b = __ballot_sync(0xffffffffu, f);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (lane == 0) buf[warp] = __popc(b);
-  __syncthreads();
-  int before = __popc(b & ((1u << lane) - 1)), all = 0;
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    if (w < warp) before += buf[w];
-    all += buf[w];
-  }
-  *total = all;
-  return before;
-}
+struct SelShared {
+  uint32_t hist[kBins];
+  uint32_t warp_sum[kSelWarps];
+  uint32_t gt[kSelWarps], eq[kSelWarps];  // per warp: candidates above T, equal to it
+  uint32_t all_gt, all_eq;                // of the block
+  uint32_t bin, above, in_bin;            // the bin chosen, candidates above it and in it
+};
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
-  __shared__ int buf[kSelThreads / 32];
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a,
+                                                                      int held) {
+  extern __shared__ __align__(16) uint32_t keys[];  // [held]
+  __shared__ SelShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int s = blockIdx.y, h = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency();
-  const int s = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   const int raw = a.len[s], n = clamped_len(raw, a.max_len);
-  if (h == 0 && tid == 0) {
+  if (h == 0 && rank == 0 && tid == 0) {
     if (raw != n) index_error(a.status, kIdxEvictLen, raw);
     a.new_len[s] = min(n, a.keep);
   }
   int32_t *kept = a.kept + (int64_t(s) * a.c.hkv + h) * a.keep;
-  if (n <= a.keep) {
-    for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
+  const int share = rank * kSelThreads + tid, stride = ranks * kSelThreads;
+  if (n <= a.keep) {  // (the whole cluster)
+    for (int i = share; i < a.keep; i += stride) kept[i] = i < n ? i : -1;
     return;
   }
+  for (int i = share; i < a.sink; i += stride) kept[i] = i;
+  for (int i = share; i < a.recent; i += stride) kept[a.keep - a.recent + i] = n - a.recent + i;
+
+  // this block's candidates: positions [first, first + count)
+  const int all = n - a.recent - a.sink;
+  const int per = (all + ranks - 1) / ranks;
+  const int first = a.sink + rank * per, count = max(0, min(per, all - rank * per));
   const int32_t *pages = a.pages + s * a.pages_ld;
-  const int lo = a.sink, hi = n - a.recent, need = a.keep - a.sink - a.recent;
-  auto key = [&](int i) -> uint32_t {
-    const int64_t r = kv_row(a.c, pages, h, i);
-    return r < 0 ? order_key(0.f) : order_key(a.c.sums[r]);
+  auto read_key = [&](int i) -> uint32_t {
+    const int64_t r = kv_row(a.c, pages, h, first + i);
+    return order_key(r < 0 ? 0.f : a.c.sums[r]);
   };
-  // the largest key T with at least `need` candidates at or above it
-  uint32_t T = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t trial = T | (1u << bit);
-    int c = 0;
-    for (int i = lo + tid; i < hi; i += kSelThreads) c += key(i) >= trial;
-    if (block_sum(c, buf) >= need) T = trial;
+  auto key = [&](int i) -> uint32_t { return i < held ? keys[i] : read_key(i); };
+#pragma unroll 4
+  for (int i = tid; i < min(count, held); i += kSelThreads) keys[i] = read_key(i);
+
+  uint32_t need = a.keep - a.sink - a.recent;  // candidates that stay, of those not yet above
+  uint32_t T = 0, ties = 0;                    // keys above T stay, and `ties` of those equal
+  if (need == 0) {
+    T = 0xffffffffu;
+  } else {
+    uint32_t prefix = 0;  // the chosen bits so far
+    for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
+      const int bits = shift ? 11 : 10;
+      for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < count; i += kSelThreads) {
+        const uint32_t k = key(i);
+        if (shift == 21 || k >> (shift + bits) == prefix)
+          atomicAdd(&sh.hist[k >> shift & ((1u << bits) - 1)], 1u);
+      }
+      cluster.sync();
+      // the cluster's counts of this thread's two bins, from the top bin down
+      const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
+      uint32_t c1 = 0, c0 = 0;
+#pragma unroll 8
+      for (int q = 0; q < ranks; ++q) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(sh.hist, q) + b0);
+        c0 += v.x, c1 += v.y;
+      }
+      uint32_t inc = c0 + c1;  // inclusive sum over the threads before
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += o;
+      }
+      if (lane == 31) sh.warp_sum[warp] = inc;
+      __syncthreads();
+      uint32_t before = 0;
+      for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+      const uint32_t up1 = before + inc - c0 - c1, up0 = up1 + c1;  // candidates above each bin
+      if (up1 < need && need <= up1 + c1) sh.bin = b1, sh.above = up1, sh.in_bin = c1;
+      if (up0 < need && need <= up0 + c0) sh.bin = b0, sh.above = up0, sh.in_bin = c0;
+      cluster.sync();  // (also before the histograms are cleared)
+      need -= sh.above;
+      prefix = prefix << bits | sh.bin;
+      if (shift == 0) {
+        T = prefix, ties = need;
+        break;
+      }
+      if (need == sh.in_bin && prefix != 0) {  // the whole bin stays
+        T = (prefix << shift) - 1, ties = 0;
+        break;
+      }
+      __syncthreads();
+    }
   }
-  int above = 0;
-  for (int i = lo + tid; i < hi; i += kSelThreads) above += key(i) > T;
-  int ties = need - block_sum(above, buf);  // rows equal to T that stay
-  int out = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const bool middle = i >= lo && i < hi;
-    const uint32_t k = middle ? key(i) : 0;
-    int all;
-    const int eq = block_rank(middle && k == T, buf, &all);
-    const bool stay = i < n && (!middle || k > T || (k == T && eq < ties));
-    ties -= min(ties, all);
-    const int place = block_rank(stay, buf, &all);
-    if (stay) kept[out + place] = i;
-    out += all;
+
+  // places: each warp has a run of the block's candidates
+  const int run = (count + kSelThreads - 1) / kSelThreads * 32;
+  const int r0 = min(warp * run, count), r1 = min(r0 + run, count);
+  uint32_t gt = 0, eq = 0;
+  for (int i = r0 + lane; i < r1 + lane; i += 32) {
+    const uint32_t k = i < r1 ? key(i) : 0;
+    gt += __popc(__ballot_sync(0xffffffffu, i < r1 && k > T));
+    eq += __popc(__ballot_sync(0xffffffffu, i < r1 && k == T));
+  }
+  if (lane == 0) sh.gt[warp] = gt, sh.eq[warp] = eq;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t g = __reduce_add_sync(0xffffffffu, sh.gt[lane]);
+    const uint32_t e = __reduce_add_sync(0xffffffffu, sh.eq[lane]);
+    if (lane == 0) sh.all_gt = g, sh.all_eq = e;
+  }
+  cluster.sync();
+  uint32_t gt_at = 0, eq_at = 0;  // before this warp's run
+  for (int q = 0; q < rank; ++q) {
+    gt_at += *cluster.map_shared_rank(&sh.all_gt, q);
+    eq_at += *cluster.map_shared_rank(&sh.all_eq, q);
+  }
+  cluster.sync();  // no block leaves while another reads its counts
+  for (int w = 0; w < warp; ++w) gt_at += sh.gt[w], eq_at += sh.eq[w];
+  const uint32_t below = (1u << lane) - 1;
+  for (int i = r0 + lane; i < r1 + lane; i += 32) {
+    const uint32_t k = i < r1 ? key(i) : 0;
+    const unsigned is_eq = __ballot_sync(0xffffffffu, i < r1 && k == T);
+    const bool stay = i < r1 && (k > T || (k == T && eq_at + __popc(is_eq & below) < ties));
+    const unsigned stays = __ballot_sync(0xffffffffu, stay);
+    if (stay) kept[a.sink + gt_at + min(eq_at, ties) + __popc(stays & below)] = first + i;
+    gt_at += __popc(stays) - (min(eq_at + __popc(is_eq), ties) - min(eq_at, ties));
+    eq_at += __popc(is_eq);
   }
 }
 
-__global__ void __launch_bounds__(256) evict_copy_kernel(EvictArgs a) {
-  grid_dependency();
+// RB: bytes of a row; ROWS: rows of a warp (16 or 32).
+template <int RB, int ROWS>
+__global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__ EvictArgs a) {
+  constexpr int CH = RB / 16, STEPS = ROWS * CH / 32, NU = STEPS % 4 == 0 ? 4 : STEPS % 3 == 0 ? 3 : STEPS % 2 == 0 ? 2 : 1;
   const int s = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (j >= a.keep) return;
-  const int src = a.kept[(int64_t(s) * a.c.hkv + h) * a.keep + j];
-  if (src < 0) return;
-  const int64_t r = kv_row(a.c, a.pages + s * a.pages_ld, h, src);
-  const int64_t w = kv_row(a.c, a.new_pages + s * a.new_pages_ld, h, j);
-  if (r < 0 || w < 0) {
-    if (lane == 0)
-      index_error(a.status, kIdxEvictPage,
-                  r < 0 ? a.pages[s * a.pages_ld + src / a.c.page.d]
-                        : a.new_pages[s * a.new_pages_ld + j / a.c.page.d]);
-    return;
+  const int j = (blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS + lane;
+  grid_dependency();
+  if (j - lane >= a.keep) return;
+  uint32_t from = 0, to = 0;
+  bool on = false;
+  if (lane < ROWS && j < a.keep) {
+    const int src = a.kept[(int64_t(s) * a.c.hkv + h) * a.keep + j];
+    if (src >= 0) {
+      const int64_t r = kv_row(a.c, a.pages + s * a.pages_ld, h, src);
+      const int64_t w = kv_row(a.c, a.new_pages + s * a.new_pages_ld, h, j);
+      on = r >= 0 && w >= 0;
+      from = (uint32_t)r, to = (uint32_t)w;
+      if (!on)
+        index_error(a.status, kIdxEvictPage,
+                    r < 0 ? a.pages[s * a.pages_ld + quotient(src, a.c.page)]
+                          : a.new_pages[s * a.new_pages_ld + quotient(j, a.c.page)]);
+    }
   }
-  const int words = (a.c.type == MQ_Q8_0 ? a.c.dim : 2 * a.c.dim) / 16;
-  for (int i = lane; i < words; i += 32) {
-    reinterpret_cast<uint4 *>(a.c.k)[w * words + i] = reinterpret_cast<const uint4 *>(a.c.k)[r * words + i];
-    reinterpret_cast<uint4 *>(a.c.v)[w * words + i] = reinterpret_cast<const uint4 *>(a.c.v)[r * words + i];
+  const unsigned live = __ballot_sync(0xffffffffu, on);
+  if (live == 0) return;
+  float sum = 0.f;
+  if (on) sum = a.c.sums[from];
+#pragma unroll 1
+  for (int st = 0; st < STEPS; st += NU) {
+    uint4 k[NU], v[NU];
+    uint32_t dst[NU];
+    bool ok[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int c = (st + i) * 32 + lane, row = c / CH, ch = c % CH;
+      const uint32_t src = __shfl_sync(0xffffffffu, from, row);
+      dst[i] = __shfl_sync(0xffffffffu, to, row);
+      ok[i] = live >> row & 1;
+      if (ok[i]) {
+        k[i] = *reinterpret_cast<const uint4 *>(a.c.k + size_t(src) * RB + ch * 16);
+        v[i] = *reinterpret_cast<const uint4 *>(a.c.v + size_t(src) * RB + ch * 16);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int ch = ((st + i) * 32 + lane) % CH;
+      if (ok[i]) {
+        *reinterpret_cast<uint4 *>(a.c.k + size_t(dst[i]) * RB + ch * 16) = k[i];
+        *reinterpret_cast<uint4 *>(a.c.v + size_t(dst[i]) * RB + ch * 16) = v[i];
+      }
+    }
   }
-  const int nb = a.c.dim / 32;
-  if (a.c.type == MQ_Q8_0 && lane < nb) {
-    a.c.ks[w * nb + lane] = a.c.ks[r * nb + lane];
-    a.c.vs[w * nb + lane] = a.c.vs[r * nb + lane];
+  if (!on) return;
+  a.c.sums[to] = sum;
+  if (a.c.type == MQ_Q8_0) {  // a lane its own row's scales
+    constexpr int NB = RB / 32;
+    const size_t f = size_t(from) * NB, t = size_t(to) * NB;
+    __half ks[NB], vs[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) ks[i] = a.c.ks[f + i], vs[i] = a.c.vs[f + i];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) a.c.ks[t + i] = ks[i], a.c.vs[t + i] = vs[i];
   }
-  if (lane == 0) a.c.sums[w] = a.c.sums[r];
+}
+
+template <int RB>
+mq_status launch_copy(const EvictArgs &a, cudaStream_t s, const DeviceState *st) {
+  const int64_t rows = a.S * a.c.hkv * a.keep;
+  const bool few = rows < int64_t(st->sms) * 16 * 32;  // less than 16 warps of 32 rows per SM
+  const int per_block = 8 * (few ? 16 : 32);
+  const dim3 grid((a.keep + per_block - 1) / per_block, (unsigned)a.S, a.c.hkv);
+  return launch_dependent("evict_copy_kernel", few ? evict_copy_kernel<RB, 16> : evict_copy_kernel<RB, 32>,
+                          grid, dim3(256, 1, 1), 0, s, a);
 }
 
 }  // namespace
 
-mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *) {
-  mq_status r = launch_dependent("evict_select_kernel", evict_select_kernel,
-                                 dim3((unsigned)a.S, a.c.hkv, 1), dim3(kSelThreads, 1, 1), 0, s, a);
-  if (r == MQ_OK)
-    r = launch_dependent("evict_copy_kernel", evict_copy_kernel,
-                         dim3((a.keep + 7) / 8, (unsigned)a.S, a.c.hkv), dim3(256, 1, 1), 0, s, a);
-  return r;
+mq_status init_kv_evict(const DeviceState *st) {
+  const int bytes = kKeysHeld * 4;
+  if (bytes + (int)sizeof(SelShared) > st->smem_optin)
+    return fail(MQ_ERR_LAUNCH, "evict_select_kernel needs %d bytes of shared memory, the device allows %d",
+                bytes + (int)sizeof(SelShared), st->smem_optin);
+  const cudaError_t e =
+      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e == cudaSuccess ? MQ_OK : cuda_fail(e, "cudaFuncSetAttribute", "evict_select_kernel");
+}
+
+mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *st) {
+  // blocks of a cluster: at least 1024 candidates each, and no more blocks than SMs
+  int ranks = 1;
+  while (ranks < kMaxCluster && a.max_len / (2 * ranks) >= kSelThreads && a.S * a.c.hkv * 2 * ranks <= st->sms)
+    ranks *= 2;
+  const int held = std::min((a.max_len + ranks - 1) / ranks, kKeysHeld);
+  mq_status r = launch_cluster("evict_select_kernel", evict_select_kernel,
+                               dim3(ranks, (unsigned)a.S, a.c.hkv), dim3(kSelThreads, 1, 1),
+                               size_t(held) * 4, s, ranks, a, held);
+  if (r != MQ_OK) return r;
+  switch (a.c.type == MQ_Q8_0 ? a.c.dim : 2 * a.c.dim) {
+    case 64: return launch_copy<64>(a, s, st);
+    case 96: return launch_copy<96>(a, s, st);
+    case 128: return launch_copy<128>(a, s, st);
+    case 192: return launch_copy<192>(a, s, st);
+    case 256: return launch_copy<256>(a, s, st);
+    case 384: return launch_copy<384>(a, s, st);
+    default: return launch_copy<512>(a, s, st);
+  }
 }
 
 }  // namespace mq

@@ -155,6 +155,7 @@ extern "C" mq_status mq_init(int device) {
   mq_status s = init_kernels(st);
   if (s == MQ_OK) s = init_matvec(st);
   if (s == MQ_OK) s = init_attn_decode(st);
+  if (s == MQ_OK) s = init_kv_evict(st);
   // the static scratch of mq_mmq_fused_static: looking its address up here loads this file's
   // device code (and with it the array) now, outside any stream capture of the caller
   uint8_t *scratch = nullptr;
