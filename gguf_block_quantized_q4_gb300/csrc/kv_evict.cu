@@ -4,8 +4,9 @@
 // Choice: a weight sum maps to an unsigned key in the order of the values (NaN above all, -0 as
 // 0).  A thread block cluster of up to 8 blocks holds the candidates' keys of one kv head in
 // shared memory (a part of the positions each) and finds the smallest key that stays by a radix
-// selection from the top: histograms of 11, 11 and 10 bits, summed over the cluster through
-// distributed shared memory.  Rows equal to that key stay from the lowest position on; ballots
+// selection from the top: histograms of 11, 11 and 10 bits, whose bins that are not empty are added
+// to rank 0's through distributed shared memory (every rank reading all of the others' took one
+// more cluster barrier and eight times the reads).  Rows equal to that key stay from the lowest position on; ballots
 // and the cluster's counts give every row its place.  What bounds it: latency, three rounds of
 // histogram and cluster barrier (it reads 4 bytes per row; counting bit by bit from global
 // memory, one block per head, took 5.2 ms for 131072 rows).
@@ -36,19 +37,28 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 struct SelShared {
   uint32_t hist[kBins];
+  uint32_t total[3][kBins];               // rank 0's: the cluster's histograms
   uint32_t warp_sum[kSelWarps];
   uint32_t gt[kSelWarps], eq[kSelWarps];  // per warp: candidates above T, equal to it
-  uint32_t all_gt, all_eq;                // of the block
+  uint32_t rank_gt[kMaxCluster], rank_eq[kMaxCluster];
   uint32_t bin, above, in_bin;            // the bin chosen, candidates above it and in it
 };
+
+// Sum over the warps before this one of a value per warp in shared memory.
+__device__ __forceinline__ uint32_t sum_before(const uint32_t *per_warp, int warp, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < warp ? per_warp[lane] : 0u);
+}
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a,
                                                                       int held) {
   extern __shared__ __align__(16) uint32_t keys[];  // [held]
-  __shared__ SelShared sh;
+  __shared__ __align__(16) SelShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int s = blockIdx.y, h = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kBins; i += kSelThreads)
+    sh.hist[i] = sh.total[0][i] = sh.total[1][i] = sh.total[2][i] = 0;
+  cluster.barrier_arrive();  // (the totals are clear; waited for before the first is added to)
   grid_dependency();
   const int raw = a.len[s], n = clamped_len(raw, a.max_len);
   if (h == 0 && rank == 0 && tid == 0) {
@@ -59,6 +69,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const int share = rank * kSelThreads + tid, stride = ranks * kSelThreads;
   if (n <= a.keep) {  // (the whole cluster)
     for (int i = share; i < a.keep; i += stride) kept[i] = i < n ? i : -1;
+    cluster.barrier_wait();
     return;
   }
   for (int i = share; i < a.sink; i += stride) kept[i] = i;
@@ -69,13 +80,33 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const int per = (all + ranks - 1) / ranks;
   const int first = a.sink + rank * per, count = max(0, min(per, all - rank * per));
   const int32_t *pages = a.pages + s * a.pages_ld;
-  auto read_key = [&](int i) -> uint32_t {
+  auto key = [&](int i) -> uint32_t {
+    if (i < held) return keys[i];
     const int64_t r = kv_row(a.c, pages, h, first + i);
     return order_key(r < 0 ? 0.f : a.c.sums[r]);
   };
-  auto key = [&](int i) -> uint32_t { return i < held ? keys[i] : read_key(i); };
-#pragma unroll 4
-  for (int i = tid; i < min(count, held); i += kSelThreads) keys[i] = read_key(i);
+  // the keys: 16 pages and then 16 sums side by side, counted by their top bits at once
+  __syncthreads();
+  constexpr int NK = 16;
+  for (int i0 = tid; i0 < count; i0 += NK * kSelThreads) {
+    uint32_t r[NK];  // rows (fewer than 2^32 - 1)
+    float w[NK];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const int i = i0 + k * kSelThreads;
+      r[k] = i < count ? (uint32_t)kv_row(a.c, pages, h, first + i) : ~0u;
+    }
+#pragma unroll
+    for (int k = 0; k < NK; ++k) w[k] = r[k] == ~0u ? 0.f : a.c.sums[r[k]];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const int i = i0 + k * kSelThreads;
+      const uint32_t v = order_key(w[k]);
+      if (i < min(count, held)) keys[i] = v;
+      if (i < count) atomicAdd(&sh.hist[v >> 21], 1u);
+    }
+  }
+  cluster.barrier_wait();
 
   uint32_t need = a.keep - a.sink - a.recent;  // candidates that stay, of those not yet above
   uint32_t T = 0, ties = 0;                    // keys above T stay, and `ties` of those equal
@@ -83,25 +114,27 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     T = 0xffffffffu;
   } else {
     uint32_t prefix = 0;  // the chosen bits so far
-    for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
-      const int bits = shift ? 11 : 10;
-      for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < count; i += kSelThreads) {
-        const uint32_t k = key(i);
-        if (shift == 21 || k >> (shift + bits) == prefix)
-          atomicAdd(&sh.hist[k >> shift & ((1u << bits) - 1)], 1u);
+    for (int pass = 0;; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      if (pass) {
+        for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+        __syncthreads();
+#pragma unroll 8
+        for (int i = tid; i < count; i += kSelThreads) {
+          const uint32_t k = key(i);
+          if (k >> (shift + bits) == prefix) atomicAdd(&sh.hist[k >> shift & ((1u << bits) - 1)], 1u);
+        }
       }
+      __syncthreads();
+      // the bins that are not empty, to rank 0
+      uint32_t *const total = cluster.map_shared_rank(sh.total[pass], 0);
+      for (int i = tid; i < kBins; i += kSelThreads)
+        if (sh.hist[i]) atomicAdd(total + i, sh.hist[i]);
       cluster.sync();
       // the cluster's counts of this thread's two bins, from the top bin down
       const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-      uint32_t c1 = 0, c0 = 0;
-#pragma unroll 8
-      for (int q = 0; q < ranks; ++q) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(sh.hist, q) + b0);
-        c0 += v.x, c1 += v.y;
-      }
-      uint32_t inc = c0 + c1;  // inclusive sum over the threads before
+      const uint2 c = *reinterpret_cast<const uint2 *>(total + b0);
+      uint32_t inc = c.x + c.y;  // inclusive sum over the threads before
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
         const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
@@ -109,15 +142,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
       }
       if (lane == 31) sh.warp_sum[warp] = inc;
       __syncthreads();
-      uint32_t before = 0;
-      for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-      const uint32_t up1 = before + inc - c0 - c1, up0 = up1 + c1;  // candidates above each bin
-      if (up1 < need && need <= up1 + c1) sh.bin = b1, sh.above = up1, sh.in_bin = c1;
-      if (up0 < need && need <= up0 + c0) sh.bin = b0, sh.above = up0, sh.in_bin = c0;
-      cluster.sync();  // (also before the histograms are cleared)
+      const uint32_t up1 = sum_before(sh.warp_sum, warp, lane) + inc - c.x - c.y;  // candidates above each bin
+      const uint32_t up0 = up1 + c.y;
+      if (up1 < need && need <= up1 + c.y) sh.bin = b1, sh.above = up1, sh.in_bin = c.y;
+      if (up0 < need && need <= up0 + c.x) sh.bin = b0, sh.above = up0, sh.in_bin = c.x;
+      __syncthreads();
       need -= sh.above;
       prefix = prefix << bits | sh.bin;
-      if (shift == 0) {
+      if (pass == 2) {
         T = prefix, ties = need;
         break;
       }
@@ -125,7 +157,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
         T = (prefix << shift) - 1, ties = 0;
         break;
       }
-      __syncthreads();
     }
   }
 
@@ -140,19 +171,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   }
   if (lane == 0) sh.gt[warp] = gt, sh.eq[warp] = eq;
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 0) {  // the block's counts, to every rank
     const uint32_t g = __reduce_add_sync(0xffffffffu, sh.gt[lane]);
     const uint32_t e = __reduce_add_sync(0xffffffffu, sh.eq[lane]);
-    if (lane == 0) sh.all_gt = g, sh.all_eq = e;
+    if (lane < ranks) {
+      *cluster.map_shared_rank(&sh.rank_gt[rank], lane) = g;
+      *cluster.map_shared_rank(&sh.rank_eq[rank], lane) = e;
+    }
   }
-  cluster.sync();
-  uint32_t gt_at = 0, eq_at = 0;  // before this warp's run
-  for (int q = 0; q < rank; ++q) {
-    gt_at += *cluster.map_shared_rank(&sh.all_gt, q);
-    eq_at += *cluster.map_shared_rank(&sh.all_eq, q);
-  }
-  cluster.sync();  // no block leaves while another reads its counts
-  for (int w = 0; w < warp; ++w) gt_at += sh.gt[w], eq_at += sh.eq[w];
+  cluster.sync();  // (the last access to another block's shared memory lies before it)
+  uint32_t gt_at = sum_before(sh.gt, warp, lane), eq_at = sum_before(sh.eq, warp, lane);
+  for (int q = 0; q < rank; ++q) gt_at += sh.rank_gt[q], eq_at += sh.rank_eq[q];
   const uint32_t below = (1u << lane) - 1;
   for (int i = r0 + lane; i < r1 + lane; i += 32) {
     const uint32_t k = i < r1 ? key(i) : 0;
