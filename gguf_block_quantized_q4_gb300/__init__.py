@@ -409,20 +409,24 @@ class _RopeStruct(ctypes.Structure):  # mq_rope
                 ("pairs", ctypes.c_int), ("n_axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 128)]
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+_IO = {}  # torch dtype -> type code of activations
+_torch = _raw_current_stream = None
 
 
-def _io(t):
-    """The C type code of an activation tensor."""
-    code = _IO.get(str(t.dtype))
-    _need(code is not None and t.is_cuda, f"a CUDA tensor of f32, f16 or bf16 is required, got "
-          f"{t.dtype} on {t.device}")
-    return code
+def _torch_setup():
+    """What the calls below need of torch, looked up once."""
+    global _torch, _raw_current_stream
+    import torch
+    _IO.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    # the current stream's handle without a Stream object (2.8 us less per call)
+    _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
 
 
-_IO = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+def _refuse(what):
+    raise ValueError(what)
 
 
 class KVCache:
@@ -433,33 +437,39 @@ class KVCache:
     larger outer strides, the same in rows for all of them."""
 
     def __init__(self, kind, k, v, k_scale=None, v_scale=None, sums=None, layout="hnd"):
-        _need(layout in ("hnd", "nhd"), f"layout {layout!r} is neither 'hnd' nor 'nhd'")
-        want = {F16: "torch.float16", BF16: "torch.bfloat16", Q8_0: "torch.int8"}.get(kind)
-        _need(want is not None, f"cache type {kind} is not F16, BF16 or Q8_0")
-        _need(k.dim() == 4 and k.shape == v.shape, "k and v are [page][...][...][head_dim]")
+        torch = _torch or _torch_setup()
+        if layout not in ("hnd", "nhd"):
+            _refuse(f"layout {layout!r} is neither 'hnd' nor 'nhd'")
+        want = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8}.get(kind)
+        if want is None:
+            _refuse(f"cache type {kind} is not F16, BF16 or Q8_0")
+        if k.dim() != 4 or k.shape != v.shape:
+            _refuse("k and v are [page][...][...][head_dim]")
         d = k.shape[3]
         planes = [("k", k, want, d), ("v", v, want, d)]
         if kind == Q8_0:
-            _need(k_scale is not None and v_scale is not None, "a Q8_0 cache needs its scales")
-            planes += [("k_scale", k_scale, "torch.float16", d // 32),
-                       ("v_scale", v_scale, "torch.float16", d // 32)]
+            if k_scale is None or v_scale is None:
+                _refuse("a Q8_0 cache needs its scales")
+            planes += [("k_scale", k_scale, torch.float16, d // 32),
+                       ("v_scale", v_scale, torch.float16, d // 32)]
         if sums is not None:
-            planes.append(("sums", sums, "torch.float32", 1))
+            planes.append(("sums", sums, torch.float32, 1))
         # strides in rows (that of an axis of one element says nothing)
         rows = [k.stride(i) // max(d, 1) if k.shape[i] > 1 else 1 for i in range(3)]
         for name, t, dtype, width in planes:
-            _need(t.is_cuda and str(t.dtype) == dtype, f"{name} must be a CUDA tensor of {dtype}")
-            _need(tuple(t.shape[:3]) == tuple(k.shape[:3]) and
-                  (t.dim() == 3 if name == "sums" else t.dim() == 4 and t.shape[3] == width),
-                  f"{name} has shape {tuple(t.shape)}")
-            _need(all(t.shape[i] == 1 or t.stride(i) == rows[i] * width for i in range(3)) and
-                  (t.dim() == 3 or width == 1 or t.stride(3) == 1),
-                  f"{name}: rows are not contiguous, or its strides differ from k's")
+            if not t.is_cuda or t.dtype != dtype:
+                _refuse(f"{name} must be a CUDA tensor of {dtype}")
+            if t.shape[:3] != k.shape[:3] or t.shape[3:] != (() if name == "sums" else (width,)):
+                _refuse(f"{name} has shape {tuple(t.shape)}")
+            if any(t.shape[i] != 1 and t.stride(i) != rows[i] * width for i in range(3)) or (
+                    t.dim() == 4 and width > 1 and t.stride(3) != 1):
+                _refuse(f"{name}: rows are not contiguous, or its strides differ from k's")
         head, slot = (1, 2) if layout == "hnd" else (2, 1)
         self.kind, self.k, self.v, self.k_scale, self.v_scale = kind, k, v, k_scale, v_scale
         self.sums, self.layout = sums, layout
         self.n_pages, self.n_kv_heads, self.page_size = k.shape[0], k.shape[head], k.shape[slot]
-        self.head_dim = d
+        self.head_dim, self.device = d, k.device
+        self._device_index = k.device.index
 
         def ptr(t):
             return None if t is None else t.data_ptr()
@@ -474,7 +484,8 @@ def kv_cache(kind, n_pages, page_size, n_kv_heads, head_dim, sums=False, layout=
              device="cuda") -> KVCache:
     """A KVCache over new zeroed planes."""
     import torch
-    _need(kind in (F16, BF16, Q8_0), f"cache type {kind} is not F16, BF16 or Q8_0")
+    if kind not in (F16, BF16, Q8_0):
+        _refuse(f"cache type {kind} is not F16, BF16 or Q8_0")
     outer = ((n_pages, n_kv_heads, page_size) if layout == "hnd"
              else (n_pages, page_size, n_kv_heads))
     dtype = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8}[kind]
@@ -517,24 +528,18 @@ class Rope:
     (i, i + rot_dim/2)."""
 
     def __init__(self, table, axis=None, pairs=False):
-        _need(table.dim() == 3 and table.shape[2] == 2 and table.is_contiguous() and table.is_cuda
-              and str(table.dtype) == "torch.float32",
-              "table must be a contiguous CUDA f32 tensor [max_pos][rot_dim/2][2]")
+        torch = _torch or _torch_setup()
+        if (table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous()
+                or not table.is_cuda or table.dtype != torch.float32):
+            _refuse("table must be a contiguous CUDA f32 tensor [max_pos][rot_dim/2][2]")
         half = table.shape[1]
-        axis = [0] * half if axis is None else [int(a) for a in axis]
-        _need(len(axis) == half and half <= 128 and all(0 <= a < 4 for a in axis),
-              "axis names one of up to 4 axes for each of at most 128 pairs")
-        self.table, self.axis, self.n_axes = table, axis, max(axis, default=0) + 1
-        self._c = _RopeStruct(table.data_ptr(), table.shape[0], 2 * half, int(pairs), self.n_axes,
-                              (ctypes.c_uint8 * 128)(*axis))
+        axis = bytes(half) if axis is None else bytes(axis)  # (refuses what is no small integer)
+        if len(axis) != half or half > 128 or max(axis, default=0) > 3:
+            _refuse("axis names one of up to 4 axes for each of at most 128 pairs")
+        self.table, self.axis, self.n_axes = table, list(axis), max(axis, default=0) + 1
+        self._c = _RopeStruct(table.data_ptr(), table.shape[0], 2 * half, int(pairs), self.n_axes)
+        ctypes.memmove(self._c.axis, axis, half)
         self._ref = ctypes.addressof(self._c)
-
-
-def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
 
 
 def rope_store(cache: KVCache, rope: Rope, qkv, pos, slot, n_heads, bias=None, q=None,
@@ -542,42 +547,53 @@ def rope_store(cache: KVCache, rope: Rope, qkv, pos, slot, n_heads, bias=None, q
     """Rotate and store T tokens: qkv [T][(n_heads + 2 n_kv_heads) head_dim] (f32, f16 or bf16;
     rows may be strided), pos int32 [n_axes][T] (or [T] for one axis), slot int64 [T].  Returns
     the rotated queries [T][n_heads][head_dim]."""
-    import torch
+    torch = _torch or _torch_setup()
     T, width = qkv.shape
-    io = _io(qkv)
-    _need(width == (n_heads + 2 * cache.n_kv_heads) * cache.head_dim and
-          (qkv.stride(1) == 1 or T == 0), f"qkv has shape {tuple(qkv.shape)}")
-    _need(pos.dtype == torch.int32 and pos.numel() >= rope.n_axes * T and pos.shape[-1] == T and
-          pos.is_contiguous(), "pos must be contiguous int32 [n_axes][T]")
-    _need(slot.dtype == torch.int64 and slot.shape == (T,) and slot.is_contiguous(),
-          "slot must be contiguous int64 [T]")
-    if bias is not None:
-        _need(bias.dtype == torch.float32 and bias.shape == (width,) and bias.is_contiguous(),
-              "bias must be contiguous f32, one per column of qkv")
+    d = cache.head_dim
+    io = _IO.get(qkv.dtype)
+    if io is None or not qkv.is_cuda:
+        _refuse(f"qkv must be a CUDA tensor of f32, f16 or bf16, not {qkv.dtype}")
+    if width != (n_heads + 2 * cache.n_kv_heads) * d or qkv.stride(1) != 1:
+        _refuse(f"qkv has shape {tuple(qkv.shape)}, strides {qkv.stride()}")
+    if (pos.dtype != torch.int32 or pos.numel() < rope.n_axes * T or pos.shape[-1] != T
+            or not pos.is_contiguous()):
+        _refuse("pos must be contiguous int32 [n_axes][T]")
+    if slot.dtype != torch.int64 or slot.shape != (T,) or not slot.is_contiguous():
+        _refuse("slot must be contiguous int64 [T]")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (width,)
+                             or not bias.is_contiguous()):
+        _refuse("bias must be contiguous f32, one per column of qkv")
     if q is None:
-        q = torch.empty((T, n_heads, cache.head_dim), dtype=qkv.dtype, device=qkv.device)
-    else:
-        _need(q.dtype == qkv.dtype and q.is_contiguous() and
-              q.numel() == T * n_heads * cache.head_dim, "q must be contiguous, of qkv's type")
-    _check(lib().mq_rope_store(cache._ref, rope._ref, io, qkv.data_ptr(),
-                               qkv.stride(0) if T > 1 else width,
-                               None if bias is None else bias.data_ptr(), pos.data_ptr(),
-                               slot.data_ptr(), q.data_ptr(), T, n_heads, _raw_stream(stream)))
+        q = qkv.new_empty((T, n_heads, d))
+    elif q.dtype != qkv.dtype or q.numel() != T * n_heads * d or not q.is_contiguous():
+        _refuse("q must be contiguous, of qkv's type")
+    status = lib().mq_rope_store(
+        cache._ref, rope._ref, io, qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
+        None if bias is None else bias.data_ptr(), pos.data_ptr(), slot.data_ptr(), q.data_ptr(),
+        T, n_heads, _raw_current_stream(cache._device_index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return q
 
 
+ATTN_WS_ZERO = 4096  # bytes at a workspace's start that must be zero before its first call
+
+
 def attn_workspace(cache: KVCache, n_seqs, n_heads, max_len, track=False):
-    """A zeroed workspace for attn_decode calls of up to this size."""
+    """A workspace for attn_decode calls of up to this size."""
     import torch
     n = lib().mq_attn_workspace_bytes(cache._ref, n_seqs, n_heads, max_len, int(bool(track)))
     if n == 0:
         raise MQError(STATUS.index("MQ_ERR_ARG"), lib().mq_last_error().decode(errors="replace"))
-    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    ws[:ATTN_WS_ZERO].zero_()
+    return ws
 
 
-def _check_pages(name, pages, n_seqs):
-    _need(str(pages.dtype) == "torch.int32" and pages.dim() == 2 and pages.shape[0] == n_seqs and
-          (pages.stride(1) == 1 or pages.shape[1] == 1), f"{name} must be int32 [S][pages]")
+def _pages_ld(name, pages, n_seqs, int32):
+    if (pages.dtype != int32 or pages.dim() != 2 or pages.shape[0] != n_seqs
+            or (pages.stride(1) != 1 and pages.shape[1] != 1)):
+        _refuse(f"{name} must be int32 [S][pages]")
     return pages.stride(0) if n_seqs > 1 else max(pages.shape[1], 1)
 
 
@@ -587,27 +603,32 @@ def attn_decode(cache: KVCache, q, pages, lens, max_len, scale=None, window=0, t
     pages int32 [S][max pages], lens int32 [S] (at most max_len).  scale defaults to
     head_dim ** -0.5.  ws: a workspace kept from attn_workspace (else one is made for the
     call).  Returns o, of q's shape and type."""
-    import torch
+    torch = _torch or _torch_setup()
     S, n_heads, d = q.shape
-    io = _io(q)
-    _need(d == cache.head_dim and q.is_contiguous(), f"q has shape {tuple(q.shape)} or strides")
-    pages_ld = _check_pages("pages", pages, S)
-    _need(lens.dtype == torch.int32 and lens.shape == (S,) and lens.is_contiguous(),
-          "lens must be contiguous int32 [S]")
-    _need(max_len <= pages.shape[1] * cache.page_size,
-          f"max_len={max_len} is more than {pages.shape[1]} pages hold")
-    _need(not track or cache.sums is not None, "the cache keeps no weight sums")
+    io = _IO.get(q.dtype)
+    if io is None or not q.is_cuda or d != cache.head_dim or not q.is_contiguous():
+        _refuse(f"q must be a contiguous CUDA tensor [S][n_heads][{cache.head_dim}] of f32, f16 "
+                f"or bf16, not {q.dtype} {tuple(q.shape)}")
+    pages_ld = _pages_ld("pages", pages, S, torch.int32)
+    if lens.dtype != torch.int32 or lens.shape != (S,) or not lens.is_contiguous():
+        _refuse("lens must be contiguous int32 [S]")
+    if max_len > pages.shape[1] * cache.page_size:
+        _refuse(f"max_len={max_len} is more than {pages.shape[1]} pages hold")
+    if track and cache.sums is None:
+        _refuse("the cache keeps no weight sums")
     if ws is None:
         ws = attn_workspace(cache, S, n_heads, max_len, track)
     if o is None:
-        o = torch.empty_like(q)
-    else:
-        _need(o.dtype == q.dtype and o.shape == q.shape and o.is_contiguous(),
-              "o must be contiguous, of q's shape and type")
-    _check(lib().mq_attn_decode(cache._ref, io, q.data_ptr(), o.data_ptr(), pages.data_ptr(),
-                                pages_ld, lens.data_ptr(), S, n_heads, max_len,
-                                d ** -0.5 if scale is None else scale, window, int(bool(track)),
-                                ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+        o = q.new_empty(q.shape)
+    elif o.dtype != q.dtype or o.shape != q.shape or not o.is_contiguous():
+        _refuse("o must be contiguous, of q's shape and type")
+    status = lib().mq_attn_decode(
+        cache._ref, io, q.data_ptr(), o.data_ptr(), pages.data_ptr(), pages_ld, lens.data_ptr(), S,
+        n_heads, max_len, d ** -0.5 if scale is None else scale, window, 1 if track else 0,
+        ws.data_ptr(), ws.numel(),
+        _raw_current_stream(cache._device_index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return o
 
 
@@ -615,29 +636,33 @@ def kv_evict(cache: KVCache, pages, lens, max_len, new_pages, keep, sink=0, rece
              new_lens=None, stream=None):
     """Copy the rows that stay (the first sink, the last recent and the heaviest of the rest, keep
     in all) to new_pages.  Returns (kept int32 [S][n_kv_heads][keep], new_lens int32 [S])."""
-    import torch
+    torch = _torch or _torch_setup()
     S = lens.shape[0]
-    pages_ld = _check_pages("pages", pages, S)
-    new_ld = _check_pages("new_pages", new_pages, S)
-    _need(lens.dtype == torch.int32 and lens.dim() == 1 and lens.is_contiguous(),
-          "lens must be contiguous int32 [S]")
-    _need(max_len <= pages.shape[1] * cache.page_size and
-          keep <= new_pages.shape[1] * cache.page_size,
-          f"max_len={max_len} or keep={keep} is more than the pages hold")
-    _need(cache.sums is not None, "the cache keeps no weight sums")
+    pages_ld = _pages_ld("pages", pages, S, torch.int32)
+    new_ld = _pages_ld("new_pages", new_pages, S, torch.int32)
+    if lens.dtype != torch.int32 or lens.dim() != 1 or not lens.is_contiguous():
+        _refuse("lens must be contiguous int32 [S]")
+    if (max_len > pages.shape[1] * cache.page_size
+            or keep > new_pages.shape[1] * cache.page_size):
+        _refuse(f"max_len={max_len} or keep={keep} is more than the pages hold")
+    if cache.sums is None:
+        _refuse("the cache keeps no weight sums")
     if kept is None:
-        kept = torch.empty((S, cache.n_kv_heads, keep), dtype=torch.int32, device=lens.device)
-    else:
-        _need(kept.dtype == torch.int32 and kept.is_contiguous() and
-              kept.numel() == S * cache.n_kv_heads * keep, "kept must be int32 [S][heads][keep]")
+        kept = lens.new_empty((S, cache.n_kv_heads, keep))
+    elif (kept.dtype != torch.int32 or kept.numel() != S * cache.n_kv_heads * keep
+          or not kept.is_contiguous()):
+        _refuse("kept must be contiguous int32 [S][n_kv_heads][keep]")
     if new_lens is None:
         new_lens = torch.empty_like(lens)
-    else:
-        _need(new_lens.dtype == torch.int32 and new_lens.shape == lens.shape and
-              new_lens.is_contiguous(), "new_lens must be contiguous int32 [S]")
-    _check(lib().mq_kv_evict(cache._ref, pages.data_ptr(), pages_ld, lens.data_ptr(), S, max_len,
-                             new_pages.data_ptr(), new_ld, keep, sink, recent, kept.data_ptr(),
-                             new_lens.data_ptr(), _raw_stream(stream)))
+    elif (new_lens.dtype != torch.int32 or new_lens.shape != lens.shape
+          or not new_lens.is_contiguous()):
+        _refuse("new_lens must be contiguous int32 [S]")
+    status = lib().mq_kv_evict(
+        cache._ref, pages.data_ptr(), pages_ld, lens.data_ptr(), S, max_len, new_pages.data_ptr(),
+        new_ld, keep, sink, recent, kept.data_ptr(), new_lens.data_ptr(),
+        _raw_current_stream(cache._device_index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return kept, new_lens
 
 

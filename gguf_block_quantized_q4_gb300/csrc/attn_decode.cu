@@ -42,7 +42,7 @@
 namespace mq {
 namespace {
 
-constexpr int kMaxParts = 1024;     // thread blocks with work (counters in the workspace)
+constexpr int kMaxParts = MQ_ATTN_WS_ZERO / 4;  // thread blocks with work (a counter each)
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 

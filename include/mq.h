@@ -393,9 +393,10 @@ mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope, mq_type i
 #define MQ_ATTN_TRACK 1u
 
 /* mq_attn_workspace_bytes -- size of mq_attn_decode's workspace for up to S sequences of up to
- * max_len cached tokens (0 for arguments mq_attn_decode would refuse).  Zero it once before its
- * first call (a count in it must start at zero; every call leaves it so).  A workspace serves
- * calls of any shape that fits, one at a time. */
+ * max_len cached tokens (0 for arguments mq_attn_decode would refuse).  Its first
+ * MQ_ATTN_WS_ZERO bytes must be zero before its first call (counts; every call leaves them zero).
+ * A workspace serves calls of any shape that fits, one at a time. */
+#define MQ_ATTN_WS_ZERO 4096
 size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads, int64_t max_len,
                                uint32_t flags);
 

@@ -130,6 +130,11 @@ def test_structures_match_the_header():
                                f).offset for t, f in fields]
 
 
+def test_workspace_constant_matches_the_header():
+    src = open(os.path.join(ROOT, "include", "mq.h")).read()
+    assert f"#define MQ_ATTN_WS_ZERO {mq.ATTN_WS_ZERO}\n" in src
+
+
 def test_axes_of_sections():
     assert mq.rope_axes([2, 1, 1]) == [0, 0, 1, 2]
     assert mq.rope_axes([3, 1, 2], weave=True) == [0, 1, 2, 0, 2, 0]
