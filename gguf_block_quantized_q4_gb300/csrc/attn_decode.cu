@@ -43,13 +43,12 @@ namespace mq {
 namespace {
 
 constexpr int kMaxParts = MQ_ATTN_WS_ZERO / 4;  // thread blocks with work (a counter each)
-constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // ---- device helpers ---------------------------------------------------------------------
-// 16 bytes to shared memory; zeros, and no read, where !on.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+// 16 bytes to shared memory, of which `size` (16 or 0) are read and the others zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, uint32_t size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
@@ -86,6 +85,14 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = a b + c in f16 operands.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float4 c) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z), "f"(c.w));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -120,7 +127,7 @@ __device__ __forceinline__ void split2(float lo, float hi, uint32_t (&part)[N]) 
     lo -= b.x, hi -= b.y;
   }
 }
-// Two int8 (the bytes that SEL picks) as f16x2: 1024 + (v + 128) by bits, less 1152.
+// Two int8 (the bytes of v ^ 0x80 that SEL picks) as f16x2: 1024 + (v + 128) by bits, less 1152.
 template <uint32_t SEL>
 __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
   uint32_t u = __byte_perm(biased, 0x64646464u, SEL);
@@ -148,9 +155,11 @@ struct Shape {
   // two that V's were divided by
   static constexpr int kScales = kQ8 ? (2 * kNG * kKeys + 4) * 4 : 0;
   static constexpr int kLdO = D + 4;
+  // the query's parts as operand words; Q8_0: and -128 times its block sums as accumulators
   static constexpr int kQuery = kParts * NT * kNG * 32 * 16;
+  static constexpr int kSums = kQ8 ? NT * kNG * 4 * 16 : 0;
   static constexpr int smem(int warps, int stages) {
-    return warps * (stages * (kStage + kScales) + kRows * (kLdO + 2) * 4) + kQuery + kRows * 4 + 16;
+    return warps * (stages * (kStage + kScales) + kRows * (kLdO + 2) * 4) + kQuery + kSums + kRows * 4 + 16;
   }
   static constexpr int kWarps = smem(8, 2) <= kSmemMax ? 8 : smem(6, 2) <= kSmemMax ? 6 : 4;
   static constexpr int kStages = smem(kWarps, 3) <= kSmemMax ? 3 : 2;
@@ -254,11 +263,13 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kThreads, 1)
 attn_decode_kernel(const __grid_constant__ Params p) {
   using C = Shape<TYPE, D, NT>;
   constexpr int NG = C::kNG, MT = C::kMT, KS = D / 16;
+  constexpr uint32_t kAll = MT == 2 ? 0xffffffffu : 0xffffu;  // all keys of a warp's tile
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t *const ring = smem;                                               // [warp][stage][K, V]
   float *const scales = reinterpret_cast<float *>(ring + C::kWarps * C::kStages * C::kStage);
   uint4 *const sq = reinterpret_cast<uint4 *>(scales + C::kWarps * C::kStages * (C::kScales / 4));
-  float *const so = reinterpret_cast<float *>(sq) + C::kQuery / 4;          // [warp][row][kLdO]
+  float4 *const ssum = reinterpret_cast<float4 *>(sq + C::kQuery / 16);     // [8 rows][block][t]
+  float *const so = reinterpret_cast<float *>(ssum + C::kSums / 16);        // [warp][row][kLdO]
   float *const sm = so + C::kWarps * C::kRows * C::kLdO, *const sl = sm + C::kWarps * C::kRows;
   float *const sfac = sl + C::kWarps * C::kRows;  // per row: scale * log2 e * 2^-e
   int *const slast = reinterpret_cast<int *>(sfac + C::kRows);
@@ -339,7 +350,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     const int e = top == 0 || top >= 0x7c00u ? 126 : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
     const float down = lane < 16 ? 1.f : __uint_as_float(uint32_t(253 - e) << 23);
     float *const to = scale0 + pend_stage * (C::kScales / 4);
-    if (lane == 0) to[2 * NG * C::kKeys] = __uint_as_float(uint32_t(e + 1) << 23);  // 2^(e - 126)
+    if (lane == 0)  // 2^(e - 126), and its inverse
+      *reinterpret_cast<float2 *>(to + 2 * NG * C::kKeys) =
+          make_float2(__uint_as_float(uint32_t(e + 1) << 23), __uint_as_float(uint32_t(253 - e) << 23));
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -349,26 +362,29 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       }
   };
   auto issue = [&](int stage) {  // the tile looked up last, into a stage; then the next look-up
-    uint32_t row = kNoRow;
+    uint32_t row = 0;
+    bool on = there;
     if (there) {
-      if (page >= 0 && page < a.c.n_pages)
+      if (page >= 0 && page < a.c.n_pages) {
         row = (uint32_t)(page * a.c.page_stride + page_head * a.c.head_stride + slot * a.c.slot_stride);
-      else
+      } else {
         index_error(a.status, kIdxAttnPage, page);
+        on = false;
+      }
     }
+    const uint32_t valid = __ballot_sync(0xffffffffu, on);
 #pragma unroll
     for (int i = 0; i + 1 < C::kStages; ++i) valid_bits[i] = valid_bits[i + 1];
-    valid_bits[C::kStages - 1] = __ballot_sync(0xffffffffu, row != kNoRow);
+    valid_bits[C::kStages - 1] = valid;
     constexpr int CH = C::kRow / 16;  // 16-byte chunks of a row
     const uint32_t dst = ring0 + stage * C::kStage;
 #pragma unroll
     for (int i = 0; i < C::kKeys * CH / 32; ++i) {
       const int key = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-      const uint32_t r = __shfl_sync(0xffffffffu, row, key);
-      const bool on = r != kNoRow;
-      const size_t off = on ? size_t(r) * C::kRow + ch * 16 : 0;
-      copy16(dst + key * C::kStride + ch * 16, a.c.k + off, on);
-      copy16(dst + (C::kKeys + key) * C::kStride + ch * 16, a.c.v + off, on);
+      const uint64_t off = uint64_t(__shfl_sync(0xffffffffu, row, key)) * C::kRow;
+      const uint32_t size = (valid >> key & 1) * 16;
+      copy16(dst + key * C::kStride + ch * 16, a.c.k + ch * 16 + off, size);
+      copy16(dst + (C::kKeys + key) * C::kStride + ch * 16, a.c.v + ch * 16 + off, size);
     }
     copies_commit();
     if (C::kQ8) {
@@ -376,8 +392,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * m + (lane & 15));
-        const __half *q = (lane < 16 ? a.c.ks : a.c.vs) + size_t(r == kNoRow ? 0 : r) * NG;
-        const bool on = r != kNoRow;
+        const __half *q = (lane < 16 ? a.c.ks : a.c.vs) + uint64_t(r) * NG;
+        const bool on = valid >> (16 * m + (lane & 15)) & 1;
         if constexpr (NG % 4 == 0) {
 #pragma unroll
           for (int j = 0; j < SW; j += 2) {
@@ -445,11 +461,30 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         if (top > 0.f && top < INFINITY) e = min(max(141 - (int)(__float_as_uint(top) >> 23), -100), 100);
       }
       const float up = __uint_as_float(uint32_t(127 + e) << 23);
-      if (lane == 0) sfac[r] = p.scale_log2 * __uint_as_float(uint32_t(127 - e) << 23);
+      // (Q8_0 keys enter the product as 2^-24 (v + 128), see below)
+      if (lane == 0)
+        sfac[r] = p.scale_log2 * __uint_as_float(uint32_t(127 - e) << 23) * (C::kQ8 ? 0x1p24f : 1.f);
       if (lane < D / 8) {
         uint32_t w[4][C::kParts];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split2<C::kBf>(x[2 * i] * up, x[2 * i + 1] * up, w[i]);
+        if (C::kQ8) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < C::kParts; ++k) {
+              const float2 v = unpack2<C::kBf>(w[i][k]);
+              sum += v.x + v.y;
+            }
+          constexpr unsigned mask = D / 8 == 32 ? 0xffffffffu : (1u << D / 8 % 32) - 1;
+          sum += __shfl_xor_sync(mask, sum, 1);
+          sum += __shfl_xor_sync(mask, sum, 2);
+          if ((lane & 3) == 0) {  // rows r & 6 and r | 1 of the accumulator's elements 0, 2 and 1, 3
+            float *const to = reinterpret_cast<float *>(ssum + ((r >> 3) * NG + (lane >> 2)) * 4 + (r >> 1 & 3));
+            to[r & 1] = to[(r & 1) + 2] = sum * (-128 * 0x1p-24f);
+          }
+        }
         // the lane's 8 dims are half `lane & 1` of step lane >> 1
         uint32_t *q = reinterpret_cast<uint32_t *>(sq + ((r >> 3) * NG + (lane >> 2)) * 32 + (r & 7) * 4);
         const int step = lane >> 1 & 1, half = lane & 1;
@@ -470,7 +505,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) fac[n][0] = sfac[8 * n + 2 * t], fac[n][1] = sfac[8 * n + 2 * t + 1];
 
-    float o[KS][NT][4] = {}, mx[NT][2], ls[NT][2] = {};
+    float o[KS][NT][4] = {}, mx[NT][2], ls[NT][2] = {}, unit = 1.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
 
@@ -495,23 +530,25 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             const uint32_t at_k = base + k_lane + 16 * m * C::kStride;
             uint32_t ka[2][4];  // two steps of 16 dims
             if (C::kQ8) {
+              // a byte of v ^ 0x80 alone in 16 bits is the f16 (subnormal) 2^-24 (v + 128); the
+              // accumulators start at -128 * 2^-24 times the block's sum of the query
               uint32_t x[4];  // keys g (0, 2) and g + 8 (1, 3), chunks 0 and 1
               ldmatrix4<false>(x, at_k + j * 32);
 #pragma unroll
               for (int st = 0; st < 2; ++st) {
                 const uint32_t xa = x[2 * st] ^ 0x80808080u, xb = x[2 * st + 1] ^ 0x80808080u;
-                ka[st][0] = int8_f16<0x4140>(xa), ka[st][1] = int8_f16<0x4140>(xb);
-                ka[st][2] = int8_f16<0x4342>(xa), ka[st][3] = int8_f16<0x4342>(xb);
+                ka[st][0] = __byte_perm(xa, 0, 0x4140), ka[st][1] = __byte_perm(xb, 0, 0x4140);
+                ka[st][2] = __byte_perm(xa, 0, 0x4342), ka[st][3] = __byte_perm(xb, 0, 0x4342);
               }
               const float da = sc[j * C::kKeys + 16 * m + g], db = sc[j * C::kKeys + 16 * m + g + 8];
 #pragma unroll
               for (int n = 0; n < NT; ++n) {  // the block's sum times the scales of keys g, g + 8
-                float c[4] = {};
-#pragma unroll
-                for (int k = 0; k < C::kParts; ++k) {
-                  mma<C::kBf>(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[k][n].x, b[k][n].y);
-                  mma<C::kBf>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[k][n].z, b[k][n].w);
-                }
+                float c[4];
+                mma_from(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[0][n].x, b[0][n].y,
+                         ssum[(n * NG + j) * 4 + t]);
+                mma<false>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[0][n].z, b[0][n].w);
+                mma<false>(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[1][n].x, b[1][n].y);
+                mma<false>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[1][n].z, b[1][n].w);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) c0[m][n][w] = fmaf(c[w], w < 2 ? da : db, c0[m][n][w]);
               }
@@ -541,13 +578,20 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) s[m][n][w] *= fac[n][w & 1];
+        if (here != kAll) {
+#pragma unroll
           for (int m = 0; m < MT; ++m) {
             const bool ga = here >> (16 * m + g) & 1, gb = here >> (16 * m + 8 + g) & 1;
-            s[m][n][0] = ga ? s[m][n][0] * fac[n][0] : -INFINITY;
-            s[m][n][1] = ga ? s[m][n][1] * fac[n][1] : -INFINITY;
-            s[m][n][2] = gb ? s[m][n][2] * fac[n][0] : -INFINITY;
-            s[m][n][3] = gb ? s[m][n][3] * fac[n][1] : -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if (!(w < 2 ? ga : gb)) s[m][n][w] = -INFINITY;
           }
+        }
         if (p.logits) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
@@ -605,7 +649,12 @@ attn_decode_kernel(const __grid_constant__ Params p) {
               }
             }
         // ---- O^T = O^T alpha + V^T P^T ----
-        const float unit = C::kQ8 ? sc[2 * NG * C::kKeys] : 1.f;
+        if (C::kQ8) {  // o stands in units of the tile's power of two
+          const float2 u = *reinterpret_cast<const float2 *>(sc + 2 * NG * C::kKeys);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) al[n][0] *= unit * u.y, al[n][1] *= unit * u.y;
+          unit = u.x;
+        }
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           float c[2][NT][4] = {};
@@ -649,10 +698,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const float old = o[2 * j + h][n][w] * al[n][w & 1];
-                o[2 * j + h][n][w] = C::kQ8 ? fmaf(c[h][n][w], unit, old) : fmaf(o[2 * j + h][n][w], al[n][w & 1], c[h][n][w]);
-              }
+              for (int w = 0; w < 4; ++w)
+                o[2 * j + h][n][w] = fmaf(o[2 * j + h][n][w], al[n][w & 1], c[h][n][w]);
         }
       }
       __syncwarp();  // the stage has been read
@@ -675,7 +722,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         for (int j = 0; j < KS; ++j)
           if (C::kQ8) {  // dims 16 j + 2g, 2g + 1
             *reinterpret_cast<float2 *>(so + r * C::kLdO + 16 * j + 2 * g) =
-                make_float2(o[j][n][w], o[j][n][w + 2]);
+                make_float2(o[j][n][w] * unit, o[j][n][w + 2] * unit);
           } else {
             so[r * C::kLdO + 16 * j + g] = o[j][n][w];
             so[r * C::kLdO + 16 * j + 8 + g] = o[j][n][w + 2];
