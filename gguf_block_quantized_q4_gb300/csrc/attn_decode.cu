@@ -51,6 +51,12 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, uint32_
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size)
                : "memory");
 }
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t size) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t size) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -136,7 +142,7 @@ __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
   return *reinterpret_cast<uint32_t *>(&r);
 }
 // ---- the shape of a kernel ----------------------------------------------------------------
-constexpr int kSmemMax = 227 * 1024;  // per thread block
+constexpr int kSmemMax = 226 * 1024;  // per thread block (of 227 KB; a little is static)
 
 template <int TYPE, int D, int NT>
 struct Shape {
@@ -150,16 +156,20 @@ struct Shape {
   static constexpr int kRows = 8 * NT;          // query rows of a unit
   // shared memory: the rings, Q8_0 scales of a ring's keys, query parts, the warps' results
   static constexpr int kStride = kRow + 16;     // an odd number of 16-byte steps
-  static constexpr int kStage = 2 * kKeys * kStride;
-  // Q8_0 scales of a stage in binary32, K's then V's, [32-element block][key]; then the power of
-  // two that V's were divided by
-  static constexpr int kScales = kQ8 ? (2 * kNG * kKeys + 4) * 4 : 0;
+  // a stage: K rows, V rows, the page entries of the tile a ring's length ahead, Q8_0 scales as
+  // they are stored (K's keys, V's keys)
+  static constexpr int kEntries = 2 * kKeys * kStride;
+  static constexpr int kRaw = kEntries + kKeys * 4;
+  static constexpr int kScaleRow = (kNG + 1) / 2 * 4;
+  static constexpr int kStage = (kRaw + (kQ8 ? 2 * kKeys * kScaleRow : 0) + 15) / 16 * 16;
+  // the scales of a warp's tile in binary32, K's then V's, [32-element block][key]
+  static constexpr int kScales = kQ8 ? 2 * kNG * kKeys * 4 : 0;
   static constexpr int kLdO = D + 4;
   // the query's parts as operand words; Q8_0: and -128 times its block sums as accumulators
   static constexpr int kQuery = kParts * NT * kNG * 32 * 16;
   static constexpr int kSums = kQ8 ? NT * kNG * 4 * 16 : 0;
   static constexpr int smem(int warps, int stages) {
-    return warps * (stages * (kStage + kScales) + kRows * (kLdO + 2) * 4) + kQuery + kSums + kRows * 4 + 16;
+    return warps * (stages * kStage + kScales + kRows * (kLdO + 2) * 4) + kQuery + kSums + kRows * 4;
   }
   static constexpr int kWarps = smem(8, 2) <= kSmemMax ? 8 : smem(6, 2) <= kSmemMax ? 6 : 4;
   static constexpr int kStages = smem(kWarps, 3) <= kSmemMax ? 3 : 2;
@@ -234,6 +244,76 @@ __device__ __forceinline__ void next_tile(Cursor &c, const Params &p, int tk) {
   } while (c.span.tiles == 0);
 }
 
+// A unit that several blocks share: its first query head's row of q and o, its number, its first
+// and last block, its query rows; whether this block arrived last.
+struct Split {
+  int64_t head0, unit_id, b0, b1;
+  int rows, last;
+};
+
+// Four dims of a query row's output, normalised.
+template <class C>
+__device__ __forceinline__ void finish(const Params &p, int64_t head0, int64_t unit_id, int r, int d,
+                                       int dim, float4 x, float m, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store_io4(p.a.o, p.a.io, (head0 + r) * dim + d,
+            make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+  if (d == 0 && p.stats)
+    p.stats[unit_id * C::kRows + r] = make_float2((m == -INFINITY ? 0.f : m) - C::kBias, inv);
+}
+
+// Counts a block's piece of a shared unit in; true where it is the unit's last.  One thread calls
+// it, after a barrier behind the block's stores: the release covers them (the barrier orders them
+// before it), the acquire what the other blocks stored.
+__device__ __forceinline__ bool arrive(const Params &p, int64_t b0, int64_t b1) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.count + b0) : "memory");
+  const bool last = before == (int)(b1 - b0);
+  if (last) p.count[b0] = 0;
+  return last;
+}
+
+// Joins a shared unit's pieces: a thread sums four dims of a row over the pieces in their order,
+// kJoin pieces with their maxima and sums on their way at a time (a warp per piece, one after the
+// other, took 1.4 us a round; factors shared through shared memory as long).  Out of line: what it
+// keeps in registers is not the tiles' loop's.
+constexpr int kJoin = 20;
+template <class C, int D>
+__device__ __noinline__ void join_pieces(const Params &p, const Split &u) {
+  for (int it = threadIdx.x; it < u.rows * (D / 4); it += C::kThreads) {
+    const int r = it / (D / 4);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    for (int64_t c0 = u.b0; c0 <= u.b1; c0 += kJoin) {
+      float4 y[kJoin];
+      float2 ml[kJoin];
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) {
+        y[i] = make_float4(0.f, 0.f, 0.f, 0.f), ml[i] = make_float2(-INFINITY, 0.f);
+        if (c0 + i <= u.b1) {
+          const int64_t from = ((c0 + i) * 2 + (c0 + i == u.b0)) * C::kRows;
+          ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.piece_ml) + from + r);
+          y[i] = __ldcg(reinterpret_cast<const float4 *>(p.piece_o + from * D) + it);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) top = fmaxf(top, ml[i].x);
+      const float low = top == -INFINITY ? 0.f : top, f0 = exp2_fast(m - low);
+      m = top;
+      l *= f0, x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) {
+        const float f = exp2_fast(ml[i].x - low);
+        l = fmaf(ml[i].y, f, l);
+        x.x = fmaf(y[i].x, f, x.x), x.y = fmaf(y[i].y, f, x.y);
+        x.z = fmaf(y[i].z, f, x.z), x.w = fmaf(y[i].w, f, x.w);
+      }
+    }
+    finish<C>(p, u.head0, u.unit_id, r, 4 * (it % (D / 4)), D, x, m, l);
+  }
+}
+
 // Joins the results that the warps left in shared memory: so[w][row][dim], sm / sl the maxima and
 // sums.  Calls put(row, dim, o, m, l) with four dims of o (not normalised) for the first `rows`.
 template <class C, class Put>
@@ -266,13 +346,14 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kAll = MT == 2 ? 0xffffffffu : 0xffffu;  // all keys of a warp's tile
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t *const ring = smem;                                               // [warp][stage][K, V]
-  float *const scales = reinterpret_cast<float *>(ring + C::kWarps * C::kStages * C::kStage);
-  uint4 *const sq = reinterpret_cast<uint4 *>(scales + C::kWarps * C::kStages * (C::kScales / 4));
+  float *const scales = reinterpret_cast<float *>(ring + C::kWarps * C::kStages * C::kStage);  // [warp]
+  uint4 *const sq = reinterpret_cast<uint4 *>(scales + C::kWarps * (C::kScales / 4));
   float4 *const ssum = reinterpret_cast<float4 *>(sq + C::kQuery / 16);     // [8 rows][block][t]
   float *const so = reinterpret_cast<float *>(ssum + C::kSums / 16);        // [warp][row][kLdO]
   float *const sm = so + C::kWarps * C::kRows * C::kLdO, *const sl = sm + C::kWarps * C::kRows;
   float *const sfac = sl + C::kWarps * C::kRows;  // per row: scale * log2 e * 2^-e
-  int *const slast = reinterpret_cast<int *>(sfac + C::kRows);
+  __shared__ Split split[2];
+  int splits = 0;
   const AttnArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   grid_dependency();
@@ -315,67 +396,44 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   }
 
   // ---- the ring ----
-  // Rows of a tile's keys: lane i holds key i's.  The page entry is read one tile ahead, and looked
-  // at only then.
-  int32_t page = 0;
-  uint32_t slot = 0;
-  int page_head = 0;
-  bool there = false;
-  auto look_up = [&]() {  // at cur
-    const int key = cur.span.lo + cur.tile * C::kTK + warp * C::kKeys + lane;
-    there = cur.left > 0 && lane < C::kKeys && key < cur.span.len;
-    page_head = cur.hk;
-    if (there) {
-      const uint32_t pi = quotient((uint32_t)key, a.c.page);
-      slot = (uint32_t)key - pi * a.c.page.d;
-      page = a.pages[cur.s * a.pages_ld + pi];
-    }
-  };
-  const uint32_t ring0 = smem_addr(ring) + warp * C::kStages * C::kStage;
-  float *const scale0 = scales + warp * C::kStages * (C::kScales / 4);
+  // A tile's rows are found from page entries that were copied into shared memory with the tile a
+  // ring's length before it.  (No load into registers stays on its way while a tile is multiplied:
+  // the few scoreboards of a warp are shared, and an operand's wait became a wait for it.)
+  uint8_t *const my_ring = ring + warp * C::kStages * C::kStage;
+  const uint32_t ring0 = smem_addr(my_ring);
+  float *const sc = scales + warp * (C::kScales / 4);
   uint32_t valid_bits[C::kStages] = {};  // per tile in flight (oldest first): keys that are there
-  // Q8_0 scales of the newest tile, on their way: lane i has key i % 16 (+ 16), of K or V
-  constexpr int SW = (NG + 1) / 2;  // words of a row's scales, two each
-  uint32_t pend[MT][SW];
-  int pend_stage = -1;
-  auto store_scales = [&]() {
-    if (!C::kQ8 || pend_stage < 0) return;
-    uint32_t top = 0;  // the largest of V's (f16 bits of magnitudes order as numbers)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < SW; ++j)
-        if (lane >= 16) top = max(top, max(pend[m][j] & 0x7fffu, pend[m][j] >> 16 & 0x7fffu));
-    top = __reduce_max_sync(0xffffffffu, top);
-    const int e = top == 0 || top >= 0x7c00u ? 126 : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
-    const float down = lane < 16 ? 1.f : __uint_as_float(uint32_t(253 - e) << 23);
-    float *const to = scale0 + pend_stage * (C::kScales / 4);
-    if (lane == 0)  // 2^(e - 126), and its inverse
-      *reinterpret_cast<float2 *>(to + 2 * NG * C::kKeys) =
-          make_float2(__uint_as_float(uint32_t(e + 1) << 23), __uint_as_float(uint32_t(253 - e) << 23));
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        const float2 d = unpack2<false>(pend[m][j / 2]);
-        to[((lane >> 4) * NG + j) * C::kKeys + 16 * m + (lane & 15)] = (j & 1 ? d.y : d.x) * down;
-      }
+  uint32_t odd_bits[C::kStages] = {};    // keys of odd rows (their scales, where NG is odd)
+  struct Place {
+    uint32_t row;  // this lane's key: its row within the page's first
+    bool there;
+  } place[C::kStages];  // per tile looked up (oldest first)
+  auto look_up = [&](Place &to, int32_t *entry) -> const int32_t * {  // at cur; then the next tile
+    const int key = cur.span.lo + cur.tile * C::kTK + warp * C::kKeys + lane;
+    to.there = cur.left > 0 && lane < C::kKeys && key < cur.span.len;
+    const uint32_t pi = quotient((uint32_t)(to.there ? key : 0), a.c.page);
+    to.row = (uint32_t)(cur.hk * a.c.head_stride) +
+             ((uint32_t)key - pi * a.c.page.d) * (uint32_t)a.c.slot_stride;
+    const int32_t *const from = a.pages + cur.s * a.pages_ld + pi;
+    if (entry && lane < C::kKeys) copy4(smem_addr(entry + lane), from, to.there ? 4 : 0);
+    next_tile(cur, p, C::kTK);
+    return from;
   };
-  auto issue = [&](int stage) {  // the tile looked up last, into a stage; then the next look-up
+  auto issue = [&](int stage, Place at, int32_t page) {  // a tile's rows into a stage
     uint32_t row = 0;
-    bool on = there;
-    if (there) {
+    if (at.there) {
       if (page >= 0 && page < a.c.n_pages) {
-        row = (uint32_t)(page * a.c.page_stride + page_head * a.c.head_stride + slot * a.c.slot_stride);
+        row = (uint32_t)page * (uint32_t)a.c.page_stride + at.row;
       } else {
         index_error(a.status, kIdxAttnPage, page);
-        on = false;
+        at.there = false;
       }
     }
-    const uint32_t valid = __ballot_sync(0xffffffffu, on);
+    const uint32_t valid = __ballot_sync(0xffffffffu, at.there);
 #pragma unroll
-    for (int i = 0; i + 1 < C::kStages; ++i) valid_bits[i] = valid_bits[i + 1];
+    for (int i = 0; i + 1 < C::kStages; ++i) valid_bits[i] = valid_bits[i + 1], odd_bits[i] = odd_bits[i + 1];
     valid_bits[C::kStages - 1] = valid;
+    if (NG & 1) odd_bits[C::kStages - 1] = __ballot_sync(0xffffffffu, row & 1);
     constexpr int CH = C::kRow / 16;  // 16-byte chunks of a row
     const uint32_t dst = ring0 + stage * C::kStage;
 #pragma unroll
@@ -386,46 +444,46 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       copy16(dst + key * C::kStride + ch * 16, a.c.k + ch * 16 + off, size);
       copy16(dst + (C::kKeys + key) * C::kStride + ch * 16, a.c.v + ch * 16 + off, size);
     }
-    copies_commit();
-    if (C::kQ8) {
-      store_scales();
+    if (C::kQ8) {  // lane i: key i % 16 (+ 16) of K, or of V
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * m + (lane & 15));
-        const __half *q = (lane < 16 ? a.c.ks : a.c.vs) + uint64_t(r) * NG;
-        const bool on = valid >> (16 * m + (lane & 15)) & 1;
-        if constexpr (NG % 4 == 0) {
-#pragma unroll
-          for (int j = 0; j < SW; j += 2) {
-            uint2 v = make_uint2(0, 0);
-            if (on) v = *reinterpret_cast<const uint2 *>(q + 2 * j);
-            pend[m][j] = v.x, pend[m][j + 1] = v.y;
-          }
+        const int key = 16 * m + (lane & 15);
+        const uint32_t r = __shfl_sync(0xffffffffu, row, key), on = valid >> key & 1;
+        const __half *const from = (lane < 16 ? a.c.ks : a.c.vs) + uint64_t(r) * NG;
+        const uint32_t to = dst + C::kRaw + ((lane >> 4) * C::kKeys + key) * C::kScaleRow;
+        if constexpr (NG == 8) {
+          copy16(to, reinterpret_cast<const uint8_t *>(from), on * 16);
+        } else if constexpr (NG == 4) {
+          copy8(to, from, on * 8);
         } else if constexpr (NG % 2 == 0) {
 #pragma unroll
-          for (int j = 0; j < SW; ++j) pend[m][j] = on ? *reinterpret_cast<const uint32_t *>(q + 2 * j) : 0;
-        } else {  // rows of an odd number of scales are 2-byte aligned
+          for (int j = 0; j < NG / 2; ++j) copy4(to + 4 * j, from + 2 * j, on * 4);
+        } else {  // an odd row starts in the middle of a word; an even one ends there
+          const __half *const word = from - (r & 1);
 #pragma unroll
-          for (int j = 0; j < SW; ++j) {
-            uint32_t x = 0, y = 0;
-            if (on) {
-              x = __half_as_ushort(q[2 * j]);
-              if (2 * j + 1 < NG) y = __half_as_ushort(q[2 * j + 1]);
-            }
-            pend[m][j] = x | y << 16;
-          }
+          for (int j = 0; j < (NG + 1) / 2; ++j)
+            copy4(to + 4 * j, word + 2 * j, on * (2 * j + 2 > NG && !(r & 1) ? 2 : 4));
         }
       }
-      pend_stage = stage;
     }
-    next_tile(cur, p, C::kTK);
-    look_up();
   };
 
   Cursor now = cur;  // the tile being multiplied (its piece's unit)
-  look_up();
+  {
+    // the first tiles: their page entries are read here
+    int32_t first[C::kStages];
 #pragma unroll
-  for (int i = 0; i < C::kStages; ++i) issue(i);
+    for (int i = 0; i < C::kStages; ++i) {
+      const int32_t *const from = look_up(place[i], nullptr);
+      first[i] = place[i].there ? *from : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < C::kStages; ++i) {
+      issue(i, place[i], first[i]);
+      look_up(place[i], reinterpret_cast<int32_t *>(my_ring + i * C::kStage + C::kEntries));
+      copies_commit();
+    }
+  }
   int stage = 0;
 
   // operand addresses of this lane within a stage: matrix lane >> 3, row lane & 7
@@ -514,56 +572,114 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       __syncwarp();
       const uint32_t here = valid_bits[0];
       const uint32_t base = ring0 + stage * C::kStage;
-      const float *const sc = scale0 + stage * (C::kScales / 4);
+      uint8_t *const my_stage = my_ring + stage * C::kStage;
       if (here) {
-        // ---- S^T = K Q^T ----  (c0: the first part of the query, c1: the others)
-        float s[MT][NT][4], c0[MT][NT][4] = {}, c1[MT][NT][4] = {};
+        float tile_unit = 1.f, per_unit = 1.f;  // the power of two of V's scales, and its inverse
+        if (C::kQ8) {  // the tile's scales in binary32, V's scaled to at most 1 by a power of two
+          constexpr int SW = C::kScaleRow / 4;
+          uint32_t w[MT][SW], top = 0;
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          uint4 b[C::kParts][NT];
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t *const from = reinterpret_cast<const uint32_t *>(
+                my_stage + C::kRaw + ((lane >> 4) * C::kKeys + 16 * m + (lane & 15)) * C::kScaleRow);
+#pragma unroll
+            for (int j = 0; j < SW; ++j) w[m][j] = from[j];
+            if ((NG & 1) && odd_bits[0] >> (16 * m + (lane & 15)) & 1) {
+#pragma unroll
+              for (int j = 0; j < SW; ++j) w[m][j] = __funnelshift_r(w[m][j], j + 1 < SW ? w[m][(j + 1) % SW] : 0, 16);
+            }
+            if (NG & 1) w[m][SW - 1] &= 0xffffu;
+#pragma unroll
+            for (int j = 0; j < SW; ++j)  // (f16 bits of magnitudes order as numbers)
+              if (lane >= 16) top = max(top, max(w[m][j] & 0x7fffu, w[m][j] >> 16 & 0x7fffu));
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int e = top == 0 || top >= 0x7c00u
+                            ? 126
+                            : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+          tile_unit = __uint_as_float(uint32_t(e + 1) << 23), per_unit = __uint_as_float(uint32_t(253 - e) << 23);
+          const float f = lane < 16 ? 1.f : per_unit;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+              const float2 d = unpack2<false>(w[m][j / 2]);
+              sc[((lane >> 4) * NG + j) * C::kKeys + 16 * m + (lane & 15)] = (j & 1 ? d.y : d.x) * f;
+            }
+          __syncwarp();
+        }
+        // ---- S^T = K Q^T ----
+        // Two groups of 32 dims at a time, so that (with two 16-key groups for narrow rows) four
+        // chains of products are on their way; f16 and bf16 rows have an accumulator per chain
+        // and part kind (first; others) up to the end.
+        float s[MT][NT][4], acc[2][2][MT][NT][4] = {};
+#pragma unroll
+        for (int j0 = 0; j0 < NG; j0 += 2) {
+          uint4 b[2][C::kParts][NT];
+          uint32_t ka[2][MT][2][4];  // two steps of 16 dims
+          float cq[2][MT][NT][4];    // Q8_0: the blocks' sums
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = j0 + jj;
+            if (j >= NG) continue;
+#pragma unroll
+            for (int k = 0; k < C::kParts; ++k)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) b[jj][k][n] = sq[((k * NT + n) * NG + j) * 32 + lane];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const uint32_t at_k = base + k_lane + 16 * m * C::kStride;
+              if (C::kQ8) {
+                // a byte of v ^ 0x80 alone in 16 bits is the f16 (subnormal) 2^-24 (v + 128); the
+                // accumulators start at -128 * 2^-24 times the block's sum of the query
+                uint32_t x[4];  // keys g (0, 2) and g + 8 (1, 3), chunks 0 and 1
+                ldmatrix4<false>(x, at_k + j * 32);
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                  const uint32_t xa = x[2 * st] ^ 0x80808080u, xb = x[2 * st + 1] ^ 0x80808080u;
+                  ka[jj][m][st][0] = __byte_perm(xa, 0, 0x4140), ka[jj][m][st][1] = __byte_perm(xb, 0, 0x4140);
+                  ka[jj][m][st][2] = __byte_perm(xa, 0, 0x4342), ka[jj][m][st][3] = __byte_perm(xb, 0, 0x4342);
+                }
+              } else {
+                ldmatrix4<false>(ka[jj][m][0], at_k + j * 64);
+                ldmatrix4<false>(ka[jj][m][1], at_k + j * 64 + 32);
+              }
+            }
+          }
 #pragma unroll
           for (int k = 0; k < C::kParts; ++k)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) b[k][n] = sq[((k * NT + n) * NG + j) * 32 + lane];
+            for (int st = 0; st < 2; ++st)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t at_k = base + k_lane + 16 * m * C::kStride;
-            uint32_t ka[2][4];  // two steps of 16 dims
-            if (C::kQ8) {
-              // a byte of v ^ 0x80 alone in 16 bits is the f16 (subnormal) 2^-24 (v + 128); the
-              // accumulators start at -128 * 2^-24 times the block's sum of the query
-              uint32_t x[4];  // keys g (0, 2) and g + 8 (1, 3), chunks 0 and 1
-              ldmatrix4<false>(x, at_k + j * 32);
+              for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-              for (int st = 0; st < 2; ++st) {
-                const uint32_t xa = x[2 * st] ^ 0x80808080u, xb = x[2 * st + 1] ^ 0x80808080u;
-                ka[st][0] = __byte_perm(xa, 0, 0x4140), ka[st][1] = __byte_perm(xb, 0, 0x4140);
-                ka[st][2] = __byte_perm(xa, 0, 0x4342), ka[st][3] = __byte_perm(xb, 0, 0x4342);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) {
+                    if (j0 + jj >= NG) continue;
+                    const uint32_t(&x)[4] = ka[jj][m][st];
+                    const uint32_t b0 = st ? b[jj][k][n].z : b[jj][k][n].x;
+                    const uint32_t b1 = st ? b[jj][k][n].w : b[jj][k][n].y;
+                    if (!C::kQ8)
+                      mma<C::kBf>(acc[jj][k > 0][m][n], x[0], x[1], x[2], x[3], b0, b1);
+                    else if (k == 0 && st == 0)
+                      mma_from(cq[jj][m][n], x[0], x[1], x[2], x[3], b0, b1, ssum[(n * NG + j0 + jj) * 4 + t]);
+                    else
+                      mma<false>(cq[jj][m][n], x[0], x[1], x[2], x[3], b0, b1);
+                  }
+          if (C::kQ8) {  // the blocks' sums times the scales of keys g, g + 8
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                if (j0 + jj >= NG) continue;
+                const float da = sc[(j0 + jj) * C::kKeys + 16 * m + g], db = sc[(j0 + jj) * C::kKeys + 16 * m + g + 8];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int w = 0; w < 4; ++w)
+                    acc[0][0][m][n][w] = fmaf(cq[jj][m][n][w], w < 2 ? da : db, acc[0][0][m][n][w]);
               }
-              const float da = sc[j * C::kKeys + 16 * m + g], db = sc[j * C::kKeys + 16 * m + g + 8];
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {  // the block's sum times the scales of keys g, g + 8
-                float c[4];
-                mma_from(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[0][n].x, b[0][n].y,
-                         ssum[(n * NG + j) * 4 + t]);
-                mma<false>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[0][n].z, b[0][n].w);
-                mma<false>(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[1][n].x, b[1][n].y);
-                mma<false>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[1][n].z, b[1][n].w);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) c0[m][n][w] = fmaf(c[w], w < 2 ? da : db, c0[m][n][w]);
-              }
-            } else {
-              ldmatrix4<false>(ka[0], at_k + j * 64);
-              ldmatrix4<false>(ka[1], at_k + j * 64 + 32);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < C::kParts; ++k) {
-                  float(&c)[4] = k ? c1[m][n] : c0[m][n];
-                  mma<C::kBf>(c, ka[0][0], ka[0][1], ka[0][2], ka[0][3], b[k][n].x, b[k][n].y);
-                  mma<C::kBf>(c, ka[1][0], ka[1][1], ka[1][2], ka[1][3], b[k][n].z, b[k][n].w);
-                }
-            }
           }
         }
 #pragma unroll
@@ -571,7 +687,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) s[m][n][w] = C::kQ8 ? c0[m][n][w] : c0[m][n][w] + c1[m][n][w];
+            for (int w = 0; w < 4; ++w)
+              s[m][n][w] = C::kQ8 ? acc[0][0][m][n][w]
+                                  : acc[0][0][m][n][w] + acc[1][0][m][n][w] + (acc[0][1][m][n][w] + acc[1][1][m][n][w]);
         // ---- softmax ----
         const int key0 = now.span.lo + (now.tile + i) * C::kTK + warp * C::kKeys;
         float al[NT][2];
@@ -650,60 +768,84 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             }
         // ---- O^T = O^T alpha + V^T P^T ----
         if (C::kQ8) {  // o stands in units of the tile's power of two
-          const float2 u = *reinterpret_cast<const float2 *>(sc + 2 * NG * C::kKeys);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) al[n][0] *= unit * u.y, al[n][1] *= unit * u.y;
-          unit = u.x;
+          for (int n = 0; n < NT; ++n) al[n][0] *= unit * per_unit, al[n][1] *= unit * per_unit;
+          unit = tile_unit;
         }
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          float c[2][NT][4] = {};
+        for (int j0 = 0; j0 < NG; j0 += 2) {  // (two groups of 32 dims, four chains)
+          float c[2][2][NT][4] = {};
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            uint32_t va[2][4];  // [16 dims][operand word]
-            if (C::kQ8) {
-              uint32_t x[4];  // dims 2g, 2g + 1 of the keys 2t, 2t + 1: chunk 0, 1 of keys 0-7, 8-15
-              ldmatrix4<true>(x, base + v_lane8 + 16 * m * C::kStride + j * 32);
+            uint32_t va[2][2][4];  // [group][16 dims][operand word]
+            uint32_t pq[2][NT][2][C::kParts];
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+            for (int jj = 0; jj < 2; ++jj) {
+              const int j = j0 + jj;
+              if (j >= NG) continue;
+              if (C::kQ8) {
+                uint32_t x[4];  // dims 2g, 2g + 1 of the keys 2t, 2t + 1: chunk 0, 1 of keys 0-7, 8-15
+                ldmatrix4<true>(x, base + v_lane8 + 16 * m * C::kStride + j * 32);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const uint32_t u = x[2 * h + q] ^ 0x80808080u;
-                  va[h][2 * q] = int8_f16<0x4240>(u), va[h][2 * q + 1] = int8_f16<0x4341>(u);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) {
+                    const uint32_t u = x[2 * h + q] ^ 0x80808080u;
+                    va[jj][h][2 * q] = int8_f16<0x4240>(u), va[jj][h][2 * q + 1] = int8_f16<0x4341>(u);
+                  }
+                // the scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9
+                const float *const dv = sc + (NG + j) * C::kKeys + 16 * m + 2 * t;
+                const float2 d0 = *reinterpret_cast<const float2 *>(dv);
+                const float2 d1 = *reinterpret_cast<const float2 *>(dv + 8);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  split2<C::kBf>(s[m][n][0] * d0.x, s[m][n][1] * d0.y, pq[jj][n][0]);
+                  split2<C::kBf>(s[m][n][2] * d1.x, s[m][n][3] * d1.y, pq[jj][n][1]);
                 }
-              // the scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9
-              const float *const dv = sc + (NG + j) * C::kKeys + 16 * m + 2 * t;
-              const float2 d0 = *reinterpret_cast<const float2 *>(dv);
-              const float2 d1 = *reinterpret_cast<const float2 *>(dv + 8);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                split2<C::kBf>(s[m][n][0] * d0.x, s[m][n][1] * d0.y, pw[m][n][0]);
-                split2<C::kBf>(s[m][n][2] * d1.x, s[m][n][3] * d1.y, pw[m][n][1]);
+              } else {
+                ldmatrix4<true>(va[jj][0], base + v_lane + 16 * m * C::kStride + j * 64);
+                ldmatrix4<true>(va[jj][1], base + v_lane + 16 * m * C::kStride + j * 64 + 32);
               }
-            } else {
-              ldmatrix4<true>(va[0], base + v_lane + 16 * m * C::kStride + j * 64);
-              ldmatrix4<true>(va[1], base + v_lane + 16 * m * C::kStride + j * 64 + 32);
             }
+#pragma unroll
+            for (int k = 0; k < C::kParts; ++k)
+#pragma unroll
+              for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) {
+                    if (j0 + jj >= NG) continue;
+                    const uint32_t(&v)[4] = va[jj][h];
+                    mma<C::kBf>(c[jj][h][n], v[0], v[1], v[2], v[3],
+                                C::kQ8 ? pq[jj][n][0][k] : pw[m][n][0][k],
+                                C::kQ8 ? pq[jj][n][1][k] : pw[m][n][1][k]);
+                  }
+          }
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < C::kParts; ++k)
-                  mma<C::kBf>(c[h][n], va[h][0], va[h][1], va[h][2], va[h][3], pw[m][n][0][k],
-                              pw[m][n][1][k]);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                o[2 * j + h][n][w] = fmaf(o[2 * j + h][n][w], al[n][w & 1], c[h][n][w]);
+                for (int w = 0; w < 4; ++w) {
+                  if (j0 + jj >= NG) continue;
+                  float &old = o[2 * (j0 + jj) + h][n][w];
+                  old = fmaf(old, al[n][w & 1], c[jj][h][n][w]);
+                }
         }
       }
       __syncwarp();  // the stage has been read
-      issue(stage);
+      {
+        int32_t *const entry = reinterpret_cast<int32_t *>(my_stage + C::kEntries);
+        const int32_t page = entry[lane & (C::kKeys - 1)];
+        issue(stage, place[0], page);
+#pragma unroll
+        for (int q = 0; q + 1 < C::kStages; ++q) place[q] = place[q + 1];
+        look_up(place[C::kStages - 1], entry);
+        copies_commit();
+      }
       if (++stage == C::kStages) stage = 0;
     }
 
@@ -729,14 +871,10 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           }
       }
     __syncthreads();
-    auto finish = [&](int r, int d, float4 x, float m, float l) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      store_io4(a.o, a.io, (head0 + r) * D + d,
-                make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-      if (d == 0 && p.stats) p.stats[unit_id * C::kRows + r] = make_float2((m == -INFINITY ? 0.f : m) - C::kBias, inv);
-    };
     if (now.tile == 0 && count == tiles) {
-      join_warps<C>(so, sm, sl, D, rows, finish);
+      join_warps<C>(so, sm, sl, D, rows, [&](int r, int d, float4 x, float m, float l) {
+        finish<C>(p, head0, unit_id, r, d, D, x, m, l);
+      });
     } else {
       const int64_t mine = me * 2 + (now.tile == 0);  // a block leaves at most two pieces
       join_warps<C>(so, sm, sl, D, rows, [&](int r, int d, float4 x, float m, float l) {
@@ -744,57 +882,14 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         if (d == 0)
           *reinterpret_cast<float2 *>(p.piece_ml + (mine * C::kRows + r) * 2) = make_float2(m, l);
       });
-      // blocks of the unit's first and last tile: block b has the tiles from T b / parts on
-      const int64_t b0 = ((unit_first + 1) * parts - 1) / T;
-      const int64_t b1 = ((unit_first + tiles) * parts - 1) / T;
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const int before = atomicAdd(p.count + b0, 1);
-        *slast = before == (int)(b1 - b0);
-        if (*slast) p.count[b0] = 0;
+        // blocks of the unit's first and last tile: block b has the tiles from T b / parts on
+        const int64_t b0 = ((unit_first + 1) * parts - 1) / T;
+        const int64_t b1 = ((unit_first + tiles) * parts - 1) / T;
+        split[splits] = {head0, unit_id, b0, b1, rows, arrive(p, b0, b1)};
       }
-      __syncthreads();
-      if (*slast) {  // warp w joins the pieces w, w + kWarps, ...; then the warps' results
-        __threadfence();
-        constexpr int Q = C::kRows * D / 128;  // a lane's groups of four dims
-        float4 x[Q];
-        float m[Q], l[Q];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f), m[q] = -INFINITY, l[q] = 0.f;
-        for (int64_t b = b0 + warp; b <= b1; b += C::kWarps) {
-          const int64_t from = (b * 2 + (b == b0)) * C::kRows;
-          float4 y[Q];
-          float2 ml[Q];
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const int it = 32 * q + lane;
-            const bool on = it / (D / 4) < rows;
-            y[q] = make_float4(0.f, 0.f, 0.f, 0.f), ml[q] = make_float2(-INFINITY, 0.f);
-            if (on) {
-              y[q] = __ldcg(reinterpret_cast<const float4 *>(p.piece_o + from * D) + it);
-              ml[q] = __ldcg(reinterpret_cast<const float2 *>(p.piece_ml) + from + it / (D / 4));
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const float top = fmaxf(m[q], ml[q].x), low = top == -INFINITY ? 0.f : top;
-            const float f = exp2_fast(m[q] - low), h = exp2_fast(ml[q].x - low);
-            m[q] = top;
-            l[q] = l[q] * f + ml[q].y * h;
-            x[q].x = x[q].x * f + y[q].x * h, x[q].y = x[q].y * f + y[q].y * h;
-            x[q].z = x[q].z * f + y[q].z * h, x[q].w = x[q].w * f + y[q].w * h;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          const int it = 32 * q + lane, r = warp * C::kRows + it / (D / 4), d = 4 * (it % (D / 4));
-          *reinterpret_cast<float4 *>(so + r * C::kLdO + d) = x[q];
-          if (d == 0) sm[r] = m[q], sl[r] = l[q];
-        }
-        __syncthreads();
-        join_warps<C>(so, sm, sl, D, rows, finish);
-      }
+      ++splits;
     }
     // the next piece
     at += count;
@@ -802,6 +897,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     now.tile += count - 1;
     next_tile(now, p, C::kTK);
   }
+  __syncthreads();
+  for (int k = 0; k < splits; ++k)
+    if (split[k].last) join_pieces<C, D>(p, split[k]);
 }
 
 // The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
