@@ -492,6 +492,25 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   // Q8_0: the two chunks of 16 dims side by side, keys 0-7 and 8-15 each
   const uint32_t v_lane8 = (C::kKeys + (lane & 7) + (lane & 8)) * C::kStride + (lane >> 4) * 16;
 
+  // The query rows of a unit as they are read: warp w has the rows w, w + kWarps, ..., lane i the
+  // dims 8 i .. 8 i + 7.
+  constexpr int RPW = (C::kRows + C::kWarps - 1) / C::kWarps;
+  float4 query[RPW][2];
+  auto load_query = [&](const Cursor &c) {
+    const int rows = min(C::kRows, p.group - c.rg * C::kRows);
+    const int64_t head0 = int64_t(c.s) * a.hq + c.hk * p.group + c.rg * C::kRows;
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      const int r = warp + i * C::kWarps;
+      query[i][0] = query[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows && lane < D / 8) {
+        query[i][0] = load_io4(a.q, a.io, (head0 + r) * D + lane * 8);
+        query[i][1] = load_io4(a.q, a.io, (head0 + r) * D + lane * 8 + 4);
+      }
+    }
+  };
+  load_query(now);
+
   while (at < end) {
     // ---- one piece: tiles of one unit ----
     const int64_t unit_first = at - now.tile;  // the unit's first tile, of all
@@ -504,12 +523,12 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     // the query's parts as operand words: lane 4 r + t' of (part, 8-row group, 32 dims) has the
     // words of two 16-dim steps.  f16 and bf16 rows: dims 2t', 2t' + 1 and 8 more of a step;
     // Q8_0 rows: dims 4t' .. 4t' + 3 (a chunk's four bytes)
-    for (int r = warp; r < C::kRows; r += C::kWarps) {
-      float x[8];
-      const bool on = r < rows && lane < D / 8;
-      const float4 u = on ? load_io4(a.q, a.io, (head0 + r) * D + lane * 8) : make_float4(0, 0, 0, 0);
-      const float4 v = on ? load_io4(a.q, a.io, (head0 + r) * D + lane * 8 + 4) : make_float4(0, 0, 0, 0);
-      x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+#pragma unroll
+    for (int i0 = 0; i0 < RPW; ++i0) {
+      const int r = warp + i0 * C::kWarps;
+      if (r >= C::kRows) break;
+      const float4 u = query[i0][0], v = query[i0][1];
+      const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
       int e = 0;
       if (!C::kBf) {  // a power of two that puts the row's largest element in [2^14, 2^15)
         float top = 0.f;
@@ -849,7 +868,12 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       if (++stage == C::kStages) stage = 0;
     }
 
-    // ---- the piece's result ----
+    // ---- the piece's result; the next piece's query is on its way meanwhile ----
+    Cursor next = now;
+    next.left = end - at - count + 1;
+    next.tile += count - 1;
+    next_tile(next, p, C::kTK);
+    if (at + count < end) load_query(next);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -882,21 +906,20 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         if (d == 0)
           *reinterpret_cast<float2 *>(p.piece_ml + (mine * C::kRows + r) * 2) = make_float2(m, l);
       });
-      __syncthreads();
-      if (tid == 0) {
-        // blocks of the unit's first and last tile: block b has the tiles from T b / parts on
-        const int64_t b0 = ((unit_first + 1) * parts - 1) / T;
-        const int64_t b1 = ((unit_first + tiles) * parts - 1) / T;
-        split[splits] = {head0, unit_id, b0, b1, rows, arrive(p, b0, b1)};
-      }
+      // blocks of the unit's first and last tile: block b has the tiles from T b / parts on
+      if (tid == 0)
+        split[splits] = {head0, unit_id, ((unit_first + 1) * parts - 1) / T,
+                         ((unit_first + tiles) * parts - 1) / T, rows, 0};
       ++splits;
     }
-    // the next piece
     at += count;
-    now.left = end - at + 1;
-    now.tile += count - 1;
-    next_tile(now, p, C::kTK);
+    now = next;
   }
+  // Shared units, after the last piece (to count a piece in behind its stores holds a block up for
+  // more than a microsecond, at the end as after the first piece, but here once).
+  if (splits == 0) return;
+  __syncthreads();
+  if (tid < splits) split[tid].last = arrive(p, split[tid].b0, split[tid].b1);
   __syncthreads();
   for (int k = 0; k < splits; ++k)
     if (split[k].last) join_pieces<C, D>(p, split[k]);
