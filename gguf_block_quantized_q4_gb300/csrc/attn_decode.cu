@@ -204,8 +204,8 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int s, int tk) {
   r.tiles = (r.len - r.lo + tk - 1) / tk;
   return r;
 }
-// Tiles of all sequences (in units of one unit per sequence), and the sequence in which tile
-// `at` of that order lies with its first tile; every lane of the warp gets them.
+// Tiles of all sequences (in units of one unit per sequence); lane i of the warp gets its run of
+// the sequences, lane_n from lane_s on, and their first tile.
 __device__ __forceinline__ int64_t all_tiles(const AttnArgs &a, int tk, int64_t *lane_first,
                                              int *lane_s, int *lane_n) {
   const int lane = threadIdx.x & 31, S = (int)a.S;
@@ -222,6 +222,22 @@ __device__ __forceinline__ int64_t all_tiles(const AttnArgs &a, int tk, int64_t 
   }
   *lane_first = inc - sum;
   return __shfl_sync(0xffffffffu, inc, 31);
+}
+
+// The sequence in which tile `at` lies, its span, and its first tile (in units of one unit per
+// sequence); for every lane of the warp.
+__device__ __forceinline__ int sequence_of(const AttnArgs &a, int tk, int64_t at, int64_t lane_first,
+                                           int lane_s, int lane_n, int64_t *first, Span *span) {
+  const unsigned owners = __ballot_sync(0xffffffffu, lane_first <= at && lane_n > 0);
+  const int src = 31 - __clz(owners);
+  *first = __shfl_sync(0xffffffffu, lane_first, src);
+  int s = __shfl_sync(0xffffffffu, lane_s, src);
+  *span = span_of(a, s, tk);
+  while (*first + span->tiles <= at) {
+    *first += span->tiles;
+    *span = span_of(a, ++s, tk);
+  }
+  return s;
 }
 
 // Where a warp's next tile lies.
@@ -378,16 +394,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 
   Cursor cur;  // the next tile whose rows are looked up
   {
-    const unsigned owners = __ballot_sync(0xffffffffu, lane_first * p.units <= at && lane_n > 0);
-    const int src = 31 - __clz(owners);
-    int64_t first = __shfl_sync(0xffffffffu, lane_first, src) * p.units;
-    int s = __shfl_sync(0xffffffffu, lane_s, src);
-    cur.span = span_of(a, s, C::kTK);
-    while (first + int64_t(cur.span.tiles) * p.units <= at) {
-      first += int64_t(cur.span.tiles) * p.units;
-      cur.span = span_of(a, ++s, C::kTK);
-    }
-    cur.s = s;
+    int64_t first;
+    cur.s = sequence_of(a, C::kTK, at / p.units, lane_first, lane_s, lane_n, &first, &cur.span);
+    first *= p.units;
     const int unit = (int)((at - first) / cur.span.tiles);
     cur.hk = unit / p.row_groups;
     cur.rg = unit % p.row_groups;
@@ -926,44 +935,62 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 }
 
 // The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
-// head in their order.  Four keys a thread, their loads side by side (a chain of page, logits and
-// sum per key, one after the other, took 75.8 us with the attention at 32 sequences of up to 4001
-// keys).
-constexpr int kTrackKeys = 1024;
-__global__ void __launch_bounds__(256) attn_track_kernel(const __grid_constant__ Params p, int rows) {
+// head in their order.  Bounded by latency (a few bytes a row): a block has `keys` keys of all kv
+// heads, a thread four (key, head) places at a time with their page entries, logits and sums side
+// by side (one place a thread, or blocks that stay and take tiles in turn, measured the same or
+// worse: 74 to 79 us with the attention of 32 sequences of up to 4001 keys, 8 heads, against 73).
+__global__ void __launch_bounds__(256) attn_track_kernel(const __grid_constant__ Params p, int rows,
+                                                         int keys) {
+  constexpr int N = 4;
   grid_dependency();
   const AttnArgs &a = p.a;
-  const int s = blockIdx.z, h = blockIdx.y;
+  const int s = blockIdx.y, hkv = a.c.hkv;
   const Span sp = span_of(a, s, 1);
-  const int j0 = sp.lo + blockIdx.x * kTrackKeys + threadIdx.x;
-  if (j0 >= sp.len) return;
-  int64_t r[4];
-  float old[4], w[4] = {};
+  const int first = sp.lo + blockIdx.x * keys, n = min(keys, sp.len - first);
+  if (n <= 0) return;
+  const int32_t *const pages = a.pages + s * a.pages_ld;
+  for (int i0 = threadIdx.x; i0 < keys * hkv; i0 += N * 256) {
+    int64_t r[N];
+    const float *x[N];
+    const float2 *stats[N];
+    bool on[N];
+    float w[N] = {}, old[N];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int j = j0 + 256 * k;
-    r[k] = j < sp.len ? kv_row(a.c, a.pages + s * a.pages_ld, h, j) : -1;
-    old[k] = r[k] < 0 ? 0.f : a.c.sums[r[k]];
-  }
-  for (int rg = 0; rg < p.row_groups; ++rg) {
-    const int64_t unit = int64_t(s) * p.units + h * p.row_groups + rg;
-    const float *x = p.logits + (unit * a.max_len + j0) * p.logit_width;
-    const int n = min(rows, p.group - rg * rows);
-    for (int i = 0; i < n; i += 2) {  // (an odd group's last pair holds a row that is not there)
-      const float2 s0 = p.stats[unit * rows + i];
-      const float2 s1 = i + 1 < n ? p.stats[unit * rows + i + 1] : make_float2(0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (r[k] >= 0) {
-          const float2 v = *reinterpret_cast<const float2 *>(x + 256 * k * p.logit_width + i);
-          w[k] += exp2_fast(v.x - s0.x) * s0.y;
-          if (i + 1 < n) w[k] += exp2_fast(v.y - s1.x) * s1.y;
-        }
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + 256 * k;
+      const int j = i % keys, h = i / keys;
+      on[k] = j < n && h < hkv;
+      r[k] = on[k] ? kv_row(a.c, pages, h, first + j) : -1;
+      const int64_t unit = int64_t(s) * p.units + (on[k] ? h : 0) * p.row_groups;
+      x[k] = p.logits + (unit * a.max_len + first + (on[k] ? j : 0)) * p.logit_width;
+      stats[k] = p.stats + unit * rows;
     }
-  }
+    for (int rg = 0; rg < p.row_groups; ++rg) {
+      const int group = min(rows, p.group - rg * rows);
+      for (int q = 0; q < group; q += 2) {
+        const bool pair = q + 1 < group;  // (an odd group's last pair holds a row that is not there)
+        float2 v[N], s0[N], s1[N];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (r[k] >= 0) a.c.sums[r[k]] = old[k] + w[k];
+        for (int k = 0; k < N; ++k) {
+          v[k] = *reinterpret_cast<const float2 *>(x[k] + q);
+          s0[k] = stats[k][q];
+          s1[k] = pair ? stats[k][q + 1] : make_float2(INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          w[k] += exp2_fast(v[k].x - s0[k].x) * s0[k].y;
+          if (pair) w[k] += exp2_fast(v[k].y - s1[k].x) * s1[k].y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] += a.max_len * int64_t(p.logit_width), stats[k] += rows;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) old[k] = r[k] < 0 ? 0.f : a.c.sums[r[k]];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (r[k] >= 0) a.c.sums[r[k]] = old[k] + w[k];
+  }
 }
 
 // Query rows of a unit: 8 columns of the products, or 16 where the group fills more than 8 of
@@ -1074,10 +1101,12 @@ mq_status launch_attn_decode(const AttnArgs &a, cudaStream_t s, const DeviceStat
     case MQ_BF16: r = launch_dim<MQ_BF16>(p, rows, s, st); break;
     default: r = launch_dim<MQ_Q8_0>(p, rows, s, st); break;
   }
-  if (r == MQ_OK && a.track)
+  if (r == MQ_OK && a.track) {
+    const int keys = std::max(32, 1024 / a.c.hkv / 32 * 32);
     r = launch_dependent("attn_track_kernel", attn_track_kernel,
-                         dim3((a.max_len + kTrackKeys - 1) / kTrackKeys, a.c.hkv, (unsigned)a.S),
-                         dim3(256, 1, 1), 0, s, p, rows);
+                         dim3((a.max_len + keys - 1) / keys, (unsigned)a.S, 1), dim3(256, 1, 1), 0, s, p,
+                         rows, keys);
+  }
   return r;
 }
 
