@@ -79,6 +79,16 @@ __device__ __forceinline__ int64_t kv_row(const KvView &c, const int32_t *pages,
          int64_t((uint32_t)pos - pi * c.page.d) * c.slot_stride;
 }
 
+// The same in 32 bits (a cache spans at most 2^32 - 2 rows); kNoRow for -1.
+constexpr uint32_t kNoRow = 0xffffffffu;
+__device__ __forceinline__ uint32_t kv_row32(const KvView &c, const int32_t *pages, int head, int pos) {
+  const uint32_t pi = quotient((uint32_t)pos, c.page);
+  const int page = pages[pi];
+  const uint32_t row = (uint32_t)page * (uint32_t)c.page_stride + (uint32_t)head * (uint32_t)c.head_stride +
+                       ((uint32_t)pos - pi * c.page.d) * (uint32_t)c.slot_stride;
+  return (uint32_t)page < (uint32_t)c.n_pages ? row : kNoRow;
+}
+
 // Kernels are launched with programmatic stream serialisation: they may become resident while
 // the previous kernel of the stream runs, and wait for it before their first global access.
 __device__ __forceinline__ void grid_dependency() {

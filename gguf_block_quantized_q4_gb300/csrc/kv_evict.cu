@@ -2,8 +2,8 @@
 // in order.
 //
 // Choice: a weight sum maps to an unsigned key in the order of the values (NaN above all, -0 as
-// 0).  A thread block cluster of up to 8 blocks holds the candidates' keys of one kv head in
-// shared memory (a part of the positions each) and finds the smallest key that stays by a radix
+// 0).  A thread block cluster of up to 8 blocks holds the candidates' keys of one kv head (a part
+// of the positions each, 16 a thread in registers and further ones in shared memory) and finds the smallest key that stays by a radix
 // selection from the top: histograms of 11, 11 and 10 bits, whose bins that are not empty are added
 // to rank 0's through distributed shared memory (every rank reading all of the others' took one
 // more cluster barrier and eight times the reads).  Rows equal to that key stay from the lowest position on; ballots
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kKeysHeld = 48 * 1024;  // per block, in shared memory; further keys are read again
+constexpr int kKeysHeld = 48 * 1024;  // per block, in shared memory, beside 16 K in registers
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -75,36 +75,52 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   for (int i = share; i < a.sink; i += stride) kept[i] = i;
   for (int i = share; i < a.recent; i += stride) kept[a.keep - a.recent + i] = n - a.recent + i;
 
-  // this block's candidates: positions [first, first + count)
+  // this block's candidates: positions [first, first + count), a run of whole 32s for each warp;
+  // lane i of a warp has the run's i-th, 32 + i-th, ... candidate: the first NK in registers, then
+  // `held` of the block in shared memory, others are read again
   const int all = n - a.recent - a.sink;
   const int per = (all + ranks - 1) / ranks;
   const int first = a.sink + rank * per, count = max(0, min(per, all - rank * per));
-  const int32_t *pages = a.pages + s * a.pages_ld;
-  auto key = [&](int i) -> uint32_t {
-    if (i < held) return keys[i];
-    const int64_t r = kv_row(a.c, pages, h, first + i);
-    return order_key(r < 0 ? 0.f : a.c.sums[r]);
-  };
-  // the keys: 16 pages and then 16 sums side by side, counted by their top bits at once
-  __syncthreads();
+  const int run = (count + kSelThreads - 1) / kSelThreads * 32;
+  const int r0 = min(warp * run, count), r1 = min(r0 + run, count);
+  const int32_t *const pages = a.pages + s * a.pages_ld;
   constexpr int NK = 16;
-  for (int i0 = tid; i0 < count; i0 += NK * kSelThreads) {
-    uint32_t r[NK];  // rows (fewer than 2^32 - 1)
-    float w[NK];
+  const int nk = (r1 - r0 + 31) / 32;  // (the same for the warp)
+  auto valid = [&](int k) { return r0 + 32 * k + lane < r1; };
+  auto read_key = [&](int k) -> uint32_t {
+    const uint32_t r = valid(k) ? kv_row32(a.c, pages, h, first + r0 + 32 * k + lane) : kNoRow;
+    return order_key(r == kNoRow ? 0.f : a.c.sums[r]);
+  };
+  auto far_key = [&](int k) -> uint32_t {
+    const int at = (k - NK) * kSelThreads + tid;
+    return at < held ? keys[at] : read_key(k);
+  };
+  __syncthreads();
+  uint32_t near[NK];
+  {  // 16 pages and then 16 sums side by side
+    uint32_t r[NK];
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const int i = i0 + k * kSelThreads;
-      r[k] = i < count ? (uint32_t)kv_row(a.c, pages, h, first + i) : ~0u;
+      if (k >= nk) break;  // (few candidates: the rest of the unrolled code is not even fetched)
+      r[k] = valid(k) ? kv_row32(a.c, pages, h, first + r0 + 32 * k + lane) : kNoRow;
     }
-#pragma unroll
-    for (int k = 0; k < NK; ++k) w[k] = r[k] == ~0u ? 0.f : a.c.sums[r[k]];
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const int i = i0 + k * kSelThreads;
-      const uint32_t v = order_key(w[k]);
-      if (i < min(count, held)) keys[i] = v;
-      if (i < count) atomicAdd(&sh.hist[v >> 21], 1u);
+      if (k >= nk) break;
+      near[k] = order_key(r[k] == kNoRow ? 0.f : a.c.sums[r[k]]);
     }
+  }
+  // counted by their top bits at once
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    if (k >= nk) break;
+    if (valid(k)) atomicAdd(&sh.hist[near[k] >> 21], 1u);
+  }
+  for (int k = NK; k < nk; ++k) {
+    const uint32_t v = read_key(k);
+    const int at = (k - NK) * kSelThreads + tid;
+    if (at < held) keys[at] = v;
+    if (valid(k)) atomicAdd(&sh.hist[v >> 21], 1u);
   }
   cluster.barrier_wait();
 
@@ -119,11 +135,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
       if (pass) {
         for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
         __syncthreads();
-#pragma unroll 8
-        for (int i = tid; i < count; i += kSelThreads) {
-          const uint32_t k = key(i);
-          if (k >> (shift + bits) == prefix) atomicAdd(&sh.hist[k >> shift & ((1u << bits) - 1)], 1u);
+        auto add = [&](int k, uint32_t v) {
+          if (valid(k) && v >> (shift + bits) == prefix)
+            atomicAdd(&sh.hist[v >> shift & ((1u << bits) - 1)], 1u);
+        };
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          if (k >= nk) break;
+          add(k, near[k]);
         }
+        for (int k = NK; k < nk; ++k) add(k, far_key(k));
       }
       __syncthreads();
       // the bins that are not empty, to rank 0
@@ -160,15 +181,19 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     }
   }
 
-  // places: each warp has a run of the block's candidates
-  const int run = (count + kSelThreads - 1) / kSelThreads * 32;
-  const int r0 = min(warp * run, count), r1 = min(r0 + run, count);
+  // places, from the counts before a warp's run
   uint32_t gt = 0, eq = 0;
-  for (int i = r0 + lane; i < r1 + lane; i += 32) {
-    const uint32_t k = i < r1 ? key(i) : 0;
-    gt += __popc(__ballot_sync(0xffffffffu, i < r1 && k > T));
-    eq += __popc(__ballot_sync(0xffffffffu, i < r1 && k == T));
+  auto tally = [&](int k, uint32_t v) {
+    gt += valid(k) && v > T;
+    eq += valid(k) && v == T;
+  };
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    if (k >= nk) break;
+    tally(k, near[k]);
   }
+  for (int k = NK; k < nk; ++k) tally(k, far_key(k));
+  gt = __reduce_add_sync(0xffffffffu, gt), eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) sh.gt[warp] = gt, sh.eq[warp] = eq;
   __syncthreads();
   if (warp == 0) {  // the block's counts, to every rank
@@ -183,15 +208,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   uint32_t gt_at = sum_before(sh.gt, warp, lane), eq_at = sum_before(sh.eq, warp, lane);
   for (int q = 0; q < rank; ++q) gt_at += sh.rank_gt[q], eq_at += sh.rank_eq[q];
   const uint32_t below = (1u << lane) - 1;
-  for (int i = r0 + lane; i < r1 + lane; i += 32) {
-    const uint32_t k = i < r1 ? key(i) : 0;
-    const unsigned is_eq = __ballot_sync(0xffffffffu, i < r1 && k == T);
-    const bool stay = i < r1 && (k > T || (k == T && eq_at + __popc(is_eq & below) < ties));
+  auto place = [&](int k, uint32_t v) {  // (all lanes of the warp)
+    const bool is_eq = valid(k) && v == T;
+    const unsigned eqs = __ballot_sync(0xffffffffu, is_eq);
+    const bool stay = (valid(k) && v > T) || (is_eq && eq_at + __popc(eqs & below) < ties);
     const unsigned stays = __ballot_sync(0xffffffffu, stay);
-    if (stay) kept[a.sink + gt_at + min(eq_at, ties) + __popc(stays & below)] = first + i;
-    gt_at += __popc(stays) - (min(eq_at + __popc(is_eq), ties) - min(eq_at, ties));
-    eq_at += __popc(is_eq);
+    if (stay) kept[a.sink + gt_at + min(eq_at, ties) + __popc(stays & below)] = first + r0 + 32 * k + lane;
+    gt_at += __popc(stays) - (min(eq_at + __popc(eqs), ties) - min(eq_at, ties));
+    eq_at += __popc(eqs);
+  };
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    if (k >= nk) break;
+    place(k, near[k]);
   }
+  for (int k = NK; k < nk; ++k) place(k, far_key(k));
 }
 
 // RB: bytes of a row; ROWS: rows of a warp (16 or 32).
@@ -207,13 +238,12 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
   if (lane < ROWS && j < a.keep) {
     const int src = a.kept[(int64_t(s) * a.c.hkv + h) * a.keep + j];
     if (src >= 0) {
-      const int64_t r = kv_row(a.c, a.pages + s * a.pages_ld, h, src);
-      const int64_t w = kv_row(a.c, a.new_pages + s * a.new_pages_ld, h, j);
-      on = r >= 0 && w >= 0;
-      from = (uint32_t)r, to = (uint32_t)w;
+      from = kv_row32(a.c, a.pages + s * a.pages_ld, h, src);
+      to = kv_row32(a.c, a.new_pages + s * a.new_pages_ld, h, j);
+      on = from != kNoRow && to != kNoRow;
       if (!on)
         index_error(a.status, kIdxEvictPage,
-                    r < 0 ? a.pages[s * a.pages_ld + quotient(src, a.c.page)]
+                    from == kNoRow ? a.pages[s * a.pages_ld + quotient(src, a.c.page)]
                           : a.new_pages[s * a.new_pages_ld + quotient(j, a.c.page)]);
     }
   }
@@ -286,7 +316,8 @@ mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState 
   int ranks = 1;
   while (ranks < kMaxCluster && a.max_len / (2 * ranks) >= kSelThreads && a.S * a.c.hkv * 2 * ranks <= st->sms)
     ranks *= 2;
-  const int held = std::min((a.max_len + ranks - 1) / ranks, kKeysHeld);
+  const int per_rank = ((a.max_len + ranks - 1) / ranks + kSelThreads - 1) / kSelThreads * kSelThreads;
+  const int held = std::max(0, std::min(per_rank - 16 * kSelThreads, kKeysHeld));
   mq_status r = launch_cluster("evict_select_kernel", evict_select_kernel,
                                dim3(ranks, (unsigned)a.S, a.c.hkv), dim3(kSelThreads, 1, 1),
                                size_t(held) * 4, s, ranks, a, held);
