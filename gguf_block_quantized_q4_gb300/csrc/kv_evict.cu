@@ -97,17 +97,32 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   };
   __syncthreads();
   uint32_t near[NK];
-  {  // 16 pages and then 16 sums side by side
-    uint32_t r[NK];
+  {  // 16 page entries, then 16 sums on their way side by side: no branch but the way out (few
+     // candidates: the rest of the unrolled code is not even fetched) and no use behind a load
+    int page[NK];
+    float w[NK];
+    uint32_t pi[NK];
+    auto pos = [&](int k) { return (uint32_t)(first + min(r0 + 32 * k + lane, r1 - 1)); };
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      if (k >= nk) break;  // (few candidates: the rest of the unrolled code is not even fetched)
-      r[k] = valid(k) ? kv_row32(a.c, pages, h, first + r0 + 32 * k + lane) : kNoRow;
+      if (k >= nk) break;
+      pi[k] = quotient(pos(k), a.c.page);
+      page[k] = pages[pi[k]];
     }
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
       if (k >= nk) break;
-      near[k] = order_key(r[k] == kNoRow ? 0.f : a.c.sums[r[k]]);
+      const bool known = (uint32_t)page[k] < (uint32_t)a.c.n_pages;
+      const uint32_t row = (uint32_t)page[k] * (uint32_t)a.c.page_stride +
+                           (uint32_t)h * (uint32_t)a.c.head_stride +
+                           (pos(k) - pi[k] * a.c.page.d) * (uint32_t)a.c.slot_stride;
+      near[k] = known;
+      w[k] = a.c.sums[known ? row : 0];
+    }
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      if (k >= nk) break;
+      near[k] = order_key(near[k] ? w[k] : 0.f);
     }
   }
   // counted by their top bits at once
