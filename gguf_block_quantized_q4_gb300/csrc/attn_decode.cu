@@ -21,7 +21,7 @@
 // rows are padded by 16 bytes, which puts the eight rows of a matrix on different banks.
 //
 // Work: (sequence, kv head, row group) units of tiles of TK keys, laid end to end; thread block b
-// of the `parts` that have work takes the tiles [b T / parts, (b + 1) T / parts) of all T.  The
+// of the `parts` that have work takes the steps [b T / parts, (b + 1) T / parts) of all T.  The
 // split is made on the device from the lengths, so unlike lengths load all SMs alike.  A unit
 // whole in one block is written at once; the pieces of the others go to the workspace, and the
 // last block of a unit to arrive joins them in a fixed order (a counter per unit's first block,
@@ -204,57 +204,81 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int s, int tk) {
   r.tiles = (r.len - r.lo + tk - 1) / tk;
   return r;
 }
-// Tiles of all sequences (in units of one unit per sequence); lane i of the warp gets its run of
-// the sequences, lane_n from lane_s on, and their first tile.
-__device__ __forceinline__ int64_t all_tiles(const AttnArgs &a, int tk, int64_t *lane_first,
-                                             int *lane_s, int *lane_n) {
+// The units' tiles laid end to end, each unit `gap` steps after the one before it: a unit costs a
+// block about as much beside its tiles as a tile does (its query, the join of the warps), and
+// blocks of many short units are to have fewer tiles.  (Without it 32 sequences of up to 4001
+// keys took 64 us, as many of one length 54.)  Blocks of only a few tiles get no gaps.
+struct Line {
+  int64_t steps;        // of all sequences
+  int gap;
+  int64_t lane_first;   // lane i's run of the sequences: lane_n from lane_s on; its first step (in
+  int lane_s, lane_n;   // steps of one unit per sequence)
+};
+__device__ __forceinline__ Line lay_out(const AttnArgs &a, int units, int tk, int blocks) {
   const int lane = threadIdx.x & 31, S = (int)a.S;
   const int per = (S + 31) / 32;
-  *lane_s = min(lane * per, S);
-  *lane_n = min(per, S - *lane_s);
-  int64_t sum = 0;
-  for (int i = 0; i < *lane_n; ++i) sum += span_of(a, *lane_s + i, tk).tiles;
-  int64_t inc = sum;
+  Line r;
+  r.lane_s = min(lane * per, S);
+  r.lane_n = min(per, S - r.lane_s);
+  int64_t tiles = 0;
+  int live = 0;  // sequences with tiles
+  for (int i = 0; i < r.lane_n; ++i) {
+    const int n = span_of(a, r.lane_s + i, tk).tiles;
+    tiles += n, live += n > 0;
+  }
+  int64_t upto = tiles;
+  int live_upto = live;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, inc, k);
-    if (lane >= k) inc += o;
+    const int64_t o = __shfl_up_sync(0xffffffffu, upto, k);
+    const int q = __shfl_up_sync(0xffffffffu, live_upto, k);
+    if (lane >= k) upto += o, live_upto += q;
   }
-  *lane_first = inc - sum;
-  return __shfl_sync(0xffffffffu, inc, 31);
+  const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+  r.gap = all * units >= 4 * int64_t(blocks);
+  r.lane_first = upto - tiles + int64_t(live_upto - live) * r.gap;
+  r.steps = (all + int64_t(__shfl_sync(0xffffffffu, live_upto, 31)) * r.gap) * units;
+  return r;
 }
 
-// The sequence in which tile `at` lies, its span, and its first tile (in units of one unit per
-// sequence); for every lane of the warp.
-__device__ __forceinline__ int sequence_of(const AttnArgs &a, int tk, int64_t at, int64_t lane_first,
-                                           int lane_s, int lane_n, int64_t *first, Span *span) {
-  const unsigned owners = __ballot_sync(0xffffffffu, lane_first <= at && lane_n > 0);
-  const int src = 31 - __clz(owners);
-  *first = __shfl_sync(0xffffffffu, lane_first, src);
-  int s = __shfl_sync(0xffffffffu, lane_s, src);
-  *span = span_of(a, s, tk);
-  while (*first + span->tiles <= at) {
-    *first += span->tiles;
-    *span = span_of(a, ++s, tk);
-  }
-  return s;
-}
-
-// Where a warp's next tile lies.
+// A place on the line: tile `tile` of a unit, at step `at` (a unit's tile 0 lies behind its gap).
 struct Cursor {
   int s, hk, rg, tile;  // sequence, kv head, row group, tile
   Span span;
-  int64_t left;         // tiles of this block from here on
+  int64_t at;
 };
-__device__ __forceinline__ void next_tile(Cursor &c, const Params &p, int tk) {
-  --c.left;
+// The first tile at or after a step of the line; for every lane of the warp.
+__device__ __forceinline__ Cursor cursor_at(const Params &p, const Line &line, int tk, int64_t at) {
+  Cursor c;
+  const int64_t q = at / p.units;
+  const unsigned owners = __ballot_sync(0xffffffffu, line.lane_first <= q && line.lane_n > 0);
+  const int src = 31 - __clz(owners);
+  int64_t first = __shfl_sync(0xffffffffu, line.lane_first, src);
+  c.s = __shfl_sync(0xffffffffu, line.lane_s, src);
+  c.span = span_of(p.a, c.s, tk);
+  while (c.span.tiles == 0 || first + c.span.tiles + line.gap <= q) {
+    if (c.span.tiles) first += c.span.tiles + line.gap;
+    c.span = span_of(p.a, ++c.s, tk);
+  }
+  const int64_t in = at - first * p.units, unit = in / (c.span.tiles + line.gap);
+  c.hk = (int)(unit / p.row_groups);
+  c.rg = (int)(unit % p.row_groups);
+  const int step = (int)(in - unit * (c.span.tiles + line.gap));
+  c.tile = max(0, step - line.gap);
+  c.at = at - step + line.gap + c.tile;
+  return c;
+}
+// The next tile; `end` bounds the steps, from there on the sequence stays.
+__device__ __forceinline__ void next_tile(Cursor &c, const Params &p, int tk, int gap, int64_t end) {
+  ++c.at;
   if (++c.tile < c.span.tiles) return;
   c.tile = 0;
+  c.at += gap;
   if (++c.rg < p.row_groups) return;
   c.rg = 0;
   if (++c.hk < p.a.c.hkv) return;
   c.hk = 0;
-  if (c.left <= 0) return;
+  if (c.at >= end) return;
   do {
     c.span = span_of(p.a, ++c.s, tk);
   } while (c.span.tiles == 0);
@@ -383,26 +407,12 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         store_io4(a.o, a.io, int64_t(s) * a.hq * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   }
 
-  int64_t lane_first;
-  int lane_s, lane_n;
-  const int64_t T = all_tiles(a, C::kTK, &lane_first, &lane_s, &lane_n) * p.units;
-  const int64_t parts = min((int64_t)gridDim.x, T);
+  const Line line = lay_out(a, p.units, C::kTK, gridDim.x);
+  const int64_t T = line.steps, parts = min((int64_t)gridDim.x, T);
   const int64_t me = blockIdx.x;
   if (me >= parts) return;
-  int64_t at = T * me / parts;  // this block's next tile, of all
-  const int64_t end = T * (me + 1) / parts;
-
-  Cursor cur;  // the next tile whose rows are looked up
-  {
-    int64_t first;
-    cur.s = sequence_of(a, C::kTK, at / p.units, lane_first, lane_s, lane_n, &first, &cur.span);
-    first *= p.units;
-    const int unit = (int)((at - first) / cur.span.tiles);
-    cur.hk = unit / p.row_groups;
-    cur.rg = unit % p.row_groups;
-    cur.tile = (int)((at - first) % cur.span.tiles);
-    cur.left = end - at;
-  }
+  const int64_t end = T * (me + 1) / parts;                         // this block's steps end here
+  Cursor cur = cursor_at(p, line, C::kTK, T * me / parts);  // the next tile whose rows are looked up
 
   // ---- the ring ----
   // A tile's rows are found from page entries that were copied into shared memory with the tile a
@@ -419,13 +429,13 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   } place[C::kStages];  // per tile looked up (oldest first)
   auto look_up = [&](Place &to, int32_t *entry) -> const int32_t * {  // at cur; then the next tile
     const int key = cur.span.lo + cur.tile * C::kTK + warp * C::kKeys + lane;
-    to.there = cur.left > 0 && lane < C::kKeys && key < cur.span.len;
+    to.there = cur.at < end && lane < C::kKeys && key < cur.span.len;
     const uint32_t pi = quotient((uint32_t)(to.there ? key : 0), a.c.page);
     to.row = (uint32_t)(cur.hk * a.c.head_stride) +
              ((uint32_t)key - pi * a.c.page.d) * (uint32_t)a.c.slot_stride;
     const int32_t *const from = a.pages + cur.s * a.pages_ld + pi;
     if (entry && lane < C::kKeys) copy4(smem_addr(entry + lane), from, to.there ? 4 : 0);
-    next_tile(cur, p, C::kTK);
+    next_tile(cur, p, C::kTK, line.gap, end);
     return from;
   };
   auto issue = [&](int stage, Place at, int32_t page) {  // a tile's rows into a stage
@@ -520,11 +530,11 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   };
   load_query(now);
 
-  while (at < end) {
+  while (now.at < end) {
     // ---- one piece: tiles of one unit ----
-    const int64_t unit_first = at - now.tile;  // the unit's first tile, of all
+    const int64_t unit_first = now.at - now.tile;  // the step of the unit's first tile
     const int tiles = now.span.tiles;
-    const int count = (int)min(end - at, int64_t(tiles - now.tile));
+    const int count = (int)min(end - now.at, int64_t(tiles - now.tile));
     const int rows = min(C::kRows, p.group - now.rg * C::kRows);  // query rows that exist
     const int64_t head0 = int64_t(now.s) * a.hq + now.hk * p.group + now.rg * C::kRows;
     const int64_t unit_id = int64_t(now.s) * p.units + now.hk * p.row_groups + now.rg;
@@ -879,10 +889,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 
     // ---- the piece's result; the next piece's query is on its way meanwhile ----
     Cursor next = now;
-    next.left = end - at - count + 1;
-    next.tile += count - 1;
-    next_tile(next, p, C::kTK);
-    if (at + count < end) load_query(next);
+    next.tile += count - 1, next.at += count - 1;
+    next_tile(next, p, C::kTK, line.gap, end);
+    if (next.at < end) load_query(next);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -915,13 +924,12 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         if (d == 0)
           *reinterpret_cast<float2 *>(p.piece_ml + (mine * C::kRows + r) * 2) = make_float2(m, l);
       });
-      // blocks of the unit's first and last tile: block b has the tiles from T b / parts on
+      // blocks of the unit's first and last tile: block b has the steps from T b / parts on
       if (tid == 0)
         split[splits] = {head0, unit_id, ((unit_first + 1) * parts - 1) / T,
                          ((unit_first + tiles) * parts - 1) / T, rows, 0};
       ++splits;
     }
-    at += count;
     now = next;
   }
   // Shared units, after the last piece (to count a piece in behind its stores holds a block up for
