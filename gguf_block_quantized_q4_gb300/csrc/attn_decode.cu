@@ -162,14 +162,12 @@ struct Shape {
   static constexpr int kRaw = kEntries + kKeys * 4;
   static constexpr int kScaleRow = (kNG + 1) / 2 * 4;
   static constexpr int kStage = (kRaw + (kQ8 ? 2 * kKeys * kScaleRow : 0) + 15) / 16 * 16;
-  // the scales of a warp's tile in binary32, K's then V's, [32-element block][key]
-  static constexpr int kScales = kQ8 ? 2 * kNG * kKeys * 4 : 0;
   static constexpr int kLdO = D + 4;
   // the query's parts as operand words; Q8_0: and -128 times its block sums as accumulators
   static constexpr int kQuery = kParts * NT * kNG * 32 * 16;
   static constexpr int kSums = kQ8 ? NT * kNG * 4 * 16 : 0;
   static constexpr int smem(int warps, int stages) {
-    return warps * (stages * kStage + kScales + kRows * (kLdO + 2) * 4) + kQuery + kSums + kRows * 4;
+    return warps * (stages * kStage + kRows * (kLdO + 2) * 4) + kQuery + kSums + kRows * 4;
   }
   static constexpr int kWarps = smem(8, 2) <= kSmemMax ? 8 : smem(6, 2) <= kSmemMax ? 6 : 4;
   static constexpr int kStages = smem(kWarps, 3) <= kSmemMax ? 3 : 2;
@@ -386,8 +384,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kAll = MT == 2 ? 0xffffffffu : 0xffffu;  // all keys of a warp's tile
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t *const ring = smem;                                               // [warp][stage][K, V]
-  float *const scales = reinterpret_cast<float *>(ring + C::kWarps * C::kStages * C::kStage);  // [warp]
-  uint4 *const sq = reinterpret_cast<uint4 *>(scales + C::kWarps * (C::kScales / 4));
+  uint4 *const sq = reinterpret_cast<uint4 *>(ring + C::kWarps * C::kStages * C::kStage);
   float4 *const ssum = reinterpret_cast<float4 *>(sq + C::kQuery / 16);     // [8 rows][block][t]
   float *const so = reinterpret_cast<float *>(ssum + C::kSums / 16);        // [warp][row][kLdO]
   float *const sm = so + C::kWarps * C::kRows * C::kLdO, *const sl = sm + C::kWarps * C::kRows;
@@ -420,7 +417,6 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   // the few scoreboards of a warp are shared, and an operand's wait became a wait for it.)
   uint8_t *const my_ring = ring + warp * C::kStages * C::kStage;
   const uint32_t ring0 = smem_addr(my_ring);
-  float *const sc = scales + warp * (C::kScales / 4);
   uint32_t valid_bits[C::kStages] = {};  // per tile in flight (oldest first): keys that are there
   uint32_t odd_bits[C::kStages] = {};    // keys of odd rows (their scales, where NG is odd)
   struct Place {
@@ -613,44 +609,52 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       uint8_t *const my_stage = my_ring + stage * C::kStage;
       if (here) {
         float tile_unit = 1.f, per_unit = 1.f;  // the power of two of V's scales, and its inverse
-        if (C::kQ8) {  // the tile's scales in binary32, V's scaled to at most 1 by a power of two
-          constexpr int SW = C::kScaleRow / 4;
-          uint32_t w[MT][SW], top = 0;
+        constexpr int SW = C::kScaleRow / 4;    // words of a row's Q8_0 scales, two each
+        // the scales of a key: of K (plane 0) or V (1)
+        auto scales_of = [&](uint32_t (&w)[SW], int plane, int key) {
+          const uint8_t *const from = my_stage + C::kRaw + (plane * C::kKeys + key) * C::kScaleRow;
+          if constexpr (SW == 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(from);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+          } else if constexpr (SW == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(from);
+            w[0] = v.x, w[1] = v.y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < SW; ++j) w[j] = reinterpret_cast<const uint32_t *>(from)[j];
+          }
+          if constexpr (NG & 1) {  // (an odd row's start in the middle of its first word)
+            const int shift = odd_bits[0] >> key & 1 ? 16 : 0;
+#pragma unroll
+            for (int j = 0; j < SW; ++j) w[j] = __funnelshift_r(w[j], j + 1 < SW ? w[(j + 1) % SW] : 0, shift);
+          }
+        };
+        if (C::kQ8) {  // a power of two that V's largest scale of the tile is below
+          uint32_t top = 0;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const uint32_t *const from = reinterpret_cast<const uint32_t *>(
-                my_stage + C::kRaw + ((lane >> 4) * C::kKeys + 16 * m + (lane & 15)) * C::kScaleRow);
-#pragma unroll
-            for (int j = 0; j < SW; ++j) w[m][j] = from[j];
-            if ((NG & 1) && odd_bits[0] >> (16 * m + (lane & 15)) & 1) {
-#pragma unroll
-              for (int j = 0; j < SW; ++j) w[m][j] = __funnelshift_r(w[m][j], j + 1 < SW ? w[m][(j + 1) % SW] : 0, 16);
-            }
-            if (NG & 1) w[m][SW - 1] &= 0xffffu;
+            uint32_t w[SW];
+            scales_of(w, 1, 16 * m + (lane & 15));
+            if (NG & 1) w[SW - 1] &= 0xffffu;
 #pragma unroll
             for (int j = 0; j < SW; ++j)  // (f16 bits of magnitudes order as numbers)
-              if (lane >= 16) top = max(top, max(w[m][j] & 0x7fffu, w[m][j] >> 16 & 0x7fffu));
+              top = max(top, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
           }
           top = __reduce_max_sync(0xffffffffu, top);
           const int e = top == 0 || top >= 0x7c00u
                             ? 126
                             : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
           tile_unit = __uint_as_float(uint32_t(e + 1) << 23), per_unit = __uint_as_float(uint32_t(253 - e) << 23);
-          const float f = lane < 16 ? 1.f : per_unit;
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-              const float2 d = unpack2<false>(w[m][j / 2]);
-              sc[((lane >> 4) * NG + j) * C::kKeys + 16 * m + (lane & 15)] = (j & 1 ? d.y : d.x) * f;
-            }
-          __syncwarp();
         }
         // ---- S^T = K Q^T ----
         // Two groups of 32 dims at a time, so that (with two 16-key groups for narrow rows) four
         // chains of products are on their way; f16 and bf16 rows have an accumulator per chain
         // and part kind (first; others) up to the end.
         float s[MT][NT][4], acc[2][2][MT][NT][4] = {};
+        uint32_t kscale[MT][2][SW];  // Q8_0: of the keys g, g + 8
+        if (C::kQ8)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) scales_of(kscale[m][0], 0, 16 * m + g), scales_of(kscale[m][1], 0, 16 * m + 8 + g);
 #pragma unroll
         for (int j0 = 0; j0 < NG; j0 += 2) {
           uint4 b[2][C::kParts][NT];
@@ -711,7 +715,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
                 if (j0 + jj >= NG) continue;
-                const float da = sc[(j0 + jj) * C::kKeys + 16 * m + g], db = sc[(j0 + jj) * C::kKeys + 16 * m + g + 8];
+                const float2 d0 = unpack2<false>(kscale[m][0][j0 / 2]), d1 = unpack2<false>(kscale[m][1][j0 / 2]);
+                const float da = jj ? d0.y : d0.x, db = jj ? d1.y : d1.x;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -796,8 +801,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                 const uint32_t x = __float_as_uint(s[m][n][2 * h]), y = __float_as_uint(s[m][n][2 * h + 1]);
                 const uint32_t hi = transpose8x8(__byte_perm(x, y, 0x7632));
                 const uint32_t lo = transpose8x8(__byte_perm(x, y, 0x5410));
-                s[m][n][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
-                s[m][n][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+                s[m][n][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410)) * per_unit;
+                s[m][n][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632)) * per_unit;
               } else {
                 split2<C::kBf>(s[m][n][2 * h], s[m][n][2 * h + 1], pw[m][n][h]);
 #pragma unroll
@@ -810,6 +815,12 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           for (int n = 0; n < NT; ++n) al[n][0] *= unit * per_unit, al[n][1] *= unit * per_unit;
           unit = tile_unit;
         }
+        uint32_t vscale[MT][4][SW];  // Q8_0: of the keys 2t, 2t + 1, 2t + 8, 2t + 9
+        if (C::kQ8)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) scales_of(vscale[m][q], 1, 16 * m + 8 * (q >> 1) + 2 * t + (q & 1));
 #pragma unroll
         for (int j0 = 0; j0 < NG; j0 += 2) {  // (two groups of 32 dims, four chains)
           float c[2][2][NT][4] = {};
@@ -831,14 +842,16 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                     const uint32_t u = x[2 * h + q] ^ 0x80808080u;
                     va[jj][h][2 * q] = int8_f16<0x4240>(u), va[jj][h][2 * q + 1] = int8_f16<0x4341>(u);
                   }
-                // the scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9
-                const float *const dv = sc + (NG + j) * C::kKeys + 16 * m + 2 * t;
-                const float2 d0 = *reinterpret_cast<const float2 *>(dv);
-                const float2 d1 = *reinterpret_cast<const float2 *>(dv + 8);
+                float d[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float2 v = unpack2<false>(vscale[m][q][j0 / 2]);
+                  d[q] = jj ? v.y : v.x;
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                  split2<C::kBf>(s[m][n][0] * d0.x, s[m][n][1] * d0.y, pq[jj][n][0]);
-                  split2<C::kBf>(s[m][n][2] * d1.x, s[m][n][3] * d1.y, pq[jj][n][1]);
+                  split2<C::kBf>(s[m][n][0] * d[0], s[m][n][1] * d[1], pq[jj][n][0]);
+                  split2<C::kBf>(s[m][n][2] * d[2], s[m][n][3] * d[3], pq[jj][n][1]);
                 }
               } else {
                 ldmatrix4<true>(va[jj][0], base + v_lane + 16 * m * C::kStride + j * 64);
