@@ -24,9 +24,9 @@
 // of the `parts` that have work takes the steps [b T / parts, (b + 1) T / parts) of all T.  The
 // split is made on the device from the lengths, so unlike lengths load all SMs alike.  A unit
 // whole in one block is written at once; the pieces of the others go to the workspace, and the
-// last block of a unit to arrive joins them in a fixed order (a counter per unit's first block,
-// back to zero afterwards), so results do not depend on the order of execution.  The rings run
-// on across pieces.
+// last block of a unit (or of a group of its pieces) to arrive joins them in a fixed order
+// (counters, back to zero afterwards), so results do not depend on the order of execution.  The
+// rings run on across pieces.
 //
 // Precision: f16 operands are multiplied exactly and summed in binary32.  q (scaled by a power
 // of two per row) and the weights are carried as two f16 parts (22 bits), against bf16 keys and
@@ -42,7 +42,7 @@
 namespace mq {
 namespace {
 
-constexpr int kMaxParts = MQ_ATTN_WS_ZERO / 4;  // thread blocks with work (a counter each)
+constexpr int kMaxParts = MQ_ATTN_WS_ZERO / 12;  // thread blocks with work (three counters each)
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // ---- device helpers ---------------------------------------------------------------------
@@ -184,8 +184,12 @@ struct Params {
   int group, row_groups, units;  // query heads of a kv head; row groups of them; per sequence
   int logit_width;               // query rows per key in the logits (even)
   float scale_log2;
-  int *count;                    // [kMaxParts]
-  float *piece_o, *piece_ml;     // [block][2][rows][D], [block][2][rows][2]
+  int *count;                    // [3][kMaxParts]: a unit's first group, its others, its groups
+  // results of blocks (two each: a piece whose unit began before the block; one whose unit begins
+  // in it), then of groups (by their first block, two each: a unit's others, its first)
+  float *piece_o;                // [4][blocks][rows][D]
+  float2 *piece_ml;              // [4][blocks][rows]: maximum, sum
+  int blocks;
   float *logits;                 // [S][units][max_len][logit_width], or nullptr
   float2 *stats;                 // [S][units][rows]: (m - bias, 1 / l)
 };
@@ -283,11 +287,28 @@ __device__ __forceinline__ void next_tile(Cursor &c, const Params &p, int tk, in
 }
 
 // A unit that several blocks share: its first query head's row of q and o, its number, its first
-// and last block, its query rows; whether this block arrived last.
+// and last block, its query rows; whether this block arrived last at a count.
 struct Split {
   int64_t head0, unit_id, b0, b1;
   int rows, last;
+  int64_t first;  // the group of this block's piece: its first block, its blocks
+  int members;
 };
+
+// A result in the workspace: kind 0, 1 a block's pieces, 2, 3 a group's (Params).
+struct Result {
+  float *o;
+  float2 *ml;
+};
+template <class C, int D>
+__device__ __forceinline__ Result result_of(const Params &p, int kind, int64_t block) {
+  const int64_t at = (int64_t(kind) * p.blocks + block) * C::kRows;
+  return {p.piece_o + at * D, p.piece_ml + at};
+}
+__device__ __forceinline__ void store_result(const Result &to, int D, int r, int d, float4 x, float m, float l) {
+  *reinterpret_cast<float4 *>(to.o + r * D + d) = x;
+  if (d == 0) to.ml[r] = make_float2(m, l);
+}
 
 // Four dims of a query row's output, normalised.
 template <class C>
@@ -300,55 +321,89 @@ __device__ __forceinline__ void finish(const Params &p, int64_t head0, int64_t u
     p.stats[unit_id * C::kRows + r] = make_float2((m == -INFINITY ? 0.f : m) - C::kBias, inv);
 }
 
-// Counts a block's piece of a shared unit in; true where it is the unit's last.  One thread calls
-// it, after a barrier behind the block's stores: the release covers them (the barrier orders them
-// before it), the acquire what the other blocks stored.
-__device__ __forceinline__ bool arrive(const Params &p, int64_t b0, int64_t b1) {
+// Counts a piece in, of `others` + 1; true where it is the last.  One thread calls it, after a
+// barrier behind the block's stores: the release covers them (the barrier orders them before it),
+// the acquire what the other blocks stored.
+__device__ __forceinline__ bool arrive(int *count, int64_t others) {
   int before;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.count + b0) : "memory");
-  const bool last = before == (int)(b1 - b0);
-  if (last) p.count[b0] = 0;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+  const bool last = before == (int)others;
+  if (last) *count = 0;
   return last;
 }
 
-// Joins a shared unit's pieces: a thread sums four dims of a row over the pieces in their order,
-// kJoin pieces with their maxima and sums on their way at a time (a warp per piece, one after the
-// other, took 1.4 us a round; factors shared through shared memory as long).  Out of line: what it
-// keeps in registers is not the tiles' loop's.
-constexpr int kJoin = 20;
+// How a shared unit's pieces are joined: up to kOneJoin at once; more in groups of about the square
+// root of their number, by the last block of each group, then the groups by the last of those (one
+// block for all read 38 pieces in 4 us and 152 in 16: what a single SM takes in bounds it).
+constexpr int kOneJoin = 12;
+struct Groups {
+  int size, number;
+};
+__device__ __forceinline__ Groups groups_of(const Split &u) {
+  const int n = (int)(u.b1 - u.b0 + 1);
+  const int size = n <= kOneJoin ? n : (int)ceilf(sqrtf((float)n));
+  return {size, (n + size - 1) / size};
+}
+
+// Joins n results of a unit, the first at `r0`, the i-th `i * step` blocks behind `r1`: a thread
+// sums I places of four dims of a row over them in their order, J results on their way at a time.
+// To `to` in the workspace, or (to.o null) normalised to the output.  Out of line, and with plain
+// arguments: what it keeps in registers is not the tiles' loop's.
 template <class C, int D>
-__device__ __noinline__ void join_pieces(const Params &p, const Split &u) {
-  for (int it = threadIdx.x; it < u.rows * (D / 4); it += C::kThreads) {
-    const int r = it / (D / 4);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    for (int64_t c0 = u.b0; c0 <= u.b1; c0 += kJoin) {
-      float4 y[kJoin];
-      float2 ml[kJoin];
+__device__ __noinline__ void join_results(const Params &p, const Split &u, Result r0, Result r1, int step,
+                                          int n, Result to) {
+  constexpr int I = (C::kRows * D / 4 + C::kThreads - 1) / C::kThreads, J = I == 1 ? 10 : I == 2 ? 6 : 4;
+  float4 x[I];
+  float m[I], l[I];
+  int at[I];  // (a place past the rows takes the first instead, and stores nothing)
+  const int places = u.rows * (D / 4);
 #pragma unroll
-      for (int i = 0; i < kJoin; ++i) {
-        y[i] = make_float4(0.f, 0.f, 0.f, 0.f), ml[i] = make_float2(-INFINITY, 0.f);
-        if (c0 + i <= u.b1) {
-          const int64_t from = ((c0 + i) * 2 + (c0 + i == u.b0)) * C::kRows;
-          ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.piece_ml) + from + r);
-          y[i] = __ldcg(reinterpret_cast<const float4 *>(p.piece_o + from * D) + it);
+  for (int q = 0; q < I; ++q) {
+    x[q] = make_float4(0.f, 0.f, 0.f, 0.f), m[q] = -INFINITY, l[q] = 0.f;
+    at[q] = threadIdx.x + q * C::kThreads < places ? threadIdx.x + q * C::kThreads : 0;
+  }
+  for (int c0 = 0; c0 < n; c0 += J) {
+    float4 y[I][J];
+    float2 ml[I][J];
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+      const int64_t row = int64_t(c0 + i) * step * C::kRows;
+      const float *const o = c0 + i ? r1.o + row * D : r0.o;
+      const float2 *const s = c0 + i ? r1.ml + row : r0.ml;
+#pragma unroll
+      for (int q = 0; q < I; ++q) {
+        ml[q][i] = make_float2(-INFINITY, 0.f), y[q][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + i < n) {
+          ml[q][i] = __ldcg(s + at[q] / (D / 4));
+          y[q][i] = __ldcg(reinterpret_cast<const float4 *>(o) + at[q]);
         }
       }
-      float top = m;
+    }
 #pragma unroll
-      for (int i = 0; i < kJoin; ++i) top = fmaxf(top, ml[i].x);
-      const float low = top == -INFINITY ? 0.f : top, f0 = exp2_fast(m - low);
-      m = top;
-      l *= f0, x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+    for (int q = 0; q < I; ++q) {
+      float top = m[q];
 #pragma unroll
-      for (int i = 0; i < kJoin; ++i) {
-        const float f = exp2_fast(ml[i].x - low);
-        l = fmaf(ml[i].y, f, l);
-        x.x = fmaf(y[i].x, f, x.x), x.y = fmaf(y[i].y, f, x.y);
-        x.z = fmaf(y[i].z, f, x.z), x.w = fmaf(y[i].w, f, x.w);
+      for (int i = 0; i < J; ++i) top = fmaxf(top, ml[q][i].x);
+      const float low = top == -INFINITY ? 0.f : top, f0 = exp2_fast(m[q] - low);
+      m[q] = top;
+      l[q] *= f0, x[q].x *= f0, x[q].y *= f0, x[q].z *= f0, x[q].w *= f0;
+#pragma unroll
+      for (int i = 0; i < J; ++i) {
+        const float f = exp2_fast(ml[q][i].x - low);
+        l[q] = fmaf(ml[q][i].y, f, l[q]);
+        x[q].x = fmaf(y[q][i].x, f, x[q].x), x[q].y = fmaf(y[q][i].y, f, x[q].y);
+        x[q].z = fmaf(y[q][i].z, f, x[q].z), x[q].w = fmaf(y[q][i].w, f, x[q].w);
       }
     }
-    finish<C>(p, u.head0, u.unit_id, r, 4 * (it % (D / 4)), D, x, m, l);
+  }
+#pragma unroll
+  for (int q = 0; q < I; ++q) {
+    if (threadIdx.x + q * C::kThreads >= places) continue;
+    const int r = at[q] / (D / 4), d = 4 * (at[q] % (D / 4));
+    if (to.o)
+      store_result(to, D, r, d, x[q], m[q], l[q]);
+    else
+      finish<C>(p, u.head0, u.unit_id, r, d, D, x[q], m[q], l[q]);
   }
 }
 
@@ -931,28 +986,47 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         finish<C>(p, head0, unit_id, r, d, D, x, m, l);
       });
     } else {
-      const int64_t mine = me * 2 + (now.tile == 0);  // a block leaves at most two pieces
+      const Result mine = result_of<C, D>(p, now.tile == 0, me);  // a block leaves at most two pieces
       join_warps<C>(so, sm, sl, D, rows, [&](int r, int d, float4 x, float m, float l) {
-        *reinterpret_cast<float4 *>(p.piece_o + (mine * C::kRows + r) * D + d) = x;
-        if (d == 0)
-          *reinterpret_cast<float2 *>(p.piece_ml + (mine * C::kRows + r) * 2) = make_float2(m, l);
+        store_result(mine, D, r, d, x, m, l);
       });
       // blocks of the unit's first and last tile: block b has the steps from T b / parts on
       if (tid == 0)
         split[splits] = {head0, unit_id, ((unit_first + 1) * parts - 1) / T,
-                         ((unit_first + tiles) * parts - 1) / T, rows, 0};
+                         ((unit_first + tiles) * parts - 1) / T, rows, 0, 0, 0};
       ++splits;
     }
     now = next;
   }
-  // Shared units, after the last piece (to count a piece in behind its stores holds a block up for
-  // more than a microsecond, at the end as after the first piece, but here once).
+  // Shared units, after the last piece (to count a piece in behind its stores holds a block up, at
+  // the end as after the first piece, but here once).
   if (splits == 0) return;
   __syncthreads();
-  if (tid < splits) split[tid].last = arrive(p, split[tid].b0, split[tid].b1);
+  if (tid < splits) {
+    Split &u = split[tid];
+    const Groups gr = groups_of(u);
+    const int mine = (int)(me - u.b0) / gr.size;
+    u.first = u.b0 + mine * gr.size;
+    u.members = (int)min(int64_t(gr.size), u.b1 - u.first + 1);
+    u.last = arrive(p.count + (mine ? kMaxParts : 0) + u.first, u.members - 1);
+  }
   __syncthreads();
-  for (int k = 0; k < splits; ++k)
-    if (split[k].last) join_pieces<C, D>(p, split[k]);
+  for (int k = 0; k < splits; ++k) {
+    const Split &u = split[k];
+    if (!u.last) continue;
+    const Groups gr = groups_of(u);
+    const Result none = {nullptr, nullptr};
+    const Result group = result_of<C, D>(p, 2 + (u.first == u.b0), u.first);
+    join_results<C, D>(p, u, result_of<C, D>(p, u.first == u.b0, u.first), result_of<C, D>(p, 0, u.first), 1,
+                       u.members, gr.number == 1 ? none : group);
+    if (gr.number == 1) continue;
+    __syncthreads();
+    if (tid == 0) split[k].last = arrive(p.count + 2 * kMaxParts + u.b0, gr.number - 1);
+    __syncthreads();
+    if (u.last)
+      join_results<C, D>(p, u, result_of<C, D>(p, 3, u.b0), result_of<C, D>(p, 2, u.b0), gr.size, gr.number,
+                         none);
+  }
 }
 
 // The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
@@ -1020,7 +1094,7 @@ int rows_of(int group, int dim) { return group > 8 && dim <= 128 ? 16 : 8; }
 
 struct Workspace {
   size_t piece_o, piece_ml, stats, logits, total;
-  int logit_width;
+  int logit_width, blocks;
 };
 Workspace workspace_of(int64_t S, int hq, int hkv, int dim, int64_t max_len, bool track,
                        const DeviceState *st) {
@@ -1028,9 +1102,10 @@ Workspace workspace_of(int64_t S, int hq, int hkv, int dim, int64_t max_len, boo
   const size_t units = size_t(hkv) * ((group + rows - 1) / rows);
   Workspace w;
   w.logit_width = std::min(rows, (group + 1) & ~1);
-  w.piece_ml = align256(kMaxParts * sizeof(int));
-  w.piece_o = align256(w.piece_ml + size_t(grid) * 2 * rows * 2 * 4);
-  w.stats = align256(w.piece_o + size_t(grid) * 2 * rows * dim * 4);
+  w.blocks = grid;
+  w.piece_ml = MQ_ATTN_WS_ZERO;
+  w.piece_o = align256(w.piece_ml + size_t(grid) * 4 * rows * sizeof(float2));
+  w.stats = align256(w.piece_o + size_t(grid) * 4 * rows * dim * 4);
   w.logits = align256(w.stats + (track ? size_t(S) * units * rows * 8 : 0));
   w.total = align256(w.logits + (track ? size_t(S) * units * size_t(max_len) * w.logit_width * 4 : 0));
   return w;
@@ -1112,7 +1187,8 @@ mq_status launch_attn_decode(const AttnArgs &a, cudaStream_t s, const DeviceStat
   p.logit_width = w.logit_width;
   p.scale_log2 = a.scale * kLog2e;
   p.count = reinterpret_cast<int *>(a.ws);
-  p.piece_ml = reinterpret_cast<float *>(a.ws + w.piece_ml);
+  p.blocks = w.blocks;
+  p.piece_ml = reinterpret_cast<float2 *>(a.ws + w.piece_ml);
   p.piece_o = reinterpret_cast<float *>(a.ws + w.piece_o);
   p.stats = a.track ? reinterpret_cast<float2 *>(a.ws + w.stats) : nullptr;
   p.logits = a.track ? reinterpret_cast<float *>(a.ws + w.logits) : nullptr;
