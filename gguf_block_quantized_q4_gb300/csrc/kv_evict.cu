@@ -3,17 +3,21 @@
 //
 // Choice: a weight sum maps to an unsigned key in the order of the values (NaN above all, -0 as
 // 0).  A thread block cluster of up to 8 blocks holds the candidates' keys of one kv head (a part
-// of the positions each, 16 a thread in registers and further ones in shared memory) and finds the smallest key that stays by a radix
-// selection from the top: histograms of 11, 11 and 10 bits, whose bins that are not empty are added
-// to rank 0's through distributed shared memory (every rank reading all of the others' took one
-// more cluster barrier and eight times the reads).  Rows equal to that key stay from the lowest position on; ballots
-// and the cluster's counts give every row its place.  What bounds it: latency, three rounds of
-// histogram and cluster barrier (it reads 4 bytes per row; counting bit by bit from global
-// memory, one block per head, took 5.2 ms for 131072 rows).
+// of the positions each, 16 a thread in registers and further ones in shared memory) and finds the
+// smallest key that stays by a radix selection from the top.  A histogram of the first 11 bits,
+// whose bins that are not empty are added to rank 0's through distributed shared memory (every
+// rank reading all of the others' took one more cluster barrier and eight times the reads), names
+// the bin that holds it.  If that has at most 4096 keys, each block reads them all and counts
+// their next 11 and 10 bits by itself; else these are counted over the cluster as well.  Rows
+// equal to the key stay from the lowest position on; ballots and the cluster's counts give every
+// row its place.  What bounds it: latency.  131072 rows of 4 heads take 20 us: a length, its pages
+// and their sums read one after the other 5, then the cluster's barriers and reads of about 1 us
+// each (it reads 4 bytes per row; counting bit by bit from global memory, one block per head, took
+// 5.2 ms).
 //
 // Copy: bounded by the bytes of the kept rows, read and written once.  A warp looks up 32 (or,
 // when there are few, 16) rows, one per lane, then moves them 16 bytes a lane, eight loads in
-// flight.
+// flight (32768 rows of 4 heads of 128, f16: 20.5 us, 6.5 TB/s).
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -28,7 +32,9 @@ constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeysHeld = 48 * 1024;  // per block, in shared memory, beside 16 K in registers
 constexpr int kMaxCluster = 8;
+constexpr uint32_t kList = 2 * kBins;  // keys of one bin that each block reads from the cluster's
 
+// No weight's key is 0 (its float would be a NaN): it stands for no candidate.
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0xffffffffu;
   const uint32_t b = __float_as_uint(w + 0.f);  // -0 becomes 0
@@ -37,11 +43,13 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 struct SelShared {
   uint32_t hist[kBins];
-  uint32_t total[3][kBins];               // rank 0's: the cluster's histograms
+  uint32_t total[3][kBins];               // rank 0's: the cluster's histograms; the last two of
+                                          // every rank: its keys of the first chosen bin
   uint32_t warp_sum[kSelWarps];
   uint32_t gt[kSelWarps], eq[kSelWarps];  // per warp: candidates above T, equal to it
   uint32_t rank_gt[kMaxCluster], rank_eq[kMaxCluster];
   uint32_t bin, above, in_bin;            // the bin chosen, candidates above it and in it
+  uint32_t listed;                        // and their number
 };
 
 // Sum over the warps before this one of a value per warp in shared memory.
@@ -58,6 +66,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const int s = blockIdx.y, h = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins; i += kSelThreads)
     sh.hist[i] = sh.total[0][i] = sh.total[1][i] = sh.total[2][i] = 0;
+  if (tid == 0) sh.listed = 0;
   cluster.barrier_arrive();  // (the totals are clear; waited for before the first is added to)
   grid_dependency();
   const int raw = a.len[s], n = clamped_len(raw, a.max_len);
@@ -88,7 +97,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const int nk = (r1 - r0 + 31) / 32;  // (the same for the warp)
   auto valid = [&](int k) { return r0 + 32 * k + lane < r1; };
   auto read_key = [&](int k) -> uint32_t {
-    const uint32_t r = valid(k) ? kv_row32(a.c, pages, h, first + r0 + 32 * k + lane) : kNoRow;
+    if (!valid(k)) return 0;
+    const uint32_t r = kv_row32(a.c, pages, h, first + r0 + 32 * k + lane);
     return order_key(r == kNoRow ? 0.f : a.c.sums[r]);
   };
   auto far_key = [&](int k) -> uint32_t {
@@ -122,20 +132,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
       if (k >= nk) break;
-      near[k] = order_key(near[k] ? w[k] : 0.f);
+      near[k] = valid(k) ? order_key(near[k] ? w[k] : 0.f) : 0;
     }
   }
   // counted by their top bits at once
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     if (k >= nk) break;
-    if (valid(k)) atomicAdd(&sh.hist[near[k] >> 21], 1u);
+    if (near[k]) atomicAdd(&sh.hist[near[k] >> 21], 1u);
   }
   for (int k = NK; k < nk; ++k) {
     const uint32_t v = read_key(k);
     const int at = (k - NK) * kSelThreads + tid;
     if (at < held) keys[at] = v;
-    if (valid(k)) atomicAdd(&sh.hist[v >> 21], 1u);
+    if (v) atomicAdd(&sh.hist[v >> 21], 1u);
   }
   cluster.barrier_wait();
 
@@ -145,28 +155,39 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     T = 0xffffffffu;
   } else {
     uint32_t prefix = 0;  // the chosen bits so far
+    uint32_t *const list = sh.total[1];
+    uint32_t listed = 0, part[kList / kSelThreads];  // this thread's of the cluster's listed keys
+    bool own = ranks == 1;                           // the block's histogram is the whole one
     for (int pass = 0;; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       if (pass) {
         for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
         __syncthreads();
-        auto add = [&](int k, uint32_t v) {
-          if (valid(k) && v >> (shift + bits) == prefix)
+        auto add = [&](uint32_t v) {
+          if (v && v >> (shift + bits) == prefix)
             atomicAdd(&sh.hist[v >> shift & ((1u << bits) - 1)], 1u);
         };
+        if (listed) {
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          if (k >= nk) break;
-          add(k, near[k]);
+          for (int i = 0; i < int(kList) / kSelThreads; ++i)
+            if (i * kSelThreads + tid < listed) add(part[i]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            if (k >= nk) break;
+            add(near[k]);
+          }
+          for (int k = NK; k < nk; ++k) add(far_key(k));
         }
-        for (int k = NK; k < nk; ++k) add(k, far_key(k));
       }
       __syncthreads();
-      // the bins that are not empty, to rank 0
-      uint32_t *const total = cluster.map_shared_rank(sh.total[pass], 0);
-      for (int i = tid; i < kBins; i += kSelThreads)
-        if (sh.hist[i]) atomicAdd(total + i, sh.hist[i]);
-      cluster.sync();
+      uint32_t *total = sh.hist;
+      if (!own) {  // the bins that are not empty, to rank 0
+        total = cluster.map_shared_rank(sh.total[pass], 0);
+        for (int i = tid; i < kBins; i += kSelThreads)
+          if (sh.hist[i]) atomicAdd(total + i, sh.hist[i]);
+        cluster.sync();
+      }
       // the cluster's counts of this thread's two bins, from the top bin down
       const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
       const uint2 c = *reinterpret_cast<const uint2 *>(total + b0);
@@ -193,21 +214,53 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
         T = (prefix << shift) - 1, ties = 0;
         break;
       }
+      if (pass == 0 && !own && sh.in_bin <= kList) {
+        // few keys share the first bits: each block lists its own, reads all of them, and what is
+        // left to do needs no other block (a round over the cluster less, and no histogram's)
+        auto give = [&](uint32_t v) {
+          if (v && v >> shift == prefix) list[atomicAdd(&sh.listed, 1u)] = v;
+        };
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          if (k >= nk) break;
+          give(near[k]);
+        }
+        for (int k = NK; k < nk; ++k) give(far_key(k));
+        cluster.sync();
+        listed = sh.in_bin;
+        const uint32_t n_of = lane < ranks ? *cluster.map_shared_rank(&sh.listed, lane) : 0;
+        uint32_t upto = n_of;  // keys of the ranks up to this lane's
+#pragma unroll
+        for (int k = 1; k < kMaxCluster; k <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, upto, k);
+          if (lane >= k) upto += o;
+        }
+#pragma unroll
+        for (int i = 0; i < int(kList) / kSelThreads; ++i) {
+          const uint32_t at = i * kSelThreads + tid;
+          if (at - lane >= listed) break;
+          uint32_t q = 0, before = 0;
+#pragma unroll
+          for (int k = 0; k < kMaxCluster - 1; ++k) {
+            const uint32_t u = __shfl_sync(0xffffffffu, upto, k);
+            if (k < ranks - 1 && at >= u) q = k + 1, before = u;
+          }
+          part[i] = at < listed ? *cluster.map_shared_rank(list + (at - before), q) : 0;
+        }
+        own = true;
+      }
     }
   }
 
   // places, from the counts before a warp's run
   uint32_t gt = 0, eq = 0;
-  auto tally = [&](int k, uint32_t v) {
-    gt += valid(k) && v > T;
-    eq += valid(k) && v == T;
-  };
+  auto tally = [&](uint32_t v) { gt += v > T, eq += v == T; };
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     if (k >= nk) break;
-    tally(k, near[k]);
+    tally(near[k]);
   }
-  for (int k = NK; k < nk; ++k) tally(k, far_key(k));
+  for (int k = NK; k < nk; ++k) tally(far_key(k));
   gt = __reduce_add_sync(0xffffffffu, gt), eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) sh.gt[warp] = gt, sh.eq[warp] = eq;
   __syncthreads();
@@ -223,10 +276,24 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   uint32_t gt_at = sum_before(sh.gt, warp, lane), eq_at = sum_before(sh.eq, warp, lane);
   for (int q = 0; q < rank; ++q) gt_at += sh.rank_gt[q], eq_at += sh.rank_eq[q];
   const uint32_t below = (1u << lane) - 1;
+  if (eq == 0 || eq_at >= ties) {  // none of the warp's equal keys stays
+    int32_t *at = kept + a.sink + gt_at + min(eq_at, ties);
+    auto place = [&](int k, uint32_t v) {
+      const unsigned stays = __ballot_sync(0xffffffffu, v > T);
+      if (v > T) at[__popc(stays & below)] = first + r0 + 32 * k + lane;
+      at += __popc(stays);
+    };
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      if (k >= nk) break;
+      place(k, near[k]);
+    }
+    for (int k = NK; k < nk; ++k) place(k, far_key(k));
+    return;
+  }
   auto place = [&](int k, uint32_t v) {  // (all lanes of the warp)
-    const bool is_eq = valid(k) && v == T;
-    const unsigned eqs = __ballot_sync(0xffffffffu, is_eq);
-    const bool stay = (valid(k) && v > T) || (is_eq && eq_at + __popc(eqs & below) < ties);
+    const unsigned eqs = __ballot_sync(0xffffffffu, v == T);
+    const bool stay = v > T || (v == T && eq_at + __popc(eqs & below) < ties);
     const unsigned stays = __ballot_sync(0xffffffffu, stay);
     if (stay) kept[a.sink + gt_at + min(eq_at, ties) + __popc(stays & below)] = first + r0 + 32 * k + lane;
     gt_at += __popc(stays) - (min(eq_at + __popc(eqs), ties) - min(eq_at, ties));

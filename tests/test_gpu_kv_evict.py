@@ -112,6 +112,30 @@ def test_a_sequence_with_several_copies_of_one_sum_across_thread_blocks():
     assert kept[0, 0, 19899] == 19899 and kept[0, 0, 19900] == 39900
 
 
+@pytest.mark.parametrize("n,hkv", [(4500, 1), (9000, 3), (17000, 2), (40000, 1), (34000, 16),
+                                   (270000, 1)])
+@pytest.mark.parametrize("shape", ["spread", "close", "levels", "4096 alike", "4097 alike"])
+def test_choice_by_one_and_by_several_thread_blocks(n, hkv, shape):
+    """The last row that stays lies among few or many whose leading bits are its own."""
+    rng = np.random.default_rng(n)
+    p = paged("q8_0", [n], 2600, hkv=hkv, page_size=64, seed=n)
+    size = p.host["sums"].shape
+    if shape == "spread":
+        w = rng.random(size) ** 8 * 20
+    elif shape == "close":
+        w = 1 + rng.random(size) * 1e-3
+    elif shape == "levels":
+        w = rng.integers(0, 3, size) * 0.5
+    else:  # that many rows between 1 and 1.25 of the candidates, 1000 larger, the rest smaller
+        w = rng.random(size) * 0.5
+        for h in range(hkv):
+            at = 4 + rng.permutation(n - 104)[:1000 + int(shape.split()[0])]
+            page, slot = kv.place(p.pages_host[0], 64, at)
+            w[page[:1000], h, slot[:1000]] = 2 + rng.random(1000)
+            w[page[1000:], h, slot[1000:]] = 1 + rng.random(len(at) - 1000) * 0.24
+    check(p, 2600, 4, 100, w.astype(np.float32))
+
+
 def test_bad_lengths_and_pages_are_reported():
     p = paged("f16", [100, 50], 64, seed=7)
     new = torch.tensor(p.free[:8], dtype=torch.int32, device="cuda").view(2, 4)
