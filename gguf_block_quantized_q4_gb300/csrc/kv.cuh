@@ -209,6 +209,6 @@ struct EvictArgs {
   int *status;
 };
 mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *st);
-mq_status init_kv_evict(const DeviceState *st);  // shared-memory opt-in
+mq_status init_kv_evict(DeviceState *st);  // shared-memory opt-in, resident clusters
 
 }  // namespace mq

@@ -383,21 +383,36 @@ mq_status launch_copy(const EvictArgs &a, cudaStream_t s, const DeviceState *st)
 
 }  // namespace
 
-mq_status init_kv_evict(const DeviceState *st) {
+mq_status init_kv_evict(DeviceState *st) {
   const int bytes = kKeysHeld * 4;
   if (bytes + (int)sizeof(SelShared) > st->smem_optin)
     return fail(MQ_ERR_LAUNCH, "evict_select_kernel needs %d bytes of shared memory, the device allows %d",
                 bytes + (int)sizeof(SelShared), st->smem_optin);
-  const cudaError_t e =
+  cudaError_t e =
       cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 << i);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1 << i, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&st->evict_clusters[i], evict_select_kernel, &cfg);
+  }
   return e == cudaSuccess ? MQ_OK : cuda_fail(e, "cudaFuncSetAttribute", "evict_select_kernel");
 }
 
 mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *st) {
-  // blocks of a cluster: at least 1024 candidates each, and no more blocks than SMs
+  // blocks of a cluster: at least 4096 candidates each (4096 rows of 4 heads: 8.6 us by one block a
+  // head, 9.5 by two; 16384: 14.7, 12.4 by two, 11.0 by four or eight; 32768: 13.4 by four, 12.5 by
+  // eight), as long as all clusters are resident at once: 15 of eight blocks here, so that 16 heads
+  // of 32768 rows take 13.6 us by four blocks each and 21.4 by eight.
   int ranks = 1;
-  while (ranks < kMaxCluster && a.max_len / (2 * ranks) >= kSelThreads && a.S * a.c.hkv * 2 * ranks <= st->sms)
-    ranks *= 2;
+  for (int i = 1; i < 4 && (a.max_len >> i) >= 4096 && a.S * a.c.hkv <= st->evict_clusters[i]; ++i)
+    ranks = 1 << i;
   const int per_rank = ((a.max_len + ranks - 1) / ranks + kSelThreads - 1) / kSelThreads * kSelThreads;
   const int held = std::max(0, std::min(per_rank - 16 * kSelThreads, kKeysHeld));
   mq_status r = launch_cluster("evict_select_kernel", evict_select_kernel,
