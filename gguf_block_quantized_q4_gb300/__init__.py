@@ -1,4 +1,5 @@
-"""Python binding of libmq, the GB300 GGUF block-quantised matmul library.
+"""Python binding of libmq, the GB300 GGUF block-quantised matmul library, with the paged
+key-value cache and decode attention between its products.
 
 Argument marshalling only: every step of the computation runs in libmq's CUDA
 kernels.  PyTorch provides device memory and streams.  The C ABI

@@ -35,6 +35,12 @@
 // powers of two that put the largest weight at 2^15 and a tile's largest scale in [1/2, 1), so
 // that the second f16 part is a normal number for all but negligible products).  Each tile's
 // product is added to o by a binary32 fma (the tensor cores' own long sums may truncate).
+//
+// Measured (28/4 heads of 128): 38 x 8192 keys f16 104.5 us (6.1 TB/s, 91% of a plain copy's rate),
+// bf16 106, Q8_0 67 (5.1 TB/s, 76%: instructions and their latencies, not the bytes; its copies
+// alone take 55); 131072 bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start,
+// the first rows and the join); 64 ragged sequences up to 8192, f16 97 us, Q8_0 68; one sequence of
+// 37 keys, 14/2 heads of 64, 5.1.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -141,6 +147,7 @@ __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
   __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&u), *reinterpret_cast<const __half2 *>(&c));
   return *reinterpret_cast<uint32_t *>(&r);
 }
+
 // ---- the shape of a kernel ----------------------------------------------------------------
 constexpr int kSmemMax = 226 * 1024;  // per thread block (of 227 KB; a little is static)
 
@@ -154,7 +161,7 @@ struct Shape {
   static constexpr int kMT = kRow <= 128 ? 2 : 1;  // 16-key groups a warp takes at a time
   static constexpr int kKeys = 16 * kMT;
   static constexpr int kRows = 8 * NT;          // query rows of a unit
-  // shared memory: the rings, Q8_0 scales of a ring's keys, query parts, the warps' results
+  // shared memory: the rings, query parts, the warps' results
   static constexpr int kStride = kRow + 16;     // an odd number of 16-byte steps
   // a stage: K rows, V rows, the page entries of the tile a ring's length ahead, Q8_0 scales as
   // they are stored (K's keys, V's keys)
@@ -208,8 +215,8 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int s, int tk) {
 }
 // The units' tiles laid end to end, each unit `gap` steps after the one before it: a unit costs a
 // block about as much beside its tiles as a tile does (its query, the join of the warps), and
-// blocks of many short units are to have fewer tiles.  (Without it 32 sequences of up to 4001
-// keys took 64 us, as many of one length 54.)  Blocks of only a few tiles get no gaps.
+// blocks of many short units are to have fewer tiles.  (32 ragged sequences of up to 4001 keys,
+// 32/8 heads of 128, f16: 64 us without it, 54 with.)  Blocks of only a few tiles get no gaps.
 struct Line {
   int64_t steps;        // of all sequences
   int gap;
@@ -1032,8 +1039,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 // The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
 // head in their order.  Bounded by latency (a few bytes a row): a block has `keys` keys of all kv
 // heads, a thread four (key, head) places at a time with their page entries, logits and sums side
-// by side (one place a thread, or blocks that stay and take tiles in turn, measured the same or
-// worse: 74 to 79 us with the attention of 32 sequences of up to 4001 keys, 8 heads, against 73).
+// by side (one place a thread, or blocks that stay and take tiles in turn, took 1 to 6 us longer).
+// It adds 10 us to the 54 of 32 ragged sequences of up to 4001 keys, 32/8 heads of 128.
 __global__ void __launch_bounds__(256) attn_track_kernel(const __grid_constant__ Params p, int rows,
                                                          int keys) {
   constexpr int N = 4;

@@ -11,9 +11,12 @@
 // every access is 8 or 16 bytes wide.  A thread block takes one token after another, its threads
 // as many heads at a time as divide the heads evenly (a block per token pays the threads' places,
 // axes and divisions for each: 652 instructions a warp, 131 us for 16384 bf16 tokens); few tokens
-// are spread over more blocks, a round of heads each.  Q8_0 rows: the largest magnitude of a 32-element block meets in shared memory as an
-// integer maximum (the halves of a partial rotation may end inside a block, so no fixed lanes
-// share one), then the quants as in quant_row.cuh.
+// are spread over more blocks, a round of heads each.  Q8_0 rows: the largest magnitude of a
+// 32-element block meets in shared memory as an integer maximum (the halves of a partial rotation
+// may end inside a block, so no fixed lanes share one), then the quants as in quant_row.cuh.
+// Measured (28/4 heads of 128): 16384 tokens f32 to f16 98 us (5.9 TB/s, 89% of a plain copy's
+// rate), to Q8_0 93 us (90%), bf16 to f16 64 us (72%: latency of a token's chain); 4096 tokens f32
+// to f16, three axes, 25.4 us (85%); 8 tokens 2.1 us.
 #include <algorithm>
 #include <type_traits>
 

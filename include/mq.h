@@ -17,6 +17,10 @@
  *                   (mq_mmq) ("CUDA Backend Design" §4.4: the int8 MMQ path);
  *                   mq_mmq_fused does both in one kernel.
  *
+ * Between the products of a decoding step: a paged key-value cache, with rotary positions and
+ * the store of keys and values (mq_rope_store), attention of one new token per sequence
+ * (mq_attn_decode) and eviction by gathered attention weight (mq_kv_evict).
+ *
  * Conventions ("CUDA Backend Design" §4.9 GPU safety; "GPU Safety" CUDA
  * rules): every invariant violation returns an error status and never falls
  * back to another kernel or to the CPU; every launch is checked at its site;
@@ -321,10 +325,10 @@ mq_status mq_ffn_gu_matvec(mq_type type, const mq_weight *W, const float *x, flo
 mq_status mq_ffn_gu_mmq(mq_type type, const mq_weight *W, const void *xq, float *h, int64_t M,
                         int64_t N, int64_t K, mq_stream stream);
 
-/* ---- decode attention over a paged key-value cache ("minfer CUDA Backend Design" §4.3 and
- * §4.7: the attention, RoPE and KV-store nodes around the quantised matmuls; "Architecture
- * Execution Plan" C4: cells of f16 or Q8_0 rows; C8: paged sharing).  The pages name these
- * operations without writing them out; the formulas stand at each call. */
+/* ---- decode attention over a paged key-value cache ("minfer CUDA Backend Design" §4.3: the
+ * attention, RoPE and KV-store ops around the quantised matmuls; "Architecture Execution Plan"
+ * C4: cells of f16 or Q8_0 rows; C8: paged sharing).  The pages name these operations without
+ * writing them out; the formulas stand at each call. */
 
 /* A paged cache: planes the caller owns, described by value (nothing is kept between calls).
  * A row is head_dim consecutive elements: the key (or value) of one cached token and kv head.
@@ -406,7 +410,7 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * head; query head a reads kv head a / (n_heads / n_kv_heads).  A sequence of length 0 gives
  * o = 0.  Sums, softmax statistics and accumulators are binary32; f16 and Q8_0 keys meet the
  * query as two f16 parts (22 bits), bf16 keys as three bf16 parts (24 bits), and the weights
- * likewise.
+ * meet the values likewise.
  *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned
  *   len     device int32 [S], the rows to read, the new token's own among them; <= max_len
  *   max_len bound of the lengths on the host, <= pages_ld*page_size: it sizes the workspace
