@@ -42,6 +42,7 @@
 // the first rows and the join); 64 ragged sequences up to 8192, f16 97 us, Q8_0 68; one sequence of
 // 37 keys, 14/2 heads of 64, 5.1.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.cuh"
 
@@ -189,7 +190,7 @@ struct Shape {
 struct Params {
   AttnArgs a;
   int group, row_groups, units;  // query heads of a kv head; row groups of them; per sequence
-  int logit_width;               // query rows per key in the logits (even)
+  int logit_width;               // query rows per key in the logits (2, or whole fours)
   float scale_log2;
   int *count;                    // [3][kMaxParts]: a unit's first group, its others, its groups
   // results of blocks (two each: a piece whose unit began before the block; one whose unit begins
@@ -1037,61 +1038,69 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 }
 
 // The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
-// head in their order.  Bounded by latency (a few bytes a row): a block has `keys` keys of all kv
-// heads, a thread four (key, head) places at a time with their page entries, logits and sums side
-// by side (one place a thread, or blocks that stay and take tiles in turn, took 1 to 6 us longer).
-// It adds 10 us to the 54 of 32 ragged sequences of up to 4001 keys, 32/8 heads of 128.
-__global__ void __launch_bounds__(256) attn_track_kernel(const __grid_constant__ Params p, int rows,
-                                                         int keys) {
-  constexpr int N = 4;
-  grid_dependency();
+// head in their order.  Bounded by latency (a few bytes a row): a thread has four keys of a kv
+// head side by side, and finds their rows and reads their sums before it waits for the attention,
+// which writes neither (nor the tables: what came before the attention has ended when all of its
+// blocks have begun, and only then do these start).  Then the logits, four rows of a key at once,
+// and each row's maximum and sum for the four keys.  It and the logits add 8 us to the 54.5 of 32
+// ragged sequences of up to 4001 keys (32/8 heads of 128, f16), 2.3 to the 9 of 8 of up to 1100
+// (28/4); waiting first and with a place of every kv head per thread, 10 and 6.
+constexpr int kTrackThreads = 128, kTrackKeys = 4;  // keys of a thread
+template <int W>  // logits at a time
+__global__ void __launch_bounds__(kTrackThreads) attn_track_kernel(const __grid_constant__ Params p,
+                                                                   int rows, int keys) {
+  constexpr int N = kTrackKeys;
+  using Logits = typename std::conditional<W == 4, float4, float2>::type;
   const AttnArgs &a = p.a;
   const int s = blockIdx.y, hkv = a.c.hkv;
   const Span sp = span_of(a, s, 1);
   const int first = sp.lo + blockIdx.x * keys, n = min(keys, sp.len - first);
-  if (n <= 0) return;
+  bool waiting = true;
+  if (n <= 0) {
+    grid_dependency();  // (so that this kernel's end is the attention's, too)
+    return;
+  }
   const int32_t *const pages = a.pages + s * a.pages_ld;
-  for (int i0 = threadIdx.x; i0 < keys * hkv; i0 += N * 256) {
-    int64_t r[N];
-    const float *x[N];
-    const float2 *stats[N];
-    bool on[N];
+  const int apart = keys / N;  // a thread's keys
+  for (int i = threadIdx.x; i < apart * hkv; i += kTrackThreads) {
+    const int h = i / apart, j = i - h * apart;
+    const int64_t unit = (int64_t(s) * hkv + h) * p.row_groups;
+    const float *x = p.logits + (unit * a.max_len + first + j) * p.logit_width;
+    const float2 *stats = p.stats + unit * rows;
+    uint32_t r[N];
+    int step[N];  // (a key that is not there: the thread's first)
     float w[N] = {}, old[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int i = i0 + 256 * k;
-      const int j = i % keys, h = i / keys;
-      on[k] = j < n && h < hkv;
-      r[k] = on[k] ? kv_row(a.c, pages, h, first + j) : -1;
-      const int64_t unit = int64_t(s) * p.units + (on[k] ? h : 0) * p.row_groups;
-      x[k] = p.logits + (unit * a.max_len + first + (on[k] ? j : 0)) * p.logit_width;
-      stats[k] = p.stats + unit * rows;
+      const bool on = j + k * apart < n;
+      r[k] = on ? kv_row32(a.c, pages, h, first + j + k * apart) : kNoRow;
+      step[k] = on ? k * apart * p.logit_width : 0;
     }
+#pragma unroll
+    for (int k = 0; k < N; ++k) old[k] = r[k] == kNoRow ? 0.f : a.c.sums[r[k]];
+    if (waiting) grid_dependency();
+    waiting = false;
+    if (j >= n) continue;
     for (int rg = 0; rg < p.row_groups; ++rg) {
       const int group = min(rows, p.group - rg * rows);
-      for (int q = 0; q < group; q += 2) {
-        const bool pair = q + 1 < group;  // (an odd group's last pair holds a row that is not there)
-        float2 v[N], s0[N], s1[N];
+      for (int q = 0; q < group; q += W) {  // (the last ones' rows may not be there)
+        __align__(16) float v[N][W];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          v[k] = *reinterpret_cast<const float2 *>(x[k] + q);
-          s0[k] = stats[k][q];
-          s1[k] = pair ? stats[k][q + 1] : make_float2(INFINITY, 0.f);
-        }
+        for (int k = 0; k < N; ++k)
+          *reinterpret_cast<Logits *>(v[k]) = *reinterpret_cast<const Logits *>(x + step[k] + q);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          w[k] += exp2_fast(v[k].x - s0[k].x) * s0[k].y;
-          if (pair) w[k] += exp2_fast(v[k].y - s1[k].x) * s1[k].y;
+        for (int e = 0; e < W; ++e) {
+          if (q + e >= group) break;
+          const float2 st = stats[q + e];
+#pragma unroll
+          for (int k = 0; k < N; ++k) w[k] += exp2_fast(v[k][e] - st.x) * st.y;
         }
       }
-#pragma unroll
-      for (int k = 0; k < N; ++k) x[k] += a.max_len * int64_t(p.logit_width), stats[k] += rows;
+      x += a.max_len * int64_t(p.logit_width), stats += rows;
     }
 #pragma unroll
-    for (int k = 0; k < N; ++k) old[k] = r[k] < 0 ? 0.f : a.c.sums[r[k]];
-#pragma unroll
     for (int k = 0; k < N; ++k)
-      if (r[k] >= 0) a.c.sums[r[k]] = old[k] + w[k];
+      if (r[k] != kNoRow) a.c.sums[r[k]] = old[k] + w[k];
   }
 }
 
@@ -1108,7 +1117,7 @@ Workspace workspace_of(int64_t S, int hq, int hkv, int dim, int64_t max_len, boo
   const int group = hq / hkv, rows = rows_of(group, dim), grid = std::min(st->sms, kMaxParts);
   const size_t units = size_t(hkv) * ((group + rows - 1) / rows);
   Workspace w;
-  w.logit_width = std::min(rows, (group + 1) & ~1);
+  w.logit_width = std::min(rows, group <= 2 ? 2 : (group + 3) & ~3);  // (whole float2 or float4)
   w.blocks = grid;
   w.piece_ml = MQ_ATTN_WS_ZERO;
   w.piece_o = align256(w.piece_ml + size_t(grid) * 4 * rows * sizeof(float2));
@@ -1206,10 +1215,11 @@ mq_status launch_attn_decode(const AttnArgs &a, cudaStream_t s, const DeviceStat
     default: r = launch_dim<MQ_Q8_0>(p, rows, s, st); break;
   }
   if (r == MQ_OK && a.track) {
-    const int keys = std::max(32, 1024 / a.c.hkv / 32 * 32);
-    r = launch_dependent("attn_track_kernel", attn_track_kernel,
-                         dim3((a.max_len + keys - 1) / keys, (unsigned)a.S, 1), dim3(256, 1, 1), 0, s, p,
-                         rows, keys);
+    const int keys = std::max(32, kTrackThreads * kTrackKeys / a.c.hkv / 32 * 32);
+    r = launch_dependent("attn_track_kernel",
+                         w.logit_width == 2 ? attn_track_kernel<2> : attn_track_kernel<4>,
+                         dim3((a.max_len + keys - 1) / keys, (unsigned)a.S, 1),
+                         dim3(kTrackThreads, 1, 1), 0, s, p, rows, keys);
   }
   return r;
 }

@@ -90,7 +90,8 @@ __device__ __forceinline__ uint32_t kv_row32(const KvView &c, const int32_t *pag
 }
 
 // Kernels are launched with programmatic stream serialisation: they may become resident while
-// the previous kernel of the stream runs, and wait for it before their first global access.
+// the previous kernel of the stream runs, and wait for it before their first global access (the
+// weight sums' kernel of a call: before its first access to what the attention writes).
 __device__ __forceinline__ void grid_dependency() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
