@@ -2,7 +2,7 @@
 // in order.
 //
 // Choice: a weight sum maps to an unsigned key in the order of the values (NaN above all, -0 as
-// 0).  A thread block cluster of up to 8 blocks holds the candidates' keys of one kv head (a part
+// 0).  A thread block cluster of up to 16 blocks holds the candidates' keys of one kv head (a part
 // of the positions each, 16 a thread in registers and further ones in shared memory) and finds the
 // smallest key that stays by a radix selection from the top.  A histogram of the first 11 bits,
 // whose bins that are not empty are added to rank 0's through distributed shared memory (every
@@ -10,7 +10,7 @@
 // the bin that holds it.  If that has at most 4096 keys, each block reads them all and counts
 // their next 11 and 10 bits by itself; else these are counted over the cluster as well.  Rows
 // equal to the key stay from the lowest position on; ballots and the cluster's counts give every
-// row its place.  What bounds it: latency.  131072 rows of 4 heads take 20 us: a length, its pages
+// row its place.  What bounds it: latency.  131072 rows of 4 heads take 19 us: a length, its pages
 // and their sums read one after the other 5, then the cluster's barriers and reads of about 1 us
 // each (it reads 4 bytes per row; counting bit by bit from global memory, one block per head, took
 // 5.2 ms).
@@ -31,7 +31,7 @@ namespace {
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeysHeld = 48 * 1024;  // per block, in shared memory, beside 16 K in registers
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // above 8 only where the device reports such clusters
 constexpr uint32_t kList = 2 * kBins;  // keys of one bin that each block reads from the cluster's
 
 // No weight's key is 0 (its float would be a NaN): it stands for no candidate.
@@ -390,7 +390,9 @@ mq_status init_kv_evict(DeviceState *st) {
                 bytes + (int)sizeof(SelShared), st->smem_optin);
   cudaError_t e =
       cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int i = 0; i < 5 && e == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1 << i);
     cfg.blockDim = dim3(kSelThreads);
@@ -400,7 +402,10 @@ mq_status init_kv_evict(DeviceState *st) {
     attr.val.clusterDim.x = 1 << i, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&st->evict_clusters[i], evict_select_kernel, &cfg);
+    if (cudaOccupancyMaxActiveClusters(&st->evict_clusters[i], evict_select_kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      st->evict_clusters[i] = 0;
+    }
   }
   return e == cudaSuccess ? MQ_OK : cuda_fail(e, "cudaFuncSetAttribute", "evict_select_kernel");
 }
@@ -408,10 +413,11 @@ mq_status init_kv_evict(DeviceState *st) {
 mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState *st) {
   // blocks of a cluster: at least 4096 candidates each (4096 rows of 4 heads: 8.6 us by one block a
   // head, 9.5 by two; 16384: 14.7, 12.4 by two, 11.0 by four or eight; 32768: 13.4 by four, 12.5 by
-  // eight), as long as all clusters are resident at once: 15 of eight blocks here, so that 16 heads
-  // of 32768 rows take 13.6 us by four blocks each and 21.4 by eight.
+  // eight; 131072: 20.0 by eight, 18.8 by sixteen), as long as all clusters are resident at once: 15
+  // of eight blocks here, so that 16 heads of 32768 rows take 13.6 us by four blocks each and 21.4
+  // by eight.
   int ranks = 1;
-  for (int i = 1; i < 4 && (a.max_len >> i) >= 4096 && a.S * a.c.hkv <= st->evict_clusters[i]; ++i)
+  for (int i = 1; i < 5 && (a.max_len >> i) >= 4096 && a.S * a.c.hkv <= st->evict_clusters[i]; ++i)
     ranks = 1 << i;
   const int per_rank = ((a.max_len + ranks - 1) / ranks + kSelThreads - 1) / kSelThreads * kSelThreads;
   const int held = std::max(0, std::min(per_rank - 16 * kSelThreads, kKeysHeld));

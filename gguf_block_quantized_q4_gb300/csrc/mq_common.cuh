@@ -114,8 +114,9 @@ struct DeviceState {
   // for every kernel of a weight type, by type id (the GGUF number, < 32) and S = 1..16
   // (0: that cluster size cannot run); filled by init_matvec
   int mv_clusters[32][17] = {};
-  // mq_kv_evict: the most selection clusters of 1, 2, 4 and 8 thread blocks resident at once
-  int evict_clusters[4] = {};
+  // mq_kv_evict: the most selection clusters of 1, 2, 4, 8 and 16 thread blocks resident at once
+  // (0: that cluster size cannot run)
+  int evict_clusters[5] = {};
   // the stream-ordered pool of the per-call activation fragment planes of the persistent
   // matvec's Q4_K / Q5_K two-tile calls (nullptr: its x warps convert x themselves)
   cudaMemPool_t xpool = nullptr;
