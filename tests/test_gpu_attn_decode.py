@@ -109,6 +109,14 @@ def test_weight_sums(kind, dim, hq, hkv, window):
         check(p, queries(6, hq, dim, "f32", seed), "f32", dim, window=window, track=True)
 
 
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (3, 1), (5, 1), (6, 2), (12, 2), (9, 1), (12, 1),
+                                    (17, 1), (23, 1), (33, 33), (80, 40)])
+def test_weight_sums_of_all_group_sizes(hq, hkv):
+    p = Paged("f16", [0, 700, 1, 129], hkv, 64, 24, sums=True, seed=hq)
+    check(p, queries(4, hq, 64, "f32", hq), "f32", 64, track=True)
+    check(p, queries(4, hq, 64, "f32", hq + 1), "f32", 64, window=33, track=True)
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
 @pytest.mark.parametrize("S,n", [(1, 20000), (3, 9000), (1, 50001)])
 def test_long_sequences(kind, S, n):
