@@ -396,6 +396,10 @@ def mmq_blockdots(W: Weight, xq, M: int, D=None, stream=None):
 
 
 # ---- decode attention over a paged key-value cache ------------------------------------------
+#
+# What a call makes for itself (outputs, a workspace) it makes and clears under `stream`, the
+# stream that its kernels run on (default: the current one): memory of the current stream's pool
+# could have work of that stream pending, and would go back to it while the kernels still run.
 
 
 class _KVCacheStruct(ctypes.Structure):  # mq_kv_cache
@@ -555,6 +559,9 @@ def rope_store(cache: KVCache, rope: Rope, qkv, pos, slot, n_heads, bias=None, q
     rows may be strided), pos int32 [n_axes][T] (or [T] for one axis), slot int64 [T].  Returns
     the rotated queries [T][n_heads][head_dim]."""
     torch = _torch or _torch_setup()
+    if stream is not None and q is None:
+        with torch.cuda.stream(stream):
+            return rope_store(cache, rope, qkv, pos, slot, n_heads, bias)
     T, width = qkv.shape
     ld, inner = qkv.stride()
     d = cache.head_dim
@@ -614,6 +621,9 @@ def attn_decode(cache: KVCache, q, pages, lens, max_len, scale=None, window=0, t
     head_dim ** -0.5.  ws: a workspace kept from attn_workspace (else one is made for the
     call).  Returns o, of q's shape and type."""
     torch = _torch or _torch_setup()
+    if stream is not None and (ws is None or o is None):
+        with torch.cuda.stream(stream):
+            return attn_decode(cache, q, pages, lens, max_len, scale, window, track, ws, o)
     S, n_heads, d = q.shape
     io = _IO.get(q.dtype)
     if io is None or d != cache.head_dim or not q.is_contiguous():
@@ -645,6 +655,9 @@ def kv_evict(cache: KVCache, pages, lens, max_len, new_pages, keep, sink=0, rece
     """Copy the rows that stay (the first sink, the last recent and the heaviest of the rest, keep
     in all) to new_pages.  Returns (kept int32 [S][n_kv_heads][keep], new_lens int32 [S])."""
     torch = _torch or _torch_setup()
+    if stream is not None and (kept is None or new_lens is None):
+        with torch.cuda.stream(stream):
+            return kv_evict(cache, pages, lens, max_len, new_pages, keep, sink, recent, kept, new_lens)
     if lens.dtype != torch.int32 or lens.dim() != 1 or not lens.is_contiguous():
         _refuse("lens must be contiguous int32 [S]")
     S = lens.shape[0]
