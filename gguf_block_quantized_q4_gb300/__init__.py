@@ -653,7 +653,8 @@ def attn_decode(cache: KVCache, q, pages, lens, max_len, scale=None, window=0, t
 def kv_evict(cache: KVCache, pages, lens, max_len, new_pages, keep, sink=0, recent=0, kept=None,
              new_lens=None, stream=None):
     """Copy the rows that stay (the first sink, the last recent and the heaviest of the rest, keep
-    in all) to new_pages.  Returns (kept int32 [S][n_kv_heads][keep], new_lens int32 [S])."""
+    in all) to new_pages.  Returns (kept int32 [S][n_kv_heads][keep], new_lens int32 [S]); new_lens
+    may be lens itself."""
     torch = _torch or _torch_setup()
     if stream is not None and (kept is None or new_lens is None):
         with torch.cuda.stream(stream):

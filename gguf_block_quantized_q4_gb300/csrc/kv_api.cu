@@ -252,6 +252,11 @@ extern "C" mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages,
   if (sink < 0 || recent < 0 || sink > keep || recent > keep || sink + recent > keep)
     return fail(MQ_ERR_ARG, "%s: sink=%lld and recent=%lld must be >= 0 and together <= keep=%lld",
                 site, (long long)sink, (long long)recent, (long long)keep);
+  // one length is read and written by one thread: in place, but not shifted
+  const auto at = reinterpret_cast<intptr_t>(len), new_at = reinterpret_cast<intptr_t>(new_len);
+  if (at != new_at && at < new_at + 4 * S && new_at < at + 4 * S)
+    return fail(MQ_ERR_ARG, "%s: new_len=%p overlaps len=%p (it may only be the same array)", site,
+                (void *)new_len, (const void *)len);
   DeviceState *st = nullptr;
   if ((s = current_state(&st, site)) != MQ_OK) return s;
   if (S == 0) return MQ_OK;

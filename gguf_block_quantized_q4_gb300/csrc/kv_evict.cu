@@ -70,10 +70,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   cluster.barrier_arrive();  // (the totals are clear; waited for before the first is added to)
   grid_dependency();
   const int raw = a.len[s], n = clamped_len(raw, a.max_len);
-  if (h == 0 && rank == 0 && tid == 0) {
-    if (raw != n) index_error(a.status, kIdxEvictLen, raw);
-    a.new_len[s] = min(n, a.keep);
-  }
+  if (h == 0 && rank == 0 && tid == 0 && raw != n) index_error(a.status, kIdxEvictLen, raw);
   int32_t *kept = a.kept + (int64_t(s) * a.c.hkv + h) * a.keep;
   const int share = rank * kSelThreads + tid, stride = ranks * kSelThreads;
   if (n <= a.keep) {  // (the whole cluster)
@@ -314,6 +311,9 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
   const int s = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31;
   const int j = (blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS + lane;
   grid_dependency();
+  // (not by the choice, whose other blocks may still have to read the length: new_len may be len)
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+    a.new_len[s] = min(clamped_len(a.len[s], a.max_len), a.keep);
   if (j - lane >= a.keep) return;
   uint32_t from = 0, to = 0;
   bool on = false;

@@ -435,7 +435,8 @@ mq_status mq_attn_decode(const mq_kv_cache *cache, mq_type io, const void *q, vo
  * to positions 0, 1, ... of new_pages; the old pages are only read.  No page of new_pages may
  * appear in pages or twice.
  *   kept     device int32 [S][n_kv_heads][keep]: the positions that stayed, then -1; written
- *   new_len  device int32 [S]: min(n, keep); written
+ *   new_len  device int32 [S]: min(n, keep); written.  May be the array len itself (lengths
+ *            updated in place), but not overlap it otherwise
  *   sink, recent >= 0, sink + recent <= keep, 1 <= keep <= new_pages_ld*page_size
  *   max_len  bound of the lengths, <= pages_ld*page_size
  * A length outside [0, max_len] is clamped; a row whose old or new page lies outside the cache is

@@ -1,0 +1,27 @@
+"""Refusals of outputs that overlap inputs in ways the kernels cannot serve; no device needed (they
+are made before the pointers themselves are looked at)."""
+import ctypes
+
+import pytest
+
+import gguf_block_quantized_q4_gb300 as mq
+from gguf_block_quantized_q4_gb300 import build as mqbuild
+from tests.test_kv_abi_cpu import cache
+
+
+@pytest.fixture(scope="module")
+def L():
+    mqbuild.build()
+    return mq.lib()
+
+
+@pytest.mark.parametrize("S,shift,refused", [(8, 0, False), (8, 4, True), (8, -4, True), (8, 28, True),
+                                             (8, -28, True), (8, 32, False), (8, -32, False),
+                                             (1, 4, False), (1, -4, False)])
+def test_new_lengths_are_the_lengths_or_apart(L, S, shift, refused):
+    """In place or apart goes on (to the next refusal, the missing device or a NULL pointer)."""
+    base = 1 << 20
+    c = cache()
+    st = L.mq_kv_evict(ctypes.byref(c), None, 7, base, S, 100, None, 4, 64, 0, 0, None, base + shift, None)
+    assert ("overlaps" in L.mq_last_error().decode()) == refused
+    assert mq.STATUS[st] in (["MQ_ERR_ARG"] if refused else ["MQ_ERR_ARG", "MQ_ERR_STATE", "MQ_ERR_CUDA"])
