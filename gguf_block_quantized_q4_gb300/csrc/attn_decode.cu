@@ -34,7 +34,11 @@
 // the 32-element block sums in binary32, the values' scales the weights (both first scaled by
 // powers of two that put the largest weight at 2^15 and a tile's largest scale in [1/2, 1), so
 // that the second f16 part is a normal number for all but negligible products).  Each tile's
-// product is added to o by a binary32 fma (the tensor cores' own long sums may truncate).
+// product is added to o by a binary32 fma (the tensor cores' own long sums may truncate).  Operands
+// in parts do not follow the definition at infinities: of an infinite key's logit the first part
+// alone counts, and a warp whose o holds an infinity or NaN at a piece's end sums it once more from
+// the rows in memory, in binary32 throughout (values_again; the check at a piece's end and the
+// select per logit cost up to 0.3 us a call: 28/4 heads of 128, 38 x 8192 Q8_0 66.8 -> 67.6).
 //
 // Measured (28/4 heads of 128): 38 x 8192 keys f16 104.5 us (6.1 TB/s, 91% of a plain copy's rate),
 // bf16 106, Q8_0 67 (5.1 TB/s, 76%: instructions and their latencies, not the bytes; its copies
@@ -439,6 +443,67 @@ __device__ __forceinline__ void join_warps(const float *so, const float *sm, con
   }
 }
 
+// A warp's sums o of a piece once more, from the rows in memory, with weights and products in
+// binary32 as the definition has them: where the tiles' sums hold an infinity or NaN.  A weight in
+// parts does not give what the definition does there: a part that is zero or of the other sign makes
+// NaN of an infinite value.  m: the warp's maxima by row, so: its sums (what the tiles gave is
+// replaced).  Four rows at a time, lane i the dims i, 32 + i, ...; some ten times slower than the
+// tiles, and only what has such values in its rows pays it.
+template <class C, int TYPE, int D>
+__device__ __noinline__ void values_again(const Params &p, int seq, int hk, int lo, int len, int tile, int count,
+                                          int64_t head0, int rows, const float *m, float *so) {
+  constexpr int N = 4, E = D / 32;
+  const AttnArgs &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t *const pages = a.pages + seq * a.pages_ld;
+  auto value = [&](const uint8_t *plane, const __half *scales, uint32_t row, int e) {
+    const uint64_t at = uint64_t(row) * D + 32 * e + lane;
+    if (C::kQ8) return float(reinterpret_cast<const int8_t *>(plane)[at]) * __half2float(scales[uint64_t(row) * E + e]);
+    const uint16_t x = reinterpret_cast<const uint16_t *>(plane)[at];
+    return C::kBf ? __uint_as_float(uint32_t(x) << 16) : __half2float(__ushort_as_half(x));
+  };
+  for (int r0 = 0; r0 < rows; r0 += N) {
+    float q[N][E], o[N][E] = {}, low[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = min(r0 + i, rows - 1);  // (a row that is not there: the last one's work, not stored)
+      low[i] = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[i][e] = load_io1(a.q, a.io, (head0 + r) * D + 32 * e + lane) * p.scale_log2;
+    }
+    for (int t = tile; t < tile + count; ++t) {
+      const int key0 = lo + t * C::kTK + warp * C::kKeys, key1 = min(key0 + C::kKeys, len);
+      for (int key = key0; key < key1; ++key) {
+        const uint32_t row = kv_row32(a.c, pages, hk, key);
+        if (row == kNoRow) continue;
+        float s[N] = {}, v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float k = value(a.c.k, a.c.ks, row, e);
+          v[e] = value(a.c.v, a.c.vs, row, e);
+#pragma unroll
+          for (int i = 0; i < N; ++i) s[i] = fmaf(q[i][e], k, s[i]);
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1)
+#pragma unroll
+          for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float w = exp2_fast(s[i] - low[i] + C::kBias);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[i][e] = fmaf(w, v[e], o[i][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (r0 + i < rows)
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[(r0 + i) * C::kLdO + 32 * e + lane] = o[i][e];
+  }
+}
+
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kThreads, 1)
 attn_decode_kernel(const __grid_constant__ Params p) {
@@ -793,9 +858,16 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              s[m][n][w] = C::kQ8 ? acc[0][0][m][n][w]
-                                  : acc[0][0][m][n][w] + acc[1][0][m][n][w] + (acc[0][1][m][n][w] + acc[1][1][m][n][w]);
+            for (int w = 0; w < 4; ++w) {
+              if (C::kQ8) {
+                s[m][n][w] = acc[0][0][m][n][w];
+              } else {
+                // (an infinite key: the first parts' product has the sign, the others' may be NaN)
+                const float first = acc[0][0][m][n][w] + acc[1][0][m][n][w];
+                const float others = acc[0][1][m][n][w] + acc[1][1][m][n][w];
+                s[m][n][w] = first + (fabsf(first) < INFINITY ? others : 0.f);
+              }
+            }
         // ---- softmax ----
         const int key0 = now.span.lo + (now.tile + i) * C::kTK + warp * C::kKeys;
         float al[NT][2];
@@ -968,6 +1040,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
     next.tile += count - 1, next.at += count - 1;
     next_tile(next, p, C::kTK, line.gap, end);
     if (next.at < end) load_query(next);
+    bool odd = false;  // a row whose weights are numbers has a dim that is none
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -978,6 +1051,11 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         const int r = warp * C::kRows + 8 * n + 2 * t + w;
         if (g == 0) sm[r] = mx[n][w], sl[r] = l;
+        float zero[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+          zero[0] = fmaf(o[j][n][w], 0.f, zero[0]), zero[1] = fmaf(o[j][n][w + 2], 0.f, zero[1]);
+        odd |= l < INFINITY && zero[0] + zero[1] != 0.f;
 #pragma unroll
         for (int j = 0; j < KS; ++j)
           if (C::kQ8) {  // dims 16 j + 2g, 2g + 1
@@ -988,6 +1066,11 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             so[r * C::kLdO + 16 * j + 8 + g] = o[j][n][w + 2];
           }
       }
+    if (__any_sync(0xffffffffu, odd)) {
+      __syncwarp();
+      values_again<C, TYPE, D>(p, now.s, now.hk, now.span.lo, now.span.len, now.tile, count, head0, rows,
+                               sm + warp * C::kRows, so + warp * C::kRows * C::kLdO);
+    }
     __syncthreads();
     if (now.tile == 0 && count == tiles) {
       join_warps<C>(so, sm, sl, D, rows, [&](int r, int d, float4 x, float m, float l) {

@@ -138,6 +138,11 @@ __device__ __forceinline__ float4 load_io4(const void *p, int io, int64_t i) {
   const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
   return make_float4(a.x, a.y, b.x, b.y);
 }
+__device__ __forceinline__ float load_io1(const void *p, int io, int64_t i) {
+  if (io == MQ_F32) return static_cast<const float *>(p)[i];
+  const uint16_t v = static_cast<const uint16_t *>(p)[i];
+  return io == MQ_BF16 ? __uint_as_float(uint32_t(v) << 16) : __half2float(__ushort_as_half(v));
+}
 __device__ __forceinline__ uint2 pack4(float4 v, bool bf16) {  // rounded to nearest even
   uint2 u;
   if (bf16) {

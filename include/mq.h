@@ -411,6 +411,12 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * o = 0.  Sums, softmax statistics and accumulators are binary32; f16 and Q8_0 keys meet the
  * query as two f16 parts (22 bits), bf16 keys as three bf16 parts (24 bits), and the weights
  * meet the values likewise.
+ * Infinities and NaN in rows that are read (mq_rope_store rounds to them what F16 does not hold):
+ * an infinite value makes its dim of o infinite (NaN beside one of the other sign, or where its
+ * weight is zero in binary32), a NaN makes it NaN; a key whose logit is minus infinity weighs
+ * nothing (if none weighs anything, o = 0); a logit that is plus infinity or NaN makes the head's o
+ * NaN.  (To an infinite F16 key a query element below 2^-39 of its row's largest is a zero.)  The
+ * scales of Q8_0 keys must not be infinite; those that mq_rope_store writes are not.
  *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned
  *   len     device int32 [S], the rows to read, the new token's own among them; <= max_len
  *   max_len bound of the lengths on the host, <= pages_ld*page_size: it sizes the workspace
