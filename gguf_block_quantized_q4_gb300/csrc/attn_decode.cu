@@ -46,6 +46,7 @@
 // the first rows and the join); 64 ragged sequences up to 8192, f16 97 us, Q8_0 68; one sequence of
 // 37 keys, 14/2 heads of 64, 5.1.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "kv.cuh"
@@ -195,7 +196,6 @@ struct Params {
   AttnArgs a;
   int group, row_groups, units;  // query heads of a kv head; row groups of them; per sequence
   int logit_width;               // query rows per key in the logits (2, or whole fours)
-  float scale_log2;
   int *count;                    // [3][kMaxParts]: a unit's first group, its others, its groups
   // results of blocks (two each: a piece whose unit began before the block; one whose unit begins
   // in it), then of groups (by their first block, two each: a unit's others, its first)
@@ -469,7 +469,7 @@ __device__ __noinline__ void values_again(const Params &p, int seq, int hk, int 
       const int r = min(r0 + i, rows - 1);  // (a row that is not there: the last one's work, not stored)
       low[i] = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-      for (int e = 0; e < E; ++e) q[i][e] = load_io1(a.q, a.io, (head0 + r) * D + 32 * e + lane) * p.scale_log2;
+      for (int e = 0; e < E; ++e) q[i][e] = load_io1(a.q, a.io, (head0 + r) * D + 32 * e + lane) * a.scale * kLog2e;
     }
     for (int t = tile; t < tile + count; ++t) {
       const int key0 = lo + t * C::kTK + warp * C::kKeys, key1 = min(key0 + C::kKeys, len);
@@ -672,18 +672,23 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       if (r >= C::kRows) break;
       const float4 u = query[i0][0], v = query[i0][1];
       const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-      int e = 0;
-      if (!C::kBf) {  // a power of two that puts the row's largest element in [2^14, 2^15)
-        float top = 0.f;
+      // a power of two that puts the row's largest element in [2^14, 2^15); bf16 has binary32's range:
+      // only what its ends are near is put about 1
+      float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        if (top > 0.f && top < INFINITY) e = min(max(141 - (int)(__float_as_uint(top) >> 23), -100), 100);
-      }
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      const int power = (int)(__float_as_uint(top) >> 23) - 127;
+      int e = 0;
+      if (top > 0.f && top < INFINITY && (!C::kBf || abs(power) > 60))
+        e = min(max((C::kBf ? 0 : 14) - power, -126), 126);
       const float up = __uint_as_float(uint32_t(127 + e) << 23);
-      // (Q8_0 keys enter the product as 2^-24 (v + 128), see below)
-      if (lane == 0)
-        sfac[r] = p.scale_log2 * __uint_as_float(uint32_t(127 - e) << 23) * (C::kQ8 ? 0x1p24f : 1.f);
+      // (Q8_0 keys enter the product as 2^-24 (v + 128), see below; a factor past binary32 has logits
+      // there or zeros, and a finite one in its place leaves their order)
+      if (lane == 0) {
+        const float f = a.scale * __uint_as_float(uint32_t(127 - e) << 23) * (kLog2e * (C::kQ8 ? 0x1p24f : 1.f));
+        sfac[r] = fminf(fmaxf(f, -FLT_MAX), FLT_MAX);
+      }
       if (lane < D / 8) {
         uint32_t w[4][C::kParts];
 #pragma unroll
@@ -1284,7 +1289,6 @@ mq_status launch_attn_decode(const AttnArgs &a, cudaStream_t s, const DeviceStat
   p.row_groups = (p.group + rows - 1) / rows;
   p.units = a.c.hkv * p.row_groups;
   p.logit_width = w.logit_width;
-  p.scale_log2 = a.scale * kLog2e;
   p.count = reinterpret_cast<int *>(a.ws);
   p.blocks = w.blocks;
   p.piece_ml = reinterpret_cast<float2 *>(a.ws + w.piece_ml);

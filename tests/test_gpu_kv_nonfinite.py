@@ -1,5 +1,6 @@
-"""mq_attn_decode on infinities and NaN in rows that are read, against the 64-bit definition: which
-outputs are infinite, which are NaN, and the values of all others."""
+"""mq_attn_decode on infinities and NaN in rows that are read, and on queries near the ends of
+binary32, against the 64-bit definition: which outputs are infinite, which are NaN, and the values
+of all others."""
 import numpy as np
 import pytest
 
@@ -151,4 +152,30 @@ def test_no_key_weighs_anything(kind):
         put(p, "k", 0, 0, i, 0, INF)
     o = mq.attn_decode(p.cache, q.cuda(), p.pages, p.lens, p.max_len)
     assert not o[0].any() and o[1].all()
+    mq.stream_status()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("power", [127, 126, 120, 116, 100, -100, -116, -120, -125])
+def test_queries_near_the_ends_of_binary32(kind, power):
+    """Scaled queries with the inverse scale are the same attention."""
+    p = Paged(kind, [200, 33], 1, 128, 16, seed=9)
+    q = queries(2, 3, 128, 10)
+    q /= q.abs().max(-1, keepdim=True).values * 1.01  # (largest element 0.99)
+    check(p, q * 2.0 ** power, scale=2.0 ** -power)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
+def test_one_key_outweighs_all(kind):
+    """Logits of 2^90 and more apart: the largest takes all, and o is its value (2^-17: the bound's
+    part that does not come from the logits)."""
+    p = Paged(kind, [200], 1, 128, 16, seed=11)
+    q = queries(1, 3, 128, 12)
+    page, slot = kv.place(p.pages_host[0], 16, np.arange(200))
+    k, v = (kv.values(p.host, n)[page, 0, slot] for n in ("k", "v"))
+    for power, scale in ((100, 0.1), (110, 0.1), (110, -0.1), (118, 0.01), (0, 2.0 ** 110), (126, 2.0 ** -20)):
+        x = q * 2.0 ** power / 8
+        o = mq.attn_decode(p.cache, x.cuda(), p.pages, p.lens, p.max_len, scale=scale)[0].cpu().numpy()
+        want = v[(scale * (x[0].double().numpy() @ k.T)).argmax(-1)]
+        assert (np.abs(o - want) <= 2.0 ** -17 * np.abs(want)).all(), (power, scale)
     mq.stream_status()
