@@ -61,7 +61,7 @@ inline int kv_row_bytes(int type, int dim) { return type == MQ_Q8_0 ? dim : 2 * 
 
 __device__ __forceinline__ void index_error(int *status, int code, int64_t value) {
   if (atomicCAS(status + kStatusIndexWord, 0, code) == 0)
-    atomicExch(status + kStatusIndexWord + 1, (int)value);
+    atomicExch(reinterpret_cast<unsigned long long *>(status + kStatusIndexWord + 2), (unsigned long long)value);
 }
 
 // A sequence's length, clamped to [0, max_len].

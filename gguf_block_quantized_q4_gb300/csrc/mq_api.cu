@@ -722,7 +722,7 @@ extern "C" mq_status mq_stream_status(mq_stream stream) {
   mq_status s;
   if ((s = current_state(&st, site)) != MQ_OK) return s;
   CK(cudaStreamSynchronize((cudaStream_t)stream), site);
-  int h[4] = {0, 0, 0, 0};
+  int h[6] = {};
   CK(cudaMemcpy(h, st->status, sizeof(h), cudaMemcpyDeviceToHost), site);
   if (h[0] != 0) {
     CK(cudaMemset(st->status, 0, 8), site);
@@ -730,9 +730,11 @@ extern "C" mq_status mq_stream_status(mq_stream stream) {
                 site, h[0], h[1]);
   }
   if (h[kStatusIndexWord] != 0) {
-    CK(cudaMemset(st->status + kStatusIndexWord, 0, 8), site);
-    return fail(MQ_ERR_INDEX, "%s: %s %d is outside its range; what it stands for was left out",
-                site, index_error_name(h[kStatusIndexWord]), h[kStatusIndexWord + 1]);
+    CK(cudaMemset(st->status + kStatusIndexWord, 0, 16), site);
+    int64_t value;
+    memcpy(&value, h + kStatusIndexWord + 2, sizeof(value));
+    return fail(MQ_ERR_INDEX, "%s: %s %lld is outside its range; what it stands for was left out",
+                site, index_error_name(h[kStatusIndexWord]), (long long)value);
   }
   return MQ_OK;
 }

@@ -91,8 +91,8 @@ constexpr int kMaxB = 8;
 constexpr int kRowGroup = 128; // decode-plane row group (rows per matvec CTA)
 constexpr int kChunk = 256;    // decode-plane K chunk
 constexpr int kStatusTimeout = 1;
-// words of the device status: 0, 1 a timeout's code and site; 2, 3 an index error's code
-// (IndexError) and the value met
+// words of the device status: 0, 1 a timeout's code and site; 2 an index error's code
+// (IndexError), 4, 5 the value met, in 64 bits
 constexpr int kStatusIndexWord = 2;
 
 // ---- per-thread error reporting ------------------------------------------
