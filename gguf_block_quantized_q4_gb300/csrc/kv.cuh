@@ -69,17 +69,8 @@ __device__ __forceinline__ int clamped_len(int len, int max_len) {
   return min(max(len, 0), max_len);
 }
 
-// The row of (head, position), or -1 where its page lies outside the cache.
-__device__ __forceinline__ int64_t kv_row(const KvView &c, const int32_t *pages,
-                                          int head, int pos) {
-  const uint32_t pi = quotient((uint32_t)pos, c.page);
-  const int64_t page = pages[pi];
-  if (page < 0 || page >= c.n_pages) return -1;
-  return page * c.page_stride + head * c.head_stride +
-         int64_t((uint32_t)pos - pi * c.page.d) * c.slot_stride;
-}
-
-// The same in 32 bits (a cache spans at most 2^32 - 2 rows); kNoRow for -1.
+// The row of (head, position), kNoRow where its page lies outside the cache.  In 32 bits: a cache
+// spans at most 2^32 - 2 rows.
 constexpr uint32_t kNoRow = 0xffffffffu;
 __device__ __forceinline__ uint32_t kv_row32(const KvView &c, const int32_t *pages, int head, int pos) {
   const uint32_t pi = quotient((uint32_t)pos, c.page);
