@@ -427,11 +427,18 @@ def _torch_setup():
     _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     # an output (shape, strides, dtype) on the current device, which the calls require to be the
-    # cache's, straight from the allocator (3.4 us less per call)
-    guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
-    _empty_cuda = getattr(guards, "_empty_strided_cuda", None) or (
-        lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype,
-                                                          device="cuda"))
+    # cache's, straight from the allocator (3.4 us less per call) where a trial shows that its entry,
+    # which is torch's own business, is there and does that
+    def empty(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    _empty_cuda = empty
+    try:
+        direct = torch._C._dynamo.guards._empty_strided_cuda
+        trial = direct((2, 1), (1, 1), torch.int32)
+        if trial.shape == (2, 1) and trial.dtype == torch.int32:
+            _empty_cuda = direct
+    except Exception:
+        pass
     _torch = torch
     return torch
 
