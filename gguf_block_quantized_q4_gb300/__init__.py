@@ -543,9 +543,10 @@ def rope_axes(sections, weave=False):
 class Rope:
     """A rotation (mq_rope): table f32 [max_pos][pairs of a head][2] (rope_table), axis: the
     position axis of each pair (default: all on axis 0); pairs: dims (2i, 2i+1) instead of
-    (i, i + rot_dim/2)."""
+    (i, i + rot_dim/2); n_axes: the axes that positions are given on (default: up to the last one
+    that a pair turns by)."""
 
-    def __init__(self, table, axis=None, pairs=False):
+    def __init__(self, table, axis=None, pairs=False, n_axes=None):
         torch = _torch or _torch_setup()
         if (table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous()
                 or not table.is_cuda or table.dtype != torch.float32):
@@ -554,7 +555,10 @@ class Rope:
         axis = bytes(half) if axis is None else bytes(axis)  # (refuses what is no small integer)
         if len(axis) != half or half > 128 or max(axis, default=0) > 3:
             _refuse("axis names one of up to 4 axes for each of at most 128 pairs")
-        self.table, self.axis, self.n_axes = table, list(axis), max(axis, default=0) + 1
+        used = max(axis, default=0) + 1
+        if n_axes is not None and not used <= n_axes <= 4:
+            _refuse(f"n_axes={n_axes}: the pairs turn by {used} axes, and there are at most 4")
+        self.table, self.axis, self.n_axes = table, list(axis), n_axes or used
         self._c = _RopeStruct(table.data_ptr(), table.shape[0], 2 * half, int(pairs), self.n_axes)
         ctypes.memmove(self._c.axis, axis, half)
         self._ref = ctypes.addressof(self._c)
