@@ -217,9 +217,18 @@ def register_ffn_gu(qtype, gate, up, N, K, flags=REG_DEFAULT) -> FfnGuWeight:
     return FfnGuWeight(qtype, gate, up, N, K, flags)
 
 
+# What a call makes for itself (outputs, buffers, a workspace, a copy of a strided input) it makes and
+# clears under `stream`, the stream that its kernels run on (default: the current one): memory of
+# the current stream's pool could have work of that stream pending, and would go back to it while the
+# kernels still run.
+
+
 def ffn_gu_matvec(W: FfnGuWeight, x, h=None, stream=None):
     """h[B][N] = silu(W_gate x) * (W_up x) (x: CUDA f32 [B][K] or [K])."""
     import torch
+    if stream is not None and (h is None or not x.is_contiguous()):
+        with torch.cuda.stream(stream):
+            return ffn_gu_matvec(W, x, h)
     x2 = x.reshape(-1, W.K)
     B = x2.shape[0]
     if h is None:
@@ -232,6 +241,9 @@ def ffn_gu_matvec(W: FfnGuWeight, x, h=None, stream=None):
 def ffn_gu_mmq(W: FfnGuWeight, xq, M: int, h=None, stream=None):
     """h[M][N] = silu(W_gate a) * (W_up a) for the quantised activations xq."""
     import torch
+    if stream is not None and h is None:
+        with torch.cuda.stream(stream):
+            return ffn_gu_mmq(W, xq, M)
     if h is None:
         h = torch.empty((M, W.N), dtype=torch.float32, device=xq.device)
     _check(lib().mq_ffn_gu_mmq(W.qtype, W.handle, _ptr(xq), _ptr(h), M, W.N, W.K,
@@ -242,6 +254,9 @@ def ffn_gu_mmq(W: FfnGuWeight, xq, M: int, h=None, stream=None):
 def matvec(W: Weight, x, y=None, stream=None):
     """y[B][N] = dequant(W) @ x[B][K]^T (x: CUDA f32 [B][K] or [K])."""
     import torch
+    if stream is not None and (y is None or not x.is_contiguous()):
+        with torch.cuda.stream(stream):
+            return matvec(W, x, y)
     x2 = x.reshape(-1, W.K)
     B = x2.shape[0]
     if y is None:
@@ -316,6 +331,9 @@ def act_views_min(xq, M: int, K: int):
 def quantize_act(x, xq=None, stream=None):
     """Quantise CUDA f32 x[M][K]; returns the uint8 xq buffer."""
     import torch
+    if stream is not None and xq is None:
+        with torch.cuda.stream(stream):
+            return quantize_act(x)
     M, K = x.shape
     if xq is None:
         xq = torch.empty(act_bytes(M, K), dtype=torch.uint8, device=x.device)
@@ -325,6 +343,9 @@ def quantize_act(x, xq=None, stream=None):
 
 def mmq(W: Weight, xq, M: int, y=None, stream=None):
     import torch
+    if stream is not None and y is None:
+        with torch.cuda.stream(stream):
+            return mmq(W, xq, M)
     if y is None:
         y = torch.empty((M, W.N), dtype=torch.float32, device=xq.device)
     _check(lib().mq_mmq(W.qtype, W.handle, _ptr(xq), _ptr(y), M, W.N, W.K, _stream(stream)))
@@ -342,6 +363,9 @@ def mmq_fused(W: Weight, x, xq=None, y=None, stream=None):
     """Quantise x (f32 [M][K] on the device) into xq and run the MMQ, in one kernel.
     Returns (y, xq); xq then holds what quantize_act writes."""
     import torch
+    if stream is not None and (xq is None or y is None):
+        with torch.cuda.stream(stream):
+            return mmq_fused(W, x, xq, y)
     M = x.shape[0]
     if xq is None:
         xq = act_buffer(M, W.K, x.device)
@@ -378,6 +402,9 @@ def mmq_fused_static(W: Weight, x, y=None, stream=None):
     """mmq_fused with the library's static scratch in place of an xq buffer (allocates
     nothing on the device; one call in flight at a time).  Returns y."""
     import torch
+    if stream is not None and y is None:
+        with torch.cuda.stream(stream):
+            return mmq_fused_static(W, x)
     M = x.shape[0]
     if y is None:
         y = torch.empty((M, W.N), dtype=torch.float32, device=x.device)
@@ -388,6 +415,9 @@ def mmq_fused_static(W: Weight, x, y=None, stream=None):
 
 def mmq_blockdots(W: Weight, xq, M: int, D=None, stream=None):
     import torch
+    if stream is not None and D is None:
+        with torch.cuda.stream(stream):
+            return mmq_blockdots(W, xq, M)
     if D is None:
         D = torch.empty((M, W.N, W.K // 32), dtype=torch.int32, device=xq.device)
     _check(lib().mq_mmq_blockdots(W.qtype, W.handle, _ptr(xq), _ptr(D), M, W.N, W.K,
@@ -396,10 +426,6 @@ def mmq_blockdots(W: Weight, xq, M: int, D=None, stream=None):
 
 
 # ---- decode attention over a paged key-value cache ------------------------------------------
-#
-# What a call makes for itself (outputs, a workspace) it makes and clears under `stream`, the
-# stream that its kernels run on (default: the current one): memory of the current stream's pool
-# could have work of that stream pending, and would go back to it while the kernels still run.
 
 
 class _KVCacheStruct(ctypes.Structure):  # mq_kv_cache
