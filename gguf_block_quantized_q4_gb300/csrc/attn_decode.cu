@@ -187,9 +187,10 @@ struct Shape {
   static constexpr int kSmem = smem(kWarps, kStages), kThreads = 32 * kWarps;
   static constexpr int kTK = kKeys * kWarps;    // keys of a tile
   static_assert(smem(kWarps, kStages) <= kSmemMax, "shared memory");
-  // exp2 of a weight's exponent in the f16 parts: weights in (0, 2^15], so that the second part
-  // of all but negligible weights is a normal f16
-  static constexpr float kBias = kBf ? 0.f : 15.f;
+  // the f16 parts hold weights in (0, 2^15], so that the second part of all but negligible weights is
+  // a normal f16.  (Multiplied in after the exponential: added to its argument it would round that
+  // to 2^-21 where s - m itself is nearly exact.)
+  static constexpr float kUnit = kBf ? 1.f : 0x1p15f;
 };
 
 struct Params {
@@ -203,7 +204,7 @@ struct Params {
   float2 *piece_ml;              // [4][blocks][rows]: maximum, sum
   int blocks;
   float *logits;                 // [S][units][max_len][logit_width], or nullptr
-  float2 *stats;                 // [S][units][rows]: (m - bias, 1 / l)
+  float2 *stats;                 // [S][units][rows]: maximum, weight of exp2(0)
 };
 
 // ---- the schedule -------------------------------------------------------------------------
@@ -330,7 +331,7 @@ __device__ __forceinline__ void finish(const Params &p, int64_t head0, int64_t u
   store_io4(p.a.o, p.a.io, (head0 + r) * dim + d,
             make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
   if (d == 0 && p.stats)
-    p.stats[unit_id * C::kRows + r] = make_float2((m == -INFINITY ? 0.f : m) - C::kBias, inv);
+    p.stats[unit_id * C::kRows + r] = make_float2(m == -INFINITY ? 0.f : m, inv * C::kUnit);
 }
 
 // Counts a piece in, of `others` + 1; true where it is the last.  One thread calls it, after a
@@ -490,7 +491,7 @@ __device__ __noinline__ void values_again(const Params &p, int seq, int hk, int 
           for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float w = exp2_fast(s[i] - low[i] + C::kBias);
+          const float w = exp2_fast(s[i] - low[i]) * C::kUnit;
 #pragma unroll
           for (int e = 0; e < E; ++e) o[i][e] = fmaf(w, v[e], o[i][e]);
         }
@@ -922,8 +923,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             float sum = 0.f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              s[m][n][w] = exp2_fast(s[m][n][w] - low + C::kBias);
-              s[m][n][w + 2] = exp2_fast(s[m][n][w + 2] - low + C::kBias);
+              s[m][n][w] = exp2_fast(s[m][n][w] - low) * C::kUnit;
+              s[m][n][w + 2] = exp2_fast(s[m][n][w + 2] - low) * C::kUnit;
               sum += s[m][n][w] + s[m][n][w + 2];
             }
             ls[n][w] = fmaf(ls[n][w], al[n][w], sum);
@@ -1125,7 +1126,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   }
 }
 
-// The weight sums: w = exp2(s - (m - bias)) / l per query row, summed over the rows of the kv
+// The weight sums: w = exp2(s - m) / l per query row, summed over the rows of the kv
 // head in their order.  Bounded by latency (a few bytes a row): a thread has four keys of a kv
 // head side by side, and finds their rows and reads their sums before it waits for the attention,
 // which writes neither (nor the tables: what came before the attention has ended when all of its
