@@ -59,9 +59,11 @@ struct KvView {
 // A row's elements in bytes (the scales of Q8_0 lie in their own plane).
 inline int kv_row_bytes(int type, int dim) { return type == MQ_Q8_0 ? dim : 2 * dim; }
 
+// The first error's thread alone writes the value.  (By a store: an atomic exchange here, on a path
+// that no valid call takes, cost mq_rope_store 5 us of 64 at 16384 bf16 tokens, out of line 4.)
 __device__ __forceinline__ void index_error(int *status, int code, int64_t value) {
   if (atomicCAS(status + kStatusIndexWord, 0, code) == 0)
-    atomicExch(reinterpret_cast<unsigned long long *>(status + kStatusIndexWord + 2), (unsigned long long)value);
+    *reinterpret_cast<int64_t *>(status + kStatusIndexWord + 2) = value;
 }
 
 // A sequence's length, clamped to [0, max_len].
