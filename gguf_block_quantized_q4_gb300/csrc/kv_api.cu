@@ -93,6 +93,12 @@ mq_status cache_view(const char *site, const mq_kv_cache *c, bool sums, int dev,
   return MQ_OK;
 }
 
+// Whether two ranges of bytes share any.
+bool overlap(const void *a, uint64_t a_bytes, const void *b, uint64_t b_bytes) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes && b_bytes && (x < y ? y - x < a_bytes : x - y < b_bytes);
+}
+
 mq_status check_lengths(const char *site, const mq_kv_cache *c, int64_t S, int64_t max_len,
                         int64_t pages_ld) {
   if (S < 0 || S > 65535) return fail(MQ_ERR_ARG, "%s: S=%lld outside [0, 65535]", site, (long long)S);
@@ -139,6 +145,10 @@ extern "C" mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope
   if (ld * esize % 16)
     return fail(MQ_ERR_ALIGN, "%s: rows of ld=%lld elements are not 16-byte aligned", site,
                 (long long)ld);
+  // a thread writes the queries where it read them only if there is one row and q begins with it
+  if (T && !(T == 1 && q == qkv) &&
+      overlap(q, T * n_heads * cache->head_dim * esize, qkv, uint64_t((T - 1) * ld + width) * esize))
+    return fail(MQ_ERR_ARG, "%s: q=%p overlaps qkv=%p (only one token's may, from the row's start)", site, q, qkv);
   DeviceState *st = nullptr;
   if ((s = current_state(&st, site)) != MQ_OK) return s;
   if (T == 0) return MQ_OK;
@@ -253,8 +263,7 @@ extern "C" mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages,
     return fail(MQ_ERR_ARG, "%s: sink=%lld and recent=%lld must be >= 0 and together <= keep=%lld",
                 site, (long long)sink, (long long)recent, (long long)keep);
   // one length is read and written by one thread: in place, but not shifted
-  const auto at = reinterpret_cast<intptr_t>(len), new_at = reinterpret_cast<intptr_t>(new_len);
-  if (at != new_at && at < new_at + 4 * S && new_at < at + 4 * S)
+  if (len != new_len && overlap(len, 4 * S, new_len, 4 * S))
     return fail(MQ_ERR_ARG, "%s: new_len=%p overlaps len=%p (it may only be the same array)", site,
                 (void *)new_len, (const void *)len);
   DeviceState *st = nullptr;

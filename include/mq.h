@@ -380,7 +380,8 @@ typedef struct {
  * the first (n_heads + 2*n_kv_heads)*head_dim are read: query heads, key heads, value heads
  * (the fused attn_qkv product, "CUDA Backend Design" §4.6).  bias: f32, one per element of a
  * row, or NULL.  pos: int32 [n_axes][T].  slot: int64 [T], page*page_size + offset; a negative
- * slot stores nothing for its token.  q: device [T][n_heads*head_dim] of type io, written.
+ * slot stores nothing for its token.  q: device [T][n_heads*head_dim] of type io, written; apart
+ * from qkv, but a single token's may be the start of its row.
  * In binary32, every step rounded to nearest even and none contracted:
  *     a = x + bias;  r0 = a0*c - a1*s;  r1 = a0*s + a1*c
  * then rounded to io (queries) or to the cache's type (keys, and the values, which are not

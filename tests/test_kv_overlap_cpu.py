@@ -6,7 +6,7 @@ import pytest
 
 import gguf_block_quantized_q4_gb300 as mq
 from gguf_block_quantized_q4_gb300 import build as mqbuild
-from tests.test_kv_abi_cpu import cache
+from tests.test_kv_abi_cpu import cache, rope
 
 
 @pytest.fixture(scope="module")
@@ -23,5 +23,21 @@ def test_new_lengths_are_the_lengths_or_apart(L, S, shift, refused):
     base = 1 << 20
     c = cache()
     st = L.mq_kv_evict(ctypes.byref(c), None, 7, base, S, 100, None, 4, 64, 0, 0, None, base + shift, None)
+    assert ("overlaps" in L.mq_last_error().decode()) == refused
+    assert mq.STATUS[st] in (["MQ_ERR_ARG"] if refused else ["MQ_ERR_ARG", "MQ_ERR_STATE", "MQ_ERR_CUDA"])
+
+
+@pytest.mark.parametrize("T,shift,refused", [(1, 0, False),            # in place: a thread its own elements
+                                             (1, 16, True), (1, -16, True),
+                                             (1, 36 * 128 * 2, False), (1, -28 * 128 * 2, False),
+                                             (3, 0, True),             # a token's queries over another's row
+                                             (3, 2 * 40 * 128 * 2, True), (3, -3 * 28 * 128 * 2 + 16, True),
+                                             (3, (2 * 40 + 36) * 128 * 2, False), (3, -3 * 28 * 128 * 2, False)])
+def test_rotated_queries_are_apart_from_the_rows(L, T, shift, refused):
+    """Rows of 36 heads, 40 heads from one to the next, f16; queries of 28 heads."""
+    base = 1 << 24
+    c, r = cache(), rope()
+    st = L.mq_rope_store(ctypes.byref(c), ctypes.byref(r), mq.F16, base, 40 * 128, None, None, None,
+                         base + shift, T, 28, None)
     assert ("overlaps" in L.mq_last_error().decode()) == refused
     assert mq.STATUS[st] in (["MQ_ERR_ARG"] if refused else ["MQ_ERR_ARG", "MQ_ERR_STATE", "MQ_ERR_CUDA"])
