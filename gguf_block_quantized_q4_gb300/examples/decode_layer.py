@@ -22,6 +22,10 @@ class DecodeLayer:
 
     def __init__(self, wqkv, wo, n_seqs, n_heads, n_kv_heads, head_dim, limit, keep, sink=4,
                  recent=16, kind=mq.Q8_0, page_size=16, bias=None, max_pos=32768, freq_base=1e6):
+        if not 0 < keep < limit:
+            raise ValueError(f"keep={keep} must leave room below limit={limit}")
+        if sink < 0 or recent < 0 or sink + recent > keep:
+            raise ValueError(f"sink={sink} and recent={recent} are more than keep={keep}")
         self.wqkv, self.wo, self.n_heads, self.bias = wqkv, wo, n_heads, bias
         self.limit, self.keep, self.sink, self.recent = limit, keep, sink, recent
         self.width = -(-limit // page_size)
@@ -45,6 +49,8 @@ class DecodeLayer:
         """Room for the next token of every sequence: evicts, takes pages, and writes the lengths,
         positions and slots that the device calls read."""
         ps = self.cache.page_size
+        if self.seen == self.rope.table.shape[0]:
+            raise ValueError(f"position {self.seen} is past the rotation's table")
         for s, n in enumerate(self.held):
             if n == self.limit:
                 self._evict(s)
