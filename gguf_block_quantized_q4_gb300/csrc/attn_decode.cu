@@ -6,7 +6,10 @@
 // unnormalised o, which pieces of the length join as
 //     M = max m_i,  L = sum l_i exp2(m_i - M),  o = sum o_i exp2(m_i - M) / L.
 //
-// What bounds it: the bytes of K and V, each read once.  A group of query heads shares them, so
+// What bounds it: the bytes of K and V.  A group of up to 16 query heads (8 for heads of 192 and
+// 256) shares one reading of them; a larger one is several row groups, each a unit of its own that
+// reads them again (38 x 8192, F16: 96/4 heads of 128 207 us, 64/4 107; 64/4 heads of 256 405, 8/4
+// 206).  A group's rows share the keys, so
 // both products are matrix products with 8 (or 16) columns: S^T = K Q^T and O^T = V^T P^T on
 // mma.sync m16n8k16, keys (and dims of V^T) as the 16-row operand, the query rows as the 8
 // columns.  (A tcgen05 tile has 64 or 128 rows and at least 8 columns of its own accumulator
@@ -36,15 +39,18 @@
 // that the second f16 part is a normal number for all but negligible products).  Each tile's
 // product is added to o by a binary32 fma (the tensor cores' own long sums may truncate).  Operands
 // in parts do not follow the definition at infinities: of an infinite key's logit the first part
-// alone counts, and a warp whose o holds an infinity or NaN at a piece's end sums it once more from
-// the rows in memory, in binary32 throughout (values_again; the check at a piece's end and the
-// select per logit cost up to 0.3 us a call: 28/4 heads of 128, 38 x 8192 Q8_0 66.8 -> 67.6).
+// alone counts, and a warp whose o holds an infinity or NaN at a piece's end sums what is infinite or
+// NaN among its rows once more, in binary32 (sum_infinities).  The check at a piece's end and the
+// select per logit cost nothing at 38 x 8192 (28/4 heads of 128) and up to 0.5 us where a block has
+// few tiles (16 x 4096, 16/1 heads of 128, F16: 18.3 -> 18.6 us).
 //
-// Measured (28/4 heads of 128): 38 x 8192 keys f16 104.5 us (6.1 TB/s, 91% of a plain copy's rate),
-// bf16 106, Q8_0 67 (5.1 TB/s, 76%: instructions and their latencies, not the bytes; its copies
-// alone take 55); 131072 bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start,
-// the first rows and the join); 64 ragged sequences up to 8192, f16 97 us, Q8_0 68; one sequence of
-// 37 keys, 14/2 heads of 64, 5.1.
+// Measured (28/4 heads of 128; from one card to another 3% apart): 38 x 8192 keys f16 104.5 to 108 us
+// (5.9 to 6.1 TB/s, 88 to 91% of a plain copy's rate), bf16 104.7 to 108, Q8_0 67 (5.1 TB/s, 76%: not
+// the bytes, and no pipe full: half of the issue slots stay empty, two warps per scheduler waiting
+// on fixed latencies of conversions, shared memory and products; its copies alone take 55); 131072
+// bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start, the first rows and the
+// join); 64 ragged sequences up to 8192, f16 97 to 100 us, Q8_0 67.5; one sequence of 37 keys, 14/2
+// heads of 64, 5.1.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -444,64 +450,93 @@ __device__ __forceinline__ void join_warps(const float *so, const float *sm, con
   }
 }
 
-// A warp's sums o of a piece once more, from the rows in memory, with weights and products in
-// binary32 as the definition has them: where the tiles' sums hold an infinity or NaN.  A weight in
-// parts does not give what the definition does there: a part that is zero or of the other sign makes
-// NaN of an infinite value.  m: the warp's maxima by row, so: its sums (what the tiles gave is
-// replaced).  Four rows at a time, lane i the dims i, 32 + i, ...; some ten times slower than the
-// tiles, and only what has such values in its rows pays it.
+// A warp's sums o of a piece where they hold an infinity or NaN that its weights do not explain: a
+// weight in parts does not give what the definition does (a part that is zero or of the other sign
+// makes NaN of an infinite value).  A dim's sum with such a value among its rows is that of these
+// values alone, each times its weight in binary32.  The warp's rows of V (of Q8_0 their scales) are
+// read again for them; of a row that has one, K too.  m: the warp's maxima by row, so: its sums.  Lane
+// i has the dims i, 32 + i, ...  Only calls with such values come here: a call of 38 x 8192 (28/4 heads
+// of 128) takes 210 us with one of them instead of 111 (Q8_0 99 instead of 72), 3.3 ms with one in
+// every row.  (Summing all of the warp's rows once more took 1.2 ms with one and 1.6 with all.)
 template <class C, int TYPE, int D>
-__device__ __noinline__ void values_again(const Params &p, int seq, int hk, int lo, int len, int tile, int count,
-                                          int64_t head0, int rows, const float *m, float *so) {
-  constexpr int N = 4, E = D / 32;
+__device__ __noinline__ void sum_infinities(const Params &p, int seq, int hk, int lo, int len, int tile, int count,
+                                            int64_t head0, int rows, const float *m, float *so) {
+  constexpr int N = 4, E = D / 32;  // query rows at a time, dims of a lane
   const AttnArgs &a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t *const pages = a.pages + seq * a.pages_ld;
+  constexpr uint32_t kTop = C::kBf ? 0x7f80u : 0x7c00u;  // the exponent of what is no number
+  auto is_odd = [](uint32_t x) { return (x & kTop) == kTop; };
   auto value = [&](const uint8_t *plane, const __half *scales, uint32_t row, int e) {
     const uint64_t at = uint64_t(row) * D + 32 * e + lane;
     if (C::kQ8) return float(reinterpret_cast<const int8_t *>(plane)[at]) * __half2float(scales[uint64_t(row) * E + e]);
     const uint16_t x = reinterpret_cast<const uint16_t *>(plane)[at];
     return C::kBf ? __uint_as_float(uint32_t(x) << 16) : __half2float(__ushort_as_half(x));
   };
-  for (int r0 = 0; r0 < rows; r0 += N) {
-    float q[N][E], o[N][E] = {}, low[N];
+  uint32_t seen = 0;  // this lane's dims that have had such a value
+  for (int t = tile; t < tile + count; ++t) {
+    const int key = lo + t * C::kTK + warp * C::kKeys + lane;
+    const uint32_t my_row = lane < C::kKeys && key < len ? kv_row32(a.c, pages, hk, key) : kNoRow;
+    uint32_t odd = 0;  // keys with such values
+    if (C::kQ8) {
+      if (my_row != kNoRow)
+        for (int e = 0; e < E; ++e)
+          if (is_odd(__half_as_ushort(a.c.vs[uint64_t(my_row) * E + e]))) odd = 1u << lane;
+    } else {
+      constexpr int CH = C::kRow / 16, STEPS = C::kKeys * CH / 32, U = STEPS % 8 == 0 ? 8 : STEPS % 6 == 0 ? 6 : 4;
+      static_assert(STEPS % U == 0, "whole rounds");
+      for (int i0 = 0; i0 < STEPS; i0 += U) {
+        uint4 v[U];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = min(r0 + i, rows - 1);  // (a row that is not there: the last one's work, not stored)
-      low[i] = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-      for (int e = 0; e < E; ++e) q[i][e] = load_io1(a.q, a.io, (head0 + r) * D + 32 * e + lane) * a.scale * kLog2e;
-    }
-    for (int t = tile; t < tile + count; ++t) {
-      const int key0 = lo + t * C::kTK + warp * C::kKeys, key1 = min(key0 + C::kKeys, len);
-      for (int key = key0; key < key1; ++key) {
-        const uint32_t row = kv_row32(a.c, pages, hk, key);
-        if (row == kNoRow) continue;
-        float s[N] = {}, v[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float k = value(a.c.k, a.c.ks, row, e);
-          v[e] = value(a.c.v, a.c.vs, row, e);
-#pragma unroll
-          for (int i = 0; i < N; ++i) s[i] = fmaf(q[i][e], k, s[i]);
+        for (int i = 0; i < U; ++i) {
+          const int at = (i0 + i) * 32 + lane;
+          const uint32_t row = __shfl_sync(0xffffffffu, my_row, at / CH);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (row != kNoRow)
+            v[i] = *reinterpret_cast<const uint4 *>(a.c.v + uint64_t(row) * C::kRow + at % CH * 16);
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (is_odd(w[q]) || is_odd(w[q] >> 16)) odd |= 1u << ((i0 + i) * 32 + lane) / CH;
+        }
+      }
+    }
+    for (odd = __reduce_or_sync(0xffffffffu, odd); odd; odd &= odd - 1) {
+      const uint32_t row = __shfl_sync(0xffffffffu, my_row, __ffs(odd) - 1);
+      float k[E], v[E];
+      uint32_t here = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        k[e] = value(a.c.k, a.c.ks, row, e), v[e] = value(a.c.v, a.c.vs, row, e);
+        if (!(fabsf(v[e]) < INFINITY)) here |= 1u << e;
+      }
+      for (int r0 = 0; r0 < rows; r0 += N) {
+        float s[N] = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (r0 + i < rows)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              s[i] = fmaf(load_io1(a.q, a.io, (head0 + r0 + i) * D + 32 * e + lane) * a.scale * kLog2e, k[e], s[i]);
 #pragma unroll
         for (int x = 16; x; x >>= 1)
 #pragma unroll
           for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float w = exp2_fast(s[i] - low[i]) * C::kUnit;
+          if (r0 + i >= rows) break;
+          const float top = m[r0 + i], w = exp2_fast(s[i] - (top == -INFINITY ? 0.f : top)) * C::kUnit;
+          float *const o = so + (r0 + i) * C::kLdO + lane;
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[i][e] = fmaf(w, v[e], o[i][e]);
+          for (int e = 0; e < E; ++e)
+            if (here >> e & 1) o[32 * e] = seen >> e & 1 ? fmaf(w, v[e], o[32 * e]) : w * v[e];
         }
       }
+      seen |= here;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (r0 + i < rows)
-#pragma unroll
-        for (int e = 0; e < E; ++e) so[(r0 + i) * C::kLdO + 32 * e + lane] = o[i][e];
   }
 }
 
@@ -1074,8 +1109,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       }
     if (__any_sync(0xffffffffu, odd)) {
       __syncwarp();
-      values_again<C, TYPE, D>(p, now.s, now.hk, now.span.lo, now.span.len, now.tile, count, head0, rows,
-                               sm + warp * C::kRows, so + warp * C::kRows * C::kLdO);
+      sum_infinities<C, TYPE, D>(p, now.s, now.hk, now.span.lo, now.span.len, now.tile, count, head0, rows,
+                                 sm + warp * C::kRows, so + warp * C::kRows * C::kLdO);
     }
     __syncthreads();
     if (now.tile == 0 && count == tiles) {

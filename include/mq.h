@@ -411,17 +411,25 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * head; query head a reads kv head a / (n_heads / n_kv_heads).  A sequence of length 0 gives
  * o = 0.  Sums, softmax statistics and accumulators are binary32; f16 and Q8_0 keys meet the
  * query as two f16 parts (22 bits), bf16 keys as three bf16 parts (24 bits), and the weights
- * meet the values likewise.
+ * meet the values likewise.  Two f16 parts hold a query element to 2^-40 of its row's largest at
+ * least, a weight to 2^-40 of the largest before it; weights of Q8_0 values are multiplied by the
+ * value's scale first and held to 2^-39 of the largest scale among the keys taken together (16 or
+ * 32), so that values 2^20 below a neighbour's lose accuracy where theirs is the larger weight.
  * Infinities and NaN in rows that are read (mq_rope_store rounds to them what F16 does not hold):
  * an infinite value makes its dim of o infinite (NaN beside one of the other sign, or where its
- * weight is zero in binary32), a NaN makes it NaN; a key whose logit is minus infinity weighs
+ * weight is below 2^-126), a NaN makes it NaN; a key whose logit is minus infinity weighs
  * nothing (if none weighs anything, o = 0); a logit that is plus infinity or NaN makes the head's o
  * NaN.  (To an infinite F16 key a query element below 2^-39 of its row's largest is a zero.)  The
  * scales of Q8_0 keys must not be infinite; those that mq_rope_store writes are not.
  *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned
  *   len     device int32 [S], the rows to read, the new token's own among them; <= max_len
- *   max_len bound of the lengths on the host, <= pages_ld*page_size: it sizes the workspace
- *           and the launch, not the work
+ *   max_len bound of the lengths on the host, <= pages_ld*page_size.  The attention's own work
+ *           goes by the lengths alone.  With MQ_ATTN_TRACK the workspace holds a binary32 logit
+ *           per query head (their number per kv head rounded up) and position up to max_len of
+ *           every sequence, and the sums' kernel launches blocks for as many, which end at once past
+ *           the lengths: a bound far above them costs time (32 sequences of up to 4001 rows, 32/8
+ *           heads of 128, F16: 62 us and 19 MB with max_len 4001, 75 and 137 with 32768, 124 and
+ *           539 with 131072)
  *   flags   MQ_ATTN_TRACK: weight_sum of each row read += its w summed over the kv head's
  *           query heads (two sequences of one call must then share no page)
  *   ws      device workspace of ws_bytes >= mq_attn_workspace_bytes, 256-byte aligned
@@ -445,7 +453,8 @@ mq_status mq_attn_decode(const mq_kv_cache *cache, mq_type io, const void *q, vo
  *   new_len  device int32 [S]: min(n, keep); written.  May be the array len itself (lengths
  *            updated in place), but not overlap it otherwise
  *   sink, recent >= 0, sink + recent <= keep, 1 <= keep <= new_pages_ld*page_size
- *   max_len  bound of the lengths, <= pages_ld*page_size
+ *   max_len  bound of the lengths, <= pages_ld*page_size; how many thread blocks share a kv
+ *            head's choice goes by it
  * A length outside [0, max_len] is clamped; a row whose old or new page lies outside the cache is
  * not copied; both are reported by mq_stream_status.  S = 0 does nothing. */
 mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages, int64_t pages_ld,
