@@ -11,9 +11,10 @@
 // their next 11 and 10 bits by itself; else these are counted over the cluster as well.  Rows
 // equal to the key stay from the lowest position on; ballots and the cluster's counts give every
 // row its place.  What bounds it: latency.  131072 rows of 4 heads take 19 us: a length, its pages
-// and their sums read one after the other 5, then the cluster's barriers and reads of about 1 us
-// each (it reads 4 bytes per row; counting bit by bit from global memory, one block per head, took
-// 5.2 ms).
+// and their sums read one after the other 5, four to six barriers and reads of the cluster about 1 us
+// each; the rest (the histogram's additions in shared memory, the block's own barriers, its
+// instructions' first fetch) has not been taken apart.  (It reads 4 bytes per row; counting bit by
+// bit from global memory, one block per head, took 5.2 ms.)
 //
 // Copy: bounded by the bytes of the kept rows, read and written once.  A warp looks up 32 (or,
 // when there are few, 16) rows, one per lane, then moves them 16 bytes a lane, eight loads in

@@ -15,8 +15,11 @@
 // 32-element block meets in shared memory as an integer maximum (the halves of a partial rotation
 // may end inside a block, so no fixed lanes share one), then the quants as in quant_row.cuh.
 // Measured (28/4 heads of 128): 16384 tokens f32 to f16 98 us (5.9 TB/s, 89% of a plain copy's
-// rate), to Q8_0 93 us (90%), bf16 to f16 64 us (72%: latency of a token's chain); 4096 tokens f32
-// to f16, three axes, 25.4 us (85%); 8 tokens 2.1 us.
+// rate), to Q8_0 93 us (90%; three rounds at once spill 8 bytes a thread), bf16 to f16 64 us (72%: one
+// token's loads are in flight per block, fewer bytes than cover the latency); 4096 tokens f32 to
+// f16, three axes, 25.2 us (86%); 1023 tokens bf16 to Q8_0, 32/8 heads, half of a head rotated, 9.9 us
+// (2.8 times its bytes' time: a block has one or two whole tokens, so the shares are uneven); 8
+// tokens 2.1 us.
 #include <algorithm>
 #include <type_traits>
 
