@@ -208,6 +208,11 @@ extern "C" mq_status mq_attn_decode(const mq_kv_cache *cache, mq_type io, const 
   if (window < 0) return fail(MQ_ERR_ARG, "%s: window=%lld is negative", site, (long long)window);
   if (!(scale - scale == 0.0f))
     return fail(MQ_ERR_ARG, "%s: scale=%g is not finite", site, (double)scale);
+  // a row of o is written when every block that reads the same row of q has done so: in place, but
+  // not shifted
+  const uint64_t bytes = uint64_t(S) * n_heads * cache->head_dim * (io == MQ_F32 ? 4 : 2);
+  if (o != q && overlap(o, bytes, q, bytes))
+    return fail(MQ_ERR_ARG, "%s: o=%p overlaps q=%p (it may only be the same array)", site, o, q);
   const bool track = flags & MQ_ATTN_TRACK;
   DeviceState *st = nullptr;
   if ((s = current_state(&st, site)) != MQ_OK) return s;

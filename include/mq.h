@@ -421,7 +421,8 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * nothing (if none weighs anything, o = 0); a logit that is plus infinity or NaN makes the head's o
  * NaN.  (To an infinite F16 key a query element below 2^-39 of its row's largest is a zero.)  The
  * scales of Q8_0 keys must not be infinite; those that mq_rope_store writes are not.
- *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned
+ *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned;
+ *           o may be q itself, but not overlap it otherwise
  *   len     device int32 [S], the rows to read, the new token's own among them; <= max_len
  *   max_len bound of the lengths on the host, <= pages_ld*page_size.  The attention's own work
  *           goes by the lengths alone.  With MQ_ATTN_TRACK the workspace holds a binary32 logit

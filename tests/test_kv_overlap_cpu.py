@@ -41,3 +41,14 @@ def test_rotated_queries_are_apart_from_the_rows(L, T, shift, refused):
                          base + shift, T, 28, None)
     assert ("overlaps" in L.mq_last_error().decode()) == refused
     assert mq.STATUS[st] in (["MQ_ERR_ARG"] if refused else ["MQ_ERR_ARG", "MQ_ERR_STATE", "MQ_ERR_CUDA"])
+
+
+@pytest.mark.parametrize("shift,refused", [(0, False), (16, True), (-16, True), (2 * 28 * 128 * 4 - 16, True),
+                                           (2 * 28 * 128 * 4, False), (-2 * 28 * 128 * 4, False)])
+def test_attention_outputs_are_the_queries_or_apart(L, shift, refused):
+    """Two sequences, 28 heads of 128, f32."""
+    base = 1 << 24
+    c = cache()
+    st = L.mq_attn_decode(ctypes.byref(c), 0, base, base + shift, None, 7, None, 2, 28, 100, 0.1, 0, 0, None, 0, None)
+    assert ("overlaps" in L.mq_last_error().decode()) == refused
+    assert mq.STATUS[st] in (["MQ_ERR_ARG"] if refused else ["MQ_ERR_ARG", "MQ_ERR_STATE", "MQ_ERR_CUDA"])
