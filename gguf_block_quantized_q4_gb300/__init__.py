@@ -62,6 +62,8 @@ ABI = {
     "mq_ffn_gu_mmq": (_ST, [ctypes.c_int, _P, _P, _P, _I64, _I64, _I64, _P]),
     "mq_rope_store": (_ST, [_P, _P, ctypes.c_int, _P, _I64, _P, _P, _P, _P, _I64, ctypes.c_int,
                             _P]),
+    "mq_norm_rope_store": (_ST, [_P, _P, _P, ctypes.c_int, _P, _I64, _P, _P, _P, _P, _I64,
+                                 ctypes.c_int, _P]),
     "mq_attn_workspace_bytes": (_SZ, [_P, _I64, ctypes.c_int, _I64, ctypes.c_uint32]),
     "mq_attn_decode": (_ST, [_P, ctypes.c_int, _P, _P, _P, _I64, _P, _I64, ctypes.c_int, _I64,
                              ctypes.c_float, _I64, ctypes.c_uint32, _P, _SZ, _P]),
@@ -440,6 +442,10 @@ class _RopeStruct(ctypes.Structure):  # mq_rope
                 ("pairs", ctypes.c_int), ("n_axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 128)]
 
 
+class _HeadNormStruct(ctypes.Structure):  # mq_head_norm
+    _fields_ = [("q", _P), ("k", _P), ("eps", ctypes.c_float)]
+
+
 _IO = {}  # torch dtype -> type code of activations
 _torch = _raw_current_stream = _empty_cuda = None
 
@@ -475,8 +481,9 @@ def _refuse(what):
 
 class KVCache:
     """A paged cache over the caller's planes (mq_kv_cache): k, v [page][head][slot][head_dim]
-    (layout "hnd") or [page][slot][head][head_dim] ("nhd") of f16, bf16, or int8 with f16
-    scales k_scale, v_scale of the same axes and head_dim / 32; sums f32 of the same axes
+    (layout "hnd") or [page][slot][head][head_dim] ("nhd") of f16, bf16, int8 (Q8_0) or uint8
+    with two elements a byte (Q4_0, head_dim / 2 bytes), the last two with f16 scales k_scale,
+    v_scale of the same axes and head_dim / 32; sums f32 of the same axes
     without head_dim (the weight each row has gathered), or None.  The planes may be views with
     larger outer strides, the same in rows for all of them."""
 
@@ -484,22 +491,24 @@ class KVCache:
         torch = _torch or _torch_setup()
         if layout not in ("hnd", "nhd"):
             _refuse(f"layout {layout!r} is neither 'hnd' nor 'nhd'")
-        want = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8}.get(kind)
+        want = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8, Q4_0: torch.uint8}.get(kind)
         if want is None:
-            _refuse(f"cache type {kind} is not F16, BF16 or Q8_0")
+            _refuse(f"cache type {kind} is not F16, BF16, Q8_0 or Q4_0")
         if k.dim() != 4 or k.shape != v.shape:
             _refuse("k and v are [page][...][...][head_dim]")
-        d = k.shape[3]
-        planes = [("k", k, want, d), ("v", v, want, d)]
-        if kind == Q8_0:
+        elements = k.shape[3]  # of the planes
+        d = 2 * elements if kind == Q4_0 else elements
+        scaled = kind in (Q8_0, Q4_0)
+        planes = [("k", k, want, elements), ("v", v, want, elements)]
+        if scaled:
             if k_scale is None or v_scale is None:
-                _refuse("a Q8_0 cache needs its scales")
+                _refuse(f"a {'Q8_0' if kind == Q8_0 else 'Q4_0'} cache needs its scales")
             planes += [("k_scale", k_scale, torch.float16, d // 32),
                        ("v_scale", v_scale, torch.float16, d // 32)]
         if sums is not None:
             planes.append(("sums", sums, torch.float32, 1))
         # strides in rows (that of an axis of one element says nothing)
-        rows = [k.stride(i) // max(d, 1) if k.shape[i] > 1 else 1 for i in range(3)]
+        rows = [k.stride(i) // max(elements, 1) if k.shape[i] > 1 else 1 for i in range(3)]
         for name, t, dtype, width in planes:
             if not t.is_cuda or t.dtype != dtype:
                 _refuse(f"{name} must be a CUDA tensor of {dtype}")
@@ -519,8 +528,8 @@ class KVCache:
             return None if t is None else t.data_ptr()
         self._c = _KVCacheStruct(kind, self.n_kv_heads, d, self.page_size, self.n_pages, rows[0],
                                  rows[head], rows[slot], ptr(k), ptr(v),
-                                 ptr(k_scale) if kind == Q8_0 else None,
-                                 ptr(v_scale) if kind == Q8_0 else None, ptr(sums))
+                                 ptr(k_scale) if scaled else None,
+                                 ptr(v_scale) if scaled else None, ptr(sums))
         self._ref = ctypes.addressof(self._c)
 
 
@@ -528,17 +537,17 @@ def kv_cache(kind, n_pages, page_size, n_kv_heads, head_dim, sums=False, layout=
              device="cuda") -> KVCache:
     """A KVCache over new zeroed planes."""
     import torch
-    if kind not in (F16, BF16, Q8_0):
-        _refuse(f"cache type {kind} is not F16, BF16 or Q8_0")
+    if kind not in (F16, BF16, Q8_0, Q4_0):
+        _refuse(f"cache type {kind} is not F16, BF16, Q8_0 or Q4_0")
     outer = ((n_pages, n_kv_heads, page_size) if layout == "hnd"
              else (n_pages, page_size, n_kv_heads))
-    dtype = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8}[kind]
+    dtype = {F16: torch.float16, BF16: torch.bfloat16, Q8_0: torch.int8, Q4_0: torch.uint8}[kind]
 
     def plane(*shape, dtype):
         return torch.zeros(shape, dtype=dtype, device=device)
-    k, v = (plane(*outer, head_dim, dtype=dtype) for _ in range(2))
+    k, v = (plane(*outer, head_dim // 2 if kind == Q4_0 else head_dim, dtype=dtype) for _ in range(2))
     ks, vs = ((plane(*outer, head_dim // 32, dtype=torch.float16) for _ in range(2))
-              if kind == Q8_0 else (None, None))
+              if kind in (Q8_0, Q4_0) else (None, None))
     return KVCache(kind, k, v, ks, vs, plane(*outer, dtype=torch.float32) if sums else None,
                    layout)
 
@@ -590,15 +599,31 @@ class Rope:
         self._ref = ctypes.addressof(self._c)
 
 
+class HeadNorm:
+    """Norms of the query and key heads (mq_head_norm): weights f32 [head_dim] each."""
+
+    def __init__(self, q_weight, k_weight, eps=1e-6):
+        torch = _torch or _torch_setup()
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if (w.dim() != 1 or w.shape != q_weight.shape or not w.is_contiguous() or not w.is_cuda
+                    or w.dtype != torch.float32):
+                _refuse(f"{name} must be a contiguous CUDA f32 tensor [head_dim]")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        self.head_dim = q_weight.shape[0]
+        self._c = _HeadNormStruct(q_weight.data_ptr(), k_weight.data_ptr(), eps)
+        self._ref = ctypes.addressof(self._c)
+
+
 def rope_store(cache: KVCache, rope: Rope, qkv, pos, slot, n_heads, bias=None, q=None,
-               stream=None):
-    """Rotate and store T tokens: qkv [T][(n_heads + 2 n_kv_heads) head_dim] (f32, f16 or bf16;
+               stream=None, norm=None):
+    """Rotate and store T tokens, with the query and key heads normed before where `norm`, a HeadNorm, is
+    given: qkv [T][(n_heads + 2 n_kv_heads) head_dim] (f32, f16 or bf16;
     rows may be strided), pos int32 [n_axes][T] (or [T] for one axis), slot int64 [T].  Returns
     the rotated queries [T][n_heads][head_dim]."""
     torch = _torch or _torch_setup()
     if stream is not None and q is None:
         with torch.cuda.stream(stream):
-            return rope_store(cache, rope, qkv, pos, slot, n_heads, bias)
+            return rope_store(cache, rope, qkv, pos, slot, n_heads, bias, norm=norm)
     T, width = qkv.shape
     ld, inner = qkv.stride()
     d = cache.head_dim
@@ -618,10 +643,15 @@ def rope_store(cache: KVCache, rope: Rope, qkv, pos, slot, n_heads, bias=None, q
         q = _empty_cuda((T, n_heads, d), (n_heads * d, d, 1), qkv.dtype)
     elif q.dtype != qkv.dtype or q.numel() != T * n_heads * d or not q.is_contiguous():
         _refuse("q must be contiguous, of qkv's type")
-    status = lib().mq_rope_store(
-        cache._ref, rope._ref, io, qkv.data_ptr(), ld if T > 1 else width,
-        None if bias is None else bias.data_ptr(), pos.data_ptr(), slot.data_ptr(), q.data_ptr(),
-        T, n_heads, _raw_current_stream(cache._device_index) if stream is None else stream.cuda_stream)
+    rest = (io, qkv.data_ptr(), ld if T > 1 else width, None if bias is None else bias.data_ptr(),
+            pos.data_ptr(), slot.data_ptr(), q.data_ptr(), T, n_heads,
+            _raw_current_stream(cache._device_index) if stream is None else stream.cuda_stream)
+    if norm is None:
+        status = lib().mq_rope_store(cache._ref, rope._ref, *rest)
+    else:
+        if norm.head_dim != d:
+            _refuse(f"the norms' weights are for heads of {norm.head_dim}, the cache's have {d}")
+        status = lib().mq_norm_rope_store(cache._ref, rope._ref, norm._ref, *rest)
     if status:
         _check(status)
     return q

@@ -160,27 +160,48 @@ __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
   return *reinterpret_cast<uint32_t *>(&r);
 }
 
+// The 4-bit numbers n at the bits MASK of each half as f16x2 n - 8: 1024 + n (or 1024 + 16 n) by bits,
+// then an exact subtraction (or multiplication by 1/16 and subtraction).
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t int4_f16(uint32_t v) {
+  static_assert(MASK == 0x000f000fu || MASK == 0x00f000f0u, "bits 0-3 or 4-7");
+  const uint32_t u = (v & MASK) | 0x64006400u, less = MASK == 0x000f000fu ? 0xe408e408u : 0xd480d480u;
+  const __half2 x = *reinterpret_cast<const __half2 *>(&u), c = *reinterpret_cast<const __half2 *>(&less);
+  const uint32_t by = 0x2c002c00u;  // 1/16
+  const __half2 r = MASK == 0x000f000fu ? __hadd2_rn(x, c) : __hfma2(x, *reinterpret_cast<const __half2 *>(&by), c);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+// The two parts of a pair of weights times a pair of f16 scales, as two parts: the first part's product
+// rounded, and what that leaves (exact) with the second's.
+__device__ __forceinline__ void scale_parts(const uint32_t (&p)[2], uint32_t d, uint32_t (&to)[2]) {
+  const __half2 a = *reinterpret_cast<const __half2 *>(&p[0]), b = *reinterpret_cast<const __half2 *>(&p[1]);
+  const __half2 x = *reinterpret_cast<const __half2 *>(&d), hi = __hmul2_rn(a, x);
+  const __half2 lo = __hfma2(b, x, __hfma2(a, x, __hneg2(hi)));
+  to[0] = *reinterpret_cast<const uint32_t *>(&hi), to[1] = *reinterpret_cast<const uint32_t *>(&lo);
+}
+
 // ---- the shape of a kernel ----------------------------------------------------------------
 constexpr int kSmemMax = 226 * 1024;  // per thread block (of 227 KB; a little is static)
 
 template <int TYPE, int D, int NT>
 struct Shape {
-  static constexpr bool kQ8 = TYPE == MQ_Q8_0;
+  static constexpr bool kQ8 = TYPE == MQ_Q8_0, kQ4 = TYPE == MQ_Q4_0;
+  static constexpr bool kScaled = kQ8 || kQ4;   // blocks of 32 dims with a scale each
   static constexpr bool kBf = TYPE == MQ_BF16;  // operands bf16, else f16
   static constexpr int kParts = kBf ? 3 : 2;    // of the query and of the weights
-  static constexpr int kRow = kQ8 ? D : 2 * D;  // bytes of a key row
+  static constexpr int kRow = kQ4 ? D / 2 : kQ8 ? D : 2 * D;  // bytes of a key row
   static constexpr int kNG = D / 32;            // groups of 32 dims
   static constexpr int kMT = kRow <= 128 ? 2 : 1;  // 16-key groups a warp takes at a time
   static constexpr int kKeys = 16 * kMT;
   static constexpr int kRows = 8 * NT;          // query rows of a unit
   // shared memory: the rings, query parts, the warps' results
-  static constexpr int kStride = kRow + 16;     // an odd number of 16-byte steps
-  // a stage: K rows, V rows, the page entries of the tile a ring's length ahead, Q8_0 scales as
+  static constexpr int kStride = kRow / 16 % 2 ? kRow : kRow + 16;  // an odd number of 16-byte steps
+  // a stage: K rows, V rows, the page entries of the tile a ring's length ahead, the blocks' scales as
   // they are stored (K's keys, V's keys)
   static constexpr int kEntries = 2 * kKeys * kStride;
   static constexpr int kRaw = kEntries + kKeys * 4;
   static constexpr int kScaleRow = (kNG + 1) / 2 * 4;
-  static constexpr int kStage = (kRaw + (kQ8 ? 2 * kKeys * kScaleRow : 0) + 15) / 16 * 16;
+  static constexpr int kStage = (kRaw + (kScaled ? 2 * kKeys * kScaleRow : 0) + 15) / 16 * 16;
   static constexpr int kLdO = D + 4;
   // the query's parts as operand words; Q8_0: and -128 times its block sums as accumulators
   static constexpr int kQuery = kParts * NT * kNG * 32 * 16;
@@ -470,6 +491,10 @@ __device__ __noinline__ void sum_infinities(const Params &p, int seq, int hk, in
   auto value = [&](const uint8_t *plane, const __half *scales, uint32_t row, int e) {
     const uint64_t at = uint64_t(row) * D + 32 * e + lane;
     if (C::kQ8) return float(reinterpret_cast<const int8_t *>(plane)[at]) * __half2float(scales[uint64_t(row) * E + e]);
+    if (C::kQ4) {
+      const uint32_t two = plane[uint64_t(row) * C::kRow + 16 * e + (lane & 15)];
+      return float(int(lane < 16 ? two & 15 : two >> 4) - 8) * __half2float(scales[uint64_t(row) * E + e]);
+    }
     const uint16_t x = reinterpret_cast<const uint16_t *>(plane)[at];
     return C::kBf ? __uint_as_float(uint32_t(x) << 16) : __half2float(__ushort_as_half(x));
   };
@@ -478,7 +503,7 @@ __device__ __noinline__ void sum_infinities(const Params &p, int seq, int hk, in
     const int key = lo + t * C::kTK + warp * C::kKeys + lane;
     const uint32_t my_row = lane < C::kKeys && key < len ? kv_row32(a.c, pages, hk, key) : kNoRow;
     uint32_t odd = 0;  // keys with such values
-    if (C::kQ8) {
+    if constexpr (C::kScaled) {
       if (my_row != kNoRow)
         for (int e = 0; e < E; ++e)
           if (is_odd(__half_as_ushort(a.c.vs[uint64_t(my_row) * E + e]))) odd = 1u << lane;
@@ -623,7 +648,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       copy16(dst + key * C::kStride + ch * 16, a.c.k + ch * 16 + off, size);
       copy16(dst + (C::kKeys + key) * C::kStride + ch * 16, a.c.v + ch * 16 + off, size);
     }
-    if (C::kQ8) {  // lane i: key i % 16 (+ 16) of K, or of V
+    if (C::kScaled) {  // lane i: key i % 16 (+ 16) of K, or of V
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int key = 16 * m + (lane & 15);
@@ -668,7 +693,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   // operand addresses of this lane within a stage: matrix lane >> 3, row lane & 7
   const uint32_t k_lane = ((lane & 7) + (lane & 8)) * C::kStride + (lane >> 4) * 16;
   const uint32_t v_lane = (C::kKeys + (lane & 7) + (lane >> 4) * 8) * C::kStride + (lane >> 3 & 1) * 16;
-  // Q8_0: the two chunks of 16 dims side by side, keys 0-7 and 8-15 each
+  // Q8_0: the two chunks of 16 dims side by side, keys 0-7 and 8-15 each; Q4_0: two blocks of 32
   const uint32_t v_lane8 = (C::kKeys + (lane & 7) + (lane & 8)) * C::kStride + (lane >> 4) * 16;
 
   // The query rows of a unit as they are read: warp w has the rows w, w + kWarps, ..., lane i the
@@ -701,7 +726,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 
     // the query's parts as operand words: lane 4 r + t' of (part, 8-row group, 32 dims) has the
     // words of two 16-dim steps.  f16 and bf16 rows: dims 2t', 2t' + 1 and 8 more of a step;
-    // Q8_0 rows: dims 4t' .. 4t' + 3 (a chunk's four bytes)
+    // Q8_0 rows: dims 4t' .. 4t' + 3 (a chunk's four bytes); Q4_0 rows: the dims 4t', 4t' + 2; 4t' + 1,
+    // 4t' + 3 (four bytes' low halves), and 16 more (their high halves)
 #pragma unroll
     for (int i0 = 0; i0 < RPW; ++i0) {
       const int r = warp + i0 * C::kWarps;
@@ -728,7 +754,10 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       if (lane < D / 8) {
         uint32_t w[4][C::kParts];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split2<C::kBf>(x[2 * i] * up, x[2 * i + 1] * up, w[i]);
+        for (int i = 0; i < 4; ++i) {
+          const int a = C::kQ4 ? 4 * (i >> 1) + (i & 1) : 2 * i, b = C::kQ4 ? a + 2 : a + 1;
+          split2<C::kBf>(x[a] * up, x[b] * up, w[i]);
+        }
         if (C::kQ8) {
           float sum = 0.f;
 #pragma unroll
@@ -754,7 +783,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t *const to = q + k * NT * NG * 128;
-            if (C::kQ8)
+            if (C::kScaled)
               to[(2 * half + (i >> 1)) * 4 + 2 * step + (i & 1)] = w[i][k];
             else
               to[i * 4 + 2 * step + half] = w[i][k];
@@ -778,7 +807,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
       uint8_t *const my_stage = my_ring + stage * C::kStage;
       if (here) {
         float tile_unit = 1.f, per_unit = 1.f;  // the power of two of V's scales, and its inverse
-        constexpr int SW = C::kScaleRow / 4;    // words of a row's Q8_0 scales, two each
+        constexpr int SW = C::kScaleRow / 4;    // words of a row's scales, two each
         // the scales of a key: of K (plane 0) or V (1)
         auto scales_of = [&](uint32_t (&w)[SW], int plane, int key) {
           const uint8_t *const from = my_stage + C::kRaw + (plane * C::kKeys + key) * C::kScaleRow;
@@ -798,7 +827,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             for (int j = 0; j < SW; ++j) w[j] = __funnelshift_r(w[j], j + 1 < SW ? w[(j + 1) % SW] : 0, shift);
           }
         };
-        if (C::kQ8) {  // a power of two that V's largest scale of the tile is below
+        if (C::kScaled) {  // a power of two that V's largest scale of the tile is below
           uint32_t top = 0;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -810,9 +839,11 @@ attn_decode_kernel(const __grid_constant__ Params p) {
               top = max(top, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
           }
           top = __reduce_max_sync(0xffffffffu, top);
-          const int e = top == 0 || top >= 0x7c00u
-                            ? 126
-                            : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+          int e = top == 0 || top >= 0x7c00u
+                      ? 126
+                      : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+          // (Q4_0: 1 for scales below 1, which are multiplied as they are stored)
+          if (C::kQ4) e = max(e, 126);
           tile_unit = __uint_as_float(uint32_t(e + 1) << 23), per_unit = __uint_as_float(uint32_t(253 - e) << 23);
         }
         // ---- S^T = K Q^T ----
@@ -820,15 +851,34 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         // chains of products are on their way; f16 and bf16 rows have an accumulator per chain
         // and part kind (first; others) up to the end.
         float s[MT][NT][4], acc[2][2][MT][NT][4] = {};
-        uint32_t kscale[MT][2][SW];  // Q8_0: of the keys g, g + 8
-        if (C::kQ8)
+        uint32_t kscale[MT][2][SW];  // of the keys g, g + 8
+        if (C::kScaled)
 #pragma unroll
           for (int m = 0; m < MT; ++m) scales_of(kscale[m][0], 0, 16 * m + g), scales_of(kscale[m][1], 0, 16 * m + 8 + g);
 #pragma unroll
         for (int j0 = 0; j0 < NG; j0 += 2) {
           uint4 b[2][C::kParts][NT];
           uint32_t ka[2][MT][2][4];  // two steps of 16 dims
-          float cq[2][MT][NT][4];    // Q8_0: the blocks' sums
+          float cq[2][MT][NT][4];    // Q8_0, Q4_0: the blocks' sums
+          if (C::kQ4) {
+            // Four bytes of a key's block, exact: as subnormals with the 8 in the accumulators' start, as
+            // Q8_0's are, they save 28 operations a row of 128 and lose bits (the tensor cores align a
+            // product by its factors' exponents, and a subnormal's says nothing of its leading
+            // zeros): an error to 64 bits of 2e-6 at 64 ragged sequences instead of 4e-7.
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              uint32_t x[4];  // block j0: keys g, g + 8; block j0 + 1
+              ldmatrix4<false>(x, base + k_lane + 16 * m * C::kStride + j0 * 16);
+#pragma unroll
+              for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t u = x[2 * jj + h], v = u >> 8;
+                  ka[jj][m][0][h] = int4_f16<0x000f000fu>(u), ka[jj][m][0][2 + h] = int4_f16<0x000f000fu>(v);
+                  ka[jj][m][1][h] = int4_f16<0x00f000f0u>(u), ka[jj][m][1][2 + h] = int4_f16<0x00f000f0u>(v);
+                }
+            }
+          }
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
             const int j = j0 + jj;
@@ -851,7 +901,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                   ka[jj][m][st][0] = __byte_perm(xa, 0, 0x4140), ka[jj][m][st][1] = __byte_perm(xb, 0, 0x4140);
                   ka[jj][m][st][2] = __byte_perm(xa, 0, 0x4342), ka[jj][m][st][3] = __byte_perm(xb, 0, 0x4342);
                 }
-              } else {
+              } else if (!C::kQ4) {
                 ldmatrix4<false>(ka[jj][m][0], at_k + j * 64);
                 ldmatrix4<false>(ka[jj][m][1], at_k + j * 64 + 32);
               }
@@ -871,14 +921,15 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                     const uint32_t(&x)[4] = ka[jj][m][st];
                     const uint32_t b0 = st ? b[jj][k][n].z : b[jj][k][n].x;
                     const uint32_t b1 = st ? b[jj][k][n].w : b[jj][k][n].y;
-                    if (!C::kQ8)
+                    if (!C::kScaled)
                       mma<C::kBf>(acc[jj][k > 0][m][n], x[0], x[1], x[2], x[3], b0, b1);
                     else if (k == 0 && st == 0)
-                      mma_from(cq[jj][m][n], x[0], x[1], x[2], x[3], b0, b1, ssum[(n * NG + j0 + jj) * 4 + t]);
+                      mma_from(cq[jj][m][n], x[0], x[1], x[2], x[3], b0, b1,
+                               C::kQ8 ? ssum[(n * NG + j0 + jj) * 4 + t] : make_float4(0.f, 0.f, 0.f, 0.f));
                     else
                       mma<false>(cq[jj][m][n], x[0], x[1], x[2], x[3], b0, b1);
                   }
-          if (C::kQ8) {  // the blocks' sums times the scales of keys g, g + 8
+          if (C::kScaled) {  // the blocks' sums times the scales of keys g, g + 8
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
@@ -900,7 +951,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              if (C::kQ8) {
+              if (C::kScaled) {
                 s[m][n][w] = acc[0][0][m][n][w];
               } else {
                 // (an infinite key: the first parts' product has the sign, the others' may be NaN)
@@ -980,19 +1031,20 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                 s[m][n][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410)) * per_unit;
                 s[m][n][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632)) * per_unit;
               } else {
+                if (C::kQ4) s[m][n][2 * h] *= per_unit, s[m][n][2 * h + 1] *= per_unit;
                 split2<C::kBf>(s[m][n][2 * h], s[m][n][2 * h + 1], pw[m][n][h]);
 #pragma unroll
                 for (int k = 0; k < C::kParts; ++k) pw[m][n][h][k] = transpose8x8(pw[m][n][h][k]);
               }
             }
         // ---- O^T = O^T alpha + V^T P^T ----
-        if (C::kQ8) {  // o stands in units of the tile's power of two
+        if (C::kScaled) {  // o stands in units of the tile's power of two
 #pragma unroll
           for (int n = 0; n < NT; ++n) al[n][0] *= unit * per_unit, al[n][1] *= unit * per_unit;
           unit = tile_unit;
         }
-        uint32_t vscale[MT][4][SW];  // Q8_0: of the keys 2t, 2t + 1, 2t + 8, 2t + 9
-        if (C::kQ8)
+        uint32_t vscale[MT][4][SW];  // of the keys 2t, 2t + 1, 2t + 8, 2t + 9
+        if (C::kScaled)
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -1004,6 +1056,22 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           for (int m = 0; m < MT; ++m) {
             uint32_t va[2][2][4];  // [group][16 dims][operand word]
             uint32_t pq[2][NT][2][C::kParts];
+            if constexpr (C::kQ4) {
+              uint32_t x[4];  // bytes 2g, 2g + 1 of the keys 2t, 2t + 1: block j0 of keys 0-7, 8-15, then j0 + 1
+              ldmatrix4<true>(x, base + v_lane8 + 16 * m * C::kStride + j0 * 16);
+#pragma unroll
+              for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  // low halves: dims 2g and 2g + 1, high halves: 16 more
+                  const uint32_t u = x[2 * jj + q], v = u >> 8;
+                  va[jj][0][2 * q] = int4_f16<0x000f000fu>(u), va[jj][0][2 * q + 1] = int4_f16<0x000f000fu>(v);
+                  va[jj][1][2 * q] = int4_f16<0x00f000f0u>(u), va[jj][1][2 * q + 1] = int4_f16<0x00f000f0u>(v);
+                  const uint32_t d = __byte_perm(vscale[m][2 * q][j0 / 2], vscale[m][2 * q + 1][j0 / 2], jj ? 0x7632 : 0x5410);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) scale_parts(pw[m][n][q], d, pq[jj][n][q]);
+                }
+            }
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
               const int j = j0 + jj;
@@ -1029,7 +1097,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                   split2<C::kBf>(s[m][n][0] * d[0], s[m][n][1] * d[1], pq[jj][n][0]);
                   split2<C::kBf>(s[m][n][2] * d[2], s[m][n][3] * d[3], pq[jj][n][1]);
                 }
-              } else {
+              } else if (!C::kQ4) {
                 ldmatrix4<true>(va[jj][0], base + v_lane + 16 * m * C::kStride + j * 64);
                 ldmatrix4<true>(va[jj][1], base + v_lane + 16 * m * C::kStride + j * 64 + 32);
               }
@@ -1045,8 +1113,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                     if (j0 + jj >= NG) continue;
                     const uint32_t(&v)[4] = va[jj][h];
                     mma<C::kBf>(c[jj][h][n], v[0], v[1], v[2], v[3],
-                                C::kQ8 ? pq[jj][n][0][k] : pw[m][n][0][k],
-                                C::kQ8 ? pq[jj][n][1][k] : pw[m][n][1][k]);
+                                C::kScaled ? pq[jj][n][0][k] : pw[m][n][0][k],
+                                C::kScaled ? pq[jj][n][1][k] : pw[m][n][1][k]);
                   }
           }
 #pragma unroll
@@ -1099,7 +1167,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
         odd |= l < INFINITY && zero[0] + zero[1] != 0.f;
 #pragma unroll
         for (int j = 0; j < KS; ++j)
-          if (C::kQ8) {  // dims 16 j + 2g, 2g + 1
+          if (C::kScaled) {  // dims 16 j + 2g, 2g + 1
             *reinterpret_cast<float2 *>(so + r * C::kLdO + 16 * j + 2 * g) =
                 make_float2(o[j][n][w] * unit, o[j][n][w + 2] * unit);
           } else {
@@ -1308,6 +1376,7 @@ mq_status init_attn_decode(const DeviceState *st) {
   mq_status r = opt_in<MQ_F16>(st);
   if (r == MQ_OK) r = opt_in<MQ_BF16>(st);
   if (r == MQ_OK) r = opt_in<MQ_Q8_0>(st);
+  if (r == MQ_OK) r = opt_in<MQ_Q4_0>(st);
   return r;
 }
 
@@ -1335,7 +1404,8 @@ mq_status launch_attn_decode(const AttnArgs &a, cudaStream_t s, const DeviceStat
   switch (a.c.type) {
     case MQ_F16: r = launch_dim<MQ_F16>(p, rows, s, st); break;
     case MQ_BF16: r = launch_dim<MQ_BF16>(p, rows, s, st); break;
-    default: r = launch_dim<MQ_Q8_0>(p, rows, s, st); break;
+    case MQ_Q8_0: r = launch_dim<MQ_Q8_0>(p, rows, s, st); break;
+    default: r = launch_dim<MQ_Q4_0>(p, rows, s, st); break;
   }
   if (r == MQ_OK && a.track) {
     const int keys = std::max(32, kTrackThreads * kTrackKeys / a.c.hkv / 32 * 32);

@@ -50,14 +50,14 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, const FastDiv &f) {
 // The cache, by value in the kernels' parameters.
 struct KvView {
   uint8_t *k, *v;
-  __half *ks, *vs;  // Q8_0 scales
+  __half *ks, *vs;  // scales of Q8_0 and Q4_0
   float *sums;
   int64_t n_pages, page_stride, head_stride, slot_stride;  // strides in rows
   int type, hkv, dim;
   FastDiv page;  // page size
 };
-// A row's elements in bytes (the scales of Q8_0 lie in their own plane).
-inline int kv_row_bytes(int type, int dim) { return type == MQ_Q8_0 ? dim : 2 * dim; }
+// Whether rows have scales (in planes of their own).
+inline bool kv_scaled(int type) { return type == MQ_Q8_0 || type == MQ_Q4_0; }
 
 // The first error's thread alone writes the value.  (By a store: an atomic exchange here, on a path
 // that no valid call takes, cost mq_rope_store 5 us of 64 at 16384 bf16 tokens, out of line 4.)
@@ -162,6 +162,8 @@ struct RopeArgs {
   const void *qkv;
   int64_t ld;
   const float *bias;
+  const float *norm_q, *norm_k;  // weights of the heads' norms; null: no norms
+  float eps;
   const int32_t *pos;
   const int64_t *slot;
   void *q;

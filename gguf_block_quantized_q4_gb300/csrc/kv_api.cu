@@ -12,8 +12,8 @@ namespace {
 
 mq_status check_cache(const char *site, const mq_kv_cache *c) {
   if (!c) return fail(MQ_ERR_ARG, "%s: cache is NULL", site);
-  if (c->type != MQ_F16 && c->type != MQ_BF16 && c->type != MQ_Q8_0)
-    return fail(MQ_ERR_TYPE, "%s: cache type %d (supported: 1 F16, 8 Q8_0, 30 BF16)", site,
+  if (c->type != MQ_F16 && c->type != MQ_BF16 && !kv_scaled(c->type))
+    return fail(MQ_ERR_TYPE, "%s: cache type %d (supported: 1 F16, 2 Q4_0, 8 Q8_0, 30 BF16)", site,
                 (int)c->type);
   const int d = c->head_dim;
   if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256)
@@ -71,7 +71,7 @@ mq_status cache_view(const char *site, const mq_kv_cache *c, bool sums, int dev,
   mq_status s;
   if ((s = check_dev_ptr(site, "cache.k", c->k, dev, 16)) != MQ_OK) return s;
   if ((s = check_dev_ptr(site, "cache.v", c->v, dev, 16)) != MQ_OK) return s;
-  if (c->type == MQ_Q8_0) {
+  if (kv_scaled(c->type)) {
     if ((s = check_dev_ptr(site, "cache.k_scale", c->k_scale, dev, 16)) != MQ_OK) return s;
     if ((s = check_dev_ptr(site, "cache.v_scale", c->v_scale, dev, 16)) != MQ_OK) return s;
   }
@@ -112,11 +112,11 @@ mq_status check_lengths(const char *site, const mq_kv_cache *c, int64_t S, int64
 
 }  // namespace
 
-extern "C" mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope, mq_type io,
-                                   const void *qkv, int64_t ld, const float *bias,
-                                   const int32_t *pos, const int64_t *slot, void *q, int64_t T,
-                                   int n_heads, mq_stream stream) {
-  const char *site = "mq_rope_store";
+namespace {
+
+mq_status rope_store(const char *site, const mq_kv_cache *cache, const mq_rope *rope, const mq_head_norm *norm,
+                     mq_type io, const void *qkv, int64_t ld, const float *bias, const int32_t *pos,
+                     const int64_t *slot, void *q, int64_t T, int n_heads, mq_stream stream) {
   mq_status s;
   if ((s = check_cache(site, cache)) != MQ_OK) return s;
   if ((s = check_io(site, io)) != MQ_OK) return s;
@@ -162,7 +162,12 @@ extern "C" mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope
   if ((s = check_dev_ptr(site, "pos", pos, dev, 4)) != MQ_OK) return s;
   if ((s = check_dev_ptr(site, "slot", slot, dev, 8)) != MQ_OK) return s;
   if ((s = check_dev_ptr(site, "q", q, dev, 16)) != MQ_OK) return s;
+  if (norm && (s = check_dev_ptr(site, "norm.q", norm->q, dev, 16)) != MQ_OK) return s;
+  if (norm && (s = check_dev_ptr(site, "norm.k", norm->k, dev, 16)) != MQ_OK) return s;
   a.rope = *rope;
+  a.norm_q = norm ? norm->q : nullptr;
+  a.norm_k = norm ? norm->k : nullptr;
+  a.eps = norm ? norm->eps : 0.f;
   a.io = io;
   a.qkv = qkv;
   a.ld = ld;
@@ -174,6 +179,26 @@ extern "C" mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope
   a.hq = n_heads;
   a.status = st->status;
   return launch_rope_store(a, (cudaStream_t)stream, st);
+}
+
+}  // namespace
+
+extern "C" mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope, mq_type io,
+                                   const void *qkv, int64_t ld, const float *bias,
+                                   const int32_t *pos, const int64_t *slot, void *q, int64_t T,
+                                   int n_heads, mq_stream stream) {
+  return rope_store("mq_rope_store", cache, rope, nullptr, io, qkv, ld, bias, pos, slot, q, T, n_heads, stream);
+}
+
+extern "C" mq_status mq_norm_rope_store(const mq_kv_cache *cache, const mq_rope *rope, const mq_head_norm *norm,
+                                        mq_type io, const void *qkv, int64_t ld, const float *bias,
+                                        const int32_t *pos, const int64_t *slot, void *q, int64_t T,
+                                        int n_heads, mq_stream stream) {
+  const char *site = "mq_norm_rope_store";
+  if (!norm) return fail(MQ_ERR_ARG, "%s: norm is NULL", site);
+  if (!(norm->eps >= 1e-30f && norm->eps <= 1e30f))
+    return fail(MQ_ERR_ARG, "%s: norm.eps=%g outside [1e-30, 1e30]", site, (double)norm->eps);
+  return rope_store(site, cache, rope, norm, io, qkv, ld, bias, pos, slot, q, T, n_heads, stream);
 }
 
 extern "C" size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,

@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   for (int k = NK; k < nk; ++k) place(k, far_key(k));
 }
 
-// RB: bytes of a row; ROWS: rows of a warp (16 or 32).
-template <int RB, int ROWS>
+// RB: bytes of a row; NB: scales of a row, or 0; ROWS: rows of a warp (16 or 32).
+template <int RB, int NB, int ROWS>
 __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int CH = RB / 16, STEPS = ROWS * CH / 32, NU = STEPS % 4 == 0 ? 4 : STEPS % 3 == 0 ? 3 : STEPS % 2 == 0 ? 2 : 1;
   const int s = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31;
@@ -361,8 +361,7 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
   }
   if (!on) return;
   a.c.sums[to] = sum;
-  if (a.c.type == MQ_Q8_0) {  // a lane its own row's scales
-    constexpr int NB = RB / 32;
+  if constexpr (NB > 0) {  // a lane its own row's scales
     const size_t f = size_t(from) * NB, t = size_t(to) * NB;
     __half ks[NB], vs[NB];
 #pragma unroll
@@ -372,14 +371,24 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
   }
 }
 
-template <int RB>
+template <int RB, int NB>
 mq_status launch_copy(const EvictArgs &a, cudaStream_t s, const DeviceState *st) {
+  constexpr int FEW = RB % 32 ? 32 : 16;  // (16 rows of 48 bytes are no whole number of steps)
   const int64_t rows = a.S * a.c.hkv * a.keep;
   const bool few = rows < int64_t(st->sms) * 16 * 32;  // less than 16 warps of 32 rows per SM
-  const int per_block = 8 * (few ? 16 : 32);
+  const int per_block = 8 * (few ? FEW : 32);
   const dim3 grid((a.keep + per_block - 1) / per_block, (unsigned)a.S, a.c.hkv);
-  return launch_dependent("evict_copy_kernel", few ? evict_copy_kernel<RB, 16> : evict_copy_kernel<RB, 32>,
+  return launch_dependent("evict_copy_kernel", few ? evict_copy_kernel<RB, NB, FEW> : evict_copy_kernel<RB, NB, 32>,
                           grid, dim3(256, 1, 1), 0, s, a);
+}
+
+template <int D>
+mq_status launch_type(const EvictArgs &a, cudaStream_t s, const DeviceState *st) {
+  switch (a.c.type) {
+    case MQ_Q8_0: return launch_copy<D, D / 32>(a, s, st);
+    case MQ_Q4_0: return launch_copy<D / 2, D / 32>(a, s, st);
+    default: return launch_copy<2 * D, 0>(a, s, st);
+  }
 }
 
 }  // namespace
@@ -426,14 +435,12 @@ mq_status launch_kv_evict(const EvictArgs &a, cudaStream_t s, const DeviceState 
                                dim3(ranks, (unsigned)a.S, a.c.hkv), dim3(kSelThreads, 1, 1),
                                size_t(held) * 4, s, ranks, a, held);
   if (r != MQ_OK) return r;
-  switch (a.c.type == MQ_Q8_0 ? a.c.dim : 2 * a.c.dim) {
-    case 64: return launch_copy<64>(a, s, st);
-    case 96: return launch_copy<96>(a, s, st);
-    case 128: return launch_copy<128>(a, s, st);
-    case 192: return launch_copy<192>(a, s, st);
-    case 256: return launch_copy<256>(a, s, st);
-    case 384: return launch_copy<384>(a, s, st);
-    default: return launch_copy<512>(a, s, st);
+  switch (a.c.dim) {
+    case 64: return launch_type<64>(a, s, st);
+    case 96: return launch_type<96>(a, s, st);
+    case 128: return launch_type<128>(a, s, st);
+    case 192: return launch_type<192>(a, s, st);
+    default: return launch_type<256>(a, s, st);
   }
 }
 

@@ -35,6 +35,10 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z),
                      __fadd_rn(a.w, b.w));
 }
+__device__ __forceinline__ float4 normed4(float4 x, float by, float4 w) {
+  return make_float4(__fmul_rn(__fmul_rn(x.x, by), w.x), __fmul_rn(__fmul_rn(x.y, by), w.y),
+                     __fmul_rn(__fmul_rn(x.z, by), w.z), __fmul_rn(__fmul_rn(x.w, by), w.w));
+}
 __device__ __forceinline__ void turn(float &a, float &b, float2 cs) {
   const float x = a, y = b;
   a = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
@@ -57,13 +61,81 @@ __device__ __forceinline__ uint32_t quants4(float4 v, float d) {
                      __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040), 0x5410);
 }
 
+// Q4_0 rows: a block's scale has the sign that its largest element has not, so that element is -8 or near
+// it.  The largest meets as its magnitude's bits with the sign below them (of two alike the positive one).
+__device__ __forceinline__ uint32_t signed_top4(float4 v) {
+  auto key = [](float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b << 1 | (b >> 31 ^ 1);
+  };
+  return max(max(key(v.x), key(v.y)), max(key(v.z), key(v.w)));
+}
+__device__ __forceinline__ __half block_scale4(uint32_t top) {
+  const float d = __uint_as_float(top >> 1 | (top << 31 ^ 0x80000000u)) * -0.125f;
+  return __float2half_rn(d > 65504.f ? 65504.f : d < -65504.f ? -65504.f : d);
+}
+// The numbers n of four elements, a byte each.
+__device__ __forceinline__ uint32_t numbers4(float4 v, float d) {
+  float t[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+  if (d != 0.f) quant_codes4(v, d, __frcp_rn(d), t, q);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) t[k] = __fadd_rn(fminf(fmaxf(q[k], -8.f), 7.f), kQuantMagic + 8.f);
+  return __byte_perm(__byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040),
+                     __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040), 0x5410);
+}
+
+// A sum of squares as hi + lo: what a sum rounds off goes to lo (Knuth's two-sum), and what a square
+// does (by fma).
+struct Wide {
+  float hi, lo;
+};
+__device__ __forceinline__ Wide add_wide(Wide a, Wide b) {
+  const float s = __fadd_rn(a.hi, b.hi), v = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, v)), __fsub_rn(b.hi, v));
+  return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), e)};
+}
+__device__ __forceinline__ Wide squares(float4 x, float4 y) {
+  const float2 neg = make_float2(-1.f, -1.f);
+  const float2 v[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)};
+  float2 hi, lo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // (pairs side by side)
+    const float2 p = __fmul2_rn(v[i], v[i]), e = __ffma2_rn(v[i], v[i], __fmul2_rn(p, neg));
+    if (i == 0) {
+      hi = p, lo = e;
+      continue;
+    }
+    const float2 s = __fadd2_rn(hi, p), w = __ffma2_rn(hi, neg, s);
+    const float2 a = __fadd2_rn(hi, __ffma2_rn(s, neg, w)), b = __ffma2_rn(w, neg, p);
+    lo = __fadd2_rn(lo, __fadd2_rn(e, __fadd2_rn(a, b))), hi = s;
+  }
+  return add_wide({hi.x, lo.x}, {hi.y, lo.y});
+}
+// 1 / sqrt(S / dim + eps): the approximate root y, and one step of Newton's with its residual dim - y^2
+// (S + dim eps) in two parts, so that the result is the rounded one but for values very near a tie.
+__device__ __forceinline__ float inverse_rms(Wide s, float dim, float eps) {
+  const float p = __fmul_rn(dim, eps);
+  const Wide m = add_wide(s, {p, __fmaf_rn(dim, eps, -p)});
+  const float y = rsqrtf(__fdividef(m.hi, dim));
+  const float a = __fmul_rn(y, y), b = __fmaf_rn(y, y, -a);
+  const float c = __fmul_rn(a, m.hi), d = __fmaf_rn(a, m.hi, -c);
+  const float e = __fsub_rn(__fsub_rn(__fsub_rn(dim, c), d), __fmaf_rn(a, m.lo, __fmul_rn(b, m.hi)));
+  return __fmaf_rn(y, __fmul_rn(e, __fdividef(0.5f, dim)), y);
+}
+
+// How a cache's rows are stored.
+enum Store : int { kStore16, kStoreQ8, kStoreQ4 };
+
 // per_pass: heads that the block's threads take at once; passes: the rounds of a token, of which NP
 // are loaded at a time; gridDim.y blocks share them.  A token's first loads need nothing but its
 // number, its positions and slot were read with the token before, so one latency covers a token.
-template <bool Q8, int NP, int IO>
+template <int STORE, bool NORM, int NP, int IO>
 __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_constant__ RopeArgs a,
                                                               int per_pass, int passes) {
-  __shared__ uint32_t amax[Q8 ? NP : 1][kThreads];  // [round][head of the round][32-element block]
+  constexpr bool Q8 = STORE == kStoreQ8, Q4 = STORE == kStoreQ4, QUANT = Q8 || Q4;
+  __shared__ uint32_t amax[QUANT ? NP : 1][kThreads];  // [round][head of the round][32-element block]
+  __shared__ uint32_t numbers[Q4 ? NP : 1][Q4 ? 2 * kThreads : 1];  // [round][head of the round][dim], a byte each
+  __shared__ Wide quads[NORM ? NP : 1][NORM ? kThreads / 4 : 1];  // sums of four threads, where a head's are no power of two
   const int dim = a.c.dim, units = dim / 8, hkv = a.c.hkv, heads = a.hq + 2 * hkv, nb = dim / 32;
   const int u = threadIdx.x % units, sub = threadIdx.x / units;
   const int half = a.rope.rot_dim / 2;
@@ -152,10 +224,74 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
 
     for (int pass0 = blockIdx.y * NP; pass0 < passes; pass0 += gridDim.y * NP) {
       if (pass0 != blockIdx.y * NP) load(row, pass0);
-      const bool quantises = Q8 && (pass0 + NP) * per_pass > a.hq;  // (the same for the whole block)
+      if constexpr (NORM) {
+        // bias, then the norm of the rounds' query and key heads
+        Wide sum[NP];
+        bool far = false;  // a sum past binary32
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int head = head_of(pass0 + k);
+          if (a.bias && head < heads) {
+            x[k] = add4(x[k], *reinterpret_cast<const float4 *>(a.bias + head * dim + d0));
+            y[k] = add4(y[k], *reinterpret_cast<const float4 *>(a.bias + head * dim + d0 + gap));
+          }
+        }
+        auto meet = [&](Wide (&sum)[NP]) {  // sums over a head's threads, for all of them
+          const bool whole = (units & (units - 1)) == 0;
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+            for (int i = 1; i < (whole ? units : 4); i <<= 1)
+              sum[k] = add_wide(sum[k], {__shfl_xor_sync(0xffffffffu, sum[k].hi, i),
+                                         __shfl_xor_sync(0xffffffffu, sum[k].lo, i)});
+          if (whole) return;
+          __syncthreads();  // (the sums before have been read)
+          if (threadIdx.x % 4 == 0) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) quads[NORM ? k : 0][threadIdx.x / 4] = sum[k];
+          }
+          __syncthreads();
+          const int first = min(sub, per_pass - 1) * (units / 4);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            sum[k] = quads[NORM ? k : 0][first];
+            for (int i = 1; i < units / 4; ++i) sum[k] = add_wide(sum[k], quads[NORM ? k : 0][first + i]);
+          }
+        };
+#pragma unroll
+        for (int k = 0; k < NP; ++k) sum[k] = squares(x[k], y[k]);
+        meet(sum);
+        float by[NP];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          by[k] = inverse_rms(sum[k], (float)dim, a.eps);
+          far |= !(sum[k].hi < 0x1p100f);
+        }
+        if (__syncthreads_or(far)) {  // once more in units of 2^70 (of 2^140 the squares)
+          constexpr float less = 0x1p-70f;
+          Wide small[NP];
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+            small[k] = squares(make_float4(x[k].x * less, x[k].y * less, x[k].z * less, x[k].w * less),
+                               make_float4(y[k].x * less, y[k].y * less, y[k].z * less, y[k].w * less));
+          meet(small);
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+            if (!(sum[k].hi < 0x1p100f))
+              by[k] = small[k].hi < INFINITY ? inverse_rms(small[k], (float)dim, 0.f) * less : 1.f / small[k].hi;
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int head = head_of(pass0 + k);
+          if (head >= a.hq + hkv) continue;
+          const float *const w = (head < a.hq ? a.norm_q : a.norm_k) + d0;
+          x[k] = normed4(x[k], by[k], *reinterpret_cast<const float4 *>(w));
+          y[k] = normed4(y[k], by[k], *reinterpret_cast<const float4 *>(w + gap));
+        }
+      }
+      const bool quantises = QUANT && (pass0 + NP) * per_pass > a.hq;  // (the same for the whole block)
       if (quantises) {
 #pragma unroll
-        for (int k = 0; k < NP; ++k) amax[Q8 ? k : 0][threadIdx.x] = 0;
+        for (int k = 0; k < NP; ++k) amax[QUANT ? k : 0][threadIdx.x] = 0;
         __syncthreads();
       }
 #pragma unroll
@@ -163,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
         const int head = head_of(pass0 + k);
         if (head >= heads) continue;
         const int at = head * dim + d0;
-        if (a.bias) {
+        if (!NORM && a.bias) {
           x[k] = add4(x[k], *reinterpret_cast<const float4 *>(a.bias + at));
           y[k] = add4(y[k], *reinterpret_cast<const float4 *>(a.bias + at + gap));
         }
@@ -189,6 +325,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
         if (Q8) {
           atomicMax(&amax[Q8 ? k : 0][sub * nb + d0 / 32], top4(x[k]));
           atomicMax(&amax[Q8 ? k : 0][sub * nb + d1 / 32], top4(y[k]));
+        } else if (Q4) {
+          atomicMax(&amax[QUANT ? k : 0][sub * nb + d0 / 32], signed_top4(x[k]));
+          atomicMax(&amax[QUANT ? k : 0][sub * nb + d1 / 32], signed_top4(y[k]));
         } else {
           uint16_t *const to = reinterpret_cast<uint16_t *>(key ? a.c.k : a.c.v) + ((uint64_t)r * dim + d0);
           *reinterpret_cast<uint2 *>(to) = pack4(x[k], a.c.type == MQ_BF16);
@@ -197,6 +336,32 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
       }
       if (!quantises) continue;
       __syncthreads();
+      if constexpr (Q4) {  // the numbers meet in shared memory: a byte of a row has two, 16 dims apart
+        auto wanted = [&](int head) { return head < heads && head >= a.hq && stores; };
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          if (!wanted(head_of(pass0 + k))) continue;
+          const uint32_t *const top = &amax[QUANT ? k : 0][sub * nb];
+          numbers[k][(sub * dim + d0) / 4] = numbers4(x[k], __half2float(block_scale4(top[d0 / 32])));
+          numbers[k][(sub * dim + d1) / 4] = numbers4(y[k], __half2float(block_scale4(top[d1 / 32])));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int head = head_of(pass0 + k);
+          if (!wanted(head)) continue;
+          const bool key = head < a.hq + hkv;
+          const uint32_t r = row0 + (uint32_t)(key ? head - a.hq : head - a.hq - hkv) * (uint32_t)a.c.head_stride;
+          // thread u: bytes 4u .. 4u + 3 of the row, block u / 4
+          const uint32_t *const from = &numbers[k][sub * (dim / 4) + u / 4 * 8 + u % 4];
+          *reinterpret_cast<uint32_t *>((key ? a.c.k : a.c.v) + ((uint64_t)r * (dim / 2) + 4 * u)) =
+              from[0] | from[4] << 4;
+          if (u < nb)
+            ((key ? a.c.ks : a.c.vs) + (uint64_t)r * nb)[u] = block_scale4(amax[QUANT ? k : 0][sub * nb + u]);
+        }
+        __syncthreads();
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int head = head_of(pass0 + k);
@@ -220,21 +385,26 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
 
 // (IO is a template argument so that the loads of a group stand together, without a branch on the
 // type at each)
-template <bool Q8, int NP>
+template <int STORE, bool NORM, int NP>
 mq_status launch_io(const RopeArgs &a, dim3 grid, dim3 block, int per_pass, int passes, cudaStream_t s) {
-  auto *kernel = a.io == MQ_F32   ? rope_store_kernel<Q8, NP, MQ_F32>
-                 : a.io == MQ_F16 ? rope_store_kernel<Q8, NP, MQ_F16>
-                                  : rope_store_kernel<Q8, NP, MQ_BF16>;
+  auto *kernel = a.io == MQ_F32   ? rope_store_kernel<STORE, NORM, NP, MQ_F32>
+                 : a.io == MQ_F16 ? rope_store_kernel<STORE, NORM, NP, MQ_F16>
+                                  : rope_store_kernel<STORE, NORM, NP, MQ_BF16>;
   return launch_dependent("rope_store_kernel", kernel, grid, block, 0, s, a, per_pass, passes);
 }
-template <bool Q8>
+template <int STORE, bool NORM>
 mq_status launch_rounds(const RopeArgs &a, int np, dim3 grid, dim3 block, int per_pass, int passes,
                         cudaStream_t s) {
   switch (np) {
-    case 1: return launch_io<Q8, 1>(a, grid, block, per_pass, passes, s);
-    case 2: return launch_io<Q8, 2>(a, grid, block, per_pass, passes, s);
-    default: return launch_io<Q8, 3>(a, grid, block, per_pass, passes, s);
+    case 1: return launch_io<STORE, NORM, 1>(a, grid, block, per_pass, passes, s);
+    case 2: return launch_io<STORE, NORM, 2>(a, grid, block, per_pass, passes, s);
+    default: return launch_io<STORE, NORM, 3>(a, grid, block, per_pass, passes, s);
   }
+}
+template <int STORE>
+mq_status launch_norm(const RopeArgs &a, int np, dim3 grid, dim3 block, int per_pass, int passes, cudaStream_t s) {
+  return a.norm_q ? launch_rounds<STORE, true>(a, np, grid, block, per_pass, passes, s)
+                  : launch_rounds<STORE, false>(a, np, grid, block, per_pass, passes, s);
 }
 
 }  // namespace
@@ -250,8 +420,11 @@ mq_status launch_rope_store(const RopeArgs &a, cudaStream_t s, const DeviceState
   // blocks of up to 256 threads with 64 registers: as many as are resident at once
   const int64_t resident = int64_t(st->sms) * std::max(1, std::min(2048 / (int)threads, 65536 / (64 * (int)threads)));
   const dim3 grid((unsigned)std::min(a.T, resident), split ? passes : 1, 1), block(threads, 1, 1);
-  return a.c.type == MQ_Q8_0 ? launch_rounds<true>(a, np, grid, block, per_pass, passes, s)
-                             : launch_rounds<false>(a, np, grid, block, per_pass, passes, s);
+  switch (a.c.type) {
+    case MQ_Q8_0: return launch_norm<kStoreQ8>(a, np, grid, block, per_pass, passes, s);
+    case MQ_Q4_0: return launch_norm<kStoreQ4>(a, np, grid, block, per_pass, passes, s);
+    default: return launch_norm<kStore16>(a, np, grid, block, per_pass, passes, s);
+  }
 }
 
 }  // namespace mq

@@ -334,14 +334,17 @@ mq_status mq_ffn_gu_mmq(mq_type type, const mq_weight *W, const void *xq, float 
  * A row is head_dim consecutive elements: the key (or value) of one cached token and kv head.
  * Row (page p, kv head h, slot j) has the index
  *     r = p*page_stride + h*head_stride + j*slot_stride
- * in every plane: k and v at element r*head_dim, their scales at element r*(head_dim/32),
+ * in every plane: k and v at element r*head_dim (Q4_0: byte r*head_dim/2), their scales at element r*(head_dim/32),
  * weight_sum at element r.  Any strides that keep the rows apart will do:
  * [page][head][slot] is page_stride = n_kv_heads*page_size, head_stride = page_size,
  * slot_stride = 1; [page][slot][head] is page_stride = page_size*n_kv_heads,
  * head_stride = 1, slot_stride = n_kv_heads.
- *   type       MQ_F16, MQ_BF16, or MQ_Q8_0: int8 quants in k / v and one f16 scale d per 32
- *              elements in k_scale / v_scale, value = d*q.  The scales have planes of their own
- *              because a 34-byte block would leave every row unaligned.
+ *   type       MQ_F16, MQ_BF16, MQ_Q8_0 or MQ_Q4_0.  The last two have one f16 scale d per 32
+ *              elements in k_scale / v_scale.  MQ_Q8_0: int8 quants in k / v, value = d*q.
+ *              MQ_Q4_0: head_dim/2 bytes a row in k / v, of the elements j and 16 + j of a block of
+ *              32 (j < 16) one byte, 16 to a block: n of the first in its low and of the second in
+ *              its high half, value = d*(n - 8).  The scales have planes of their own because a
+ *              34- or 18-byte block would leave every row unaligned.
  *   head_dim   64, 96, 128, 192 or 256
  *   page_size  slots of a page, 1..65536 (any number; not only powers of two)
  *   weight_sum f32, the attention weight each row has gathered (MQ_ATTN_TRACK adds,
@@ -387,12 +390,33 @@ typedef struct {
  * then rounded to io (queries) or to the cache's type (keys, and the values, which are not
  * rotated).  Q8_0 rows: per 32 elements d = f16(amax/127) (at most 65504), q = a/d rounded half
  * to even and clamped to [-127, 127], 0 where d is 0 ("Execution Plan" C4 S2b, decision 4).
+ * Q4_0 rows: per 32 elements d = f16(m/-8) (at most 65504 in magnitude), m the element of the largest
+ * magnitude with its sign (the positive one of two alike), n = 8 + a/d rounded half to even, clamped
+ * to [0, 15], 8 where d is 0.
  * The slots of one call are distinct.  A token with a position outside [0, max_pos) gets a zero
  * q and stores nothing; a slot past the cache stores nothing; both are reported by
  * mq_stream_status.  ld*sizeof(io) is a multiple of 16.  T = 0 does nothing. */
 mq_status mq_rope_store(const mq_kv_cache *cache, const mq_rope *rope, mq_type io,
                         const void *qkv, int64_t ld, const float *bias, const int32_t *pos,
                         const int64_t *slot, void *q, int64_t T, int n_heads, mq_stream stream);
+
+/* Norms of the query and key heads: weights, device f32 [head_dim] each, 16-byte aligned, and
+ * eps in [1e-30, 1e30]. */
+typedef struct {
+    const float *q, *k;
+    float eps;
+} mq_head_norm;
+
+/* mq_norm_rope_store -- mq_rope_store with a norm of every query and key head between the bias and
+ * the rotation (the pages' QkNorm, "CUDA Backend Design" §4.3):
+ *     a = x + bias;  y = (a*g)*w,  g = 1/sqrt(mean(a^2) + eps) over the head's elements,
+ * w the element's weight; then r0 = y0*c - y1*s and so on.  g is the binary32 value nearest to the
+ * exact one (or, near the middle of two, its neighbour); the two products are rounded each.  Values
+ * are not normed.  A head with an infinite element has g = 0, one with a NaN is NaN. */
+mq_status mq_norm_rope_store(const mq_kv_cache *cache, const mq_rope *rope, const mq_head_norm *norm,
+                             mq_type io, const void *qkv, int64_t ld, const float *bias,
+                             const int32_t *pos, const int64_t *slot, void *q, int64_t T,
+                             int n_heads, mq_stream stream);
 
 /* mq_attn_decode: also add the attention weights to the cache's weight_sum. */
 #define MQ_ATTN_TRACK 1u

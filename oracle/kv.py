@@ -89,3 +89,34 @@ def evict(sums, n, keep, sink, recent):
     middle = sorted(range(sink, n - recent),
                     key=lambda i: (not math.isnan(float(sums[i])), -worth(i), i))
     return sorted([*range(sink), *middle[:keep - sink - recent], *range(n - recent, n)])
+
+
+def quantise_rows4(x):
+    """Q4_0 rows of f32 x [...][D]: (the numbers n, uint8 [...][D], f16 scales)."""
+    blocks = x.astype(np.float32).reshape(*x.shape[:-1], -1, 32)
+    most, least = blocks.max(-1), blocks.min(-1)
+    m = np.where(most >= -least, most, least)
+    d = np.clip(m / np.float32(-8), np.float32(-65504), np.float32(65504)).astype(np.float16)
+    df = d.astype(np.float32)[..., None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        n = np.where(df == 0, np.float32(0), np.rint(blocks / df)) + 8
+    return np.clip(n, 0, 15).astype(np.uint8).reshape(x.shape), d
+
+
+def pack4(n):
+    """Rows of numbers [...][D] as bytes [...][D/2]."""
+    b = n.reshape(*n.shape[:-1], -1, 2, 16)
+    return (b[..., 0, :] | b[..., 1, :] << 4).astype(np.uint8).reshape(*n.shape[:-1], -1)
+
+
+def unpack4(b):
+    """Rows of bytes [...][D/2] as numbers [...][D]."""
+    x = np.asarray(b).reshape(*b.shape[:-1], -1, 16)
+    return np.stack([x & 15, x >> 4], -2).reshape(*b.shape[:-1], -1)
+
+
+def head_scale(x, eps):
+    """1 / sqrt(mean(x^2) + eps) over the last axis, in 64 bits (x: binary32 values)."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(invalid="ignore"):
+        return 1 / np.sqrt((x * x).mean(-1) + float(eps))
