@@ -68,6 +68,7 @@ ABI = {
     "mq_attn_decode": (_ST, [_P, ctypes.c_int, _P, _P, _P, _I64, _P, _I64, ctypes.c_int, _I64,
                              ctypes.c_float, _I64, ctypes.c_uint32, _P, _SZ, _P]),
     "mq_kv_evict": (_ST, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "mq_sample": (_ST, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
     "mq_stream_status": (_ST, [_P]),
     "mq_last_error": (ctypes.c_char_p, []),
     "mq_status_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -751,6 +752,47 @@ def kv_evict(cache: KVCache, pages, lens, max_len, new_pages, keep, sink=0, rece
     if status:
         _check(status)
     return kept, new_lens
+
+
+# ---- sampling ---------------------------------------------------------------------------------
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, logprob=None,
+           stream=None):
+    """The next token of each row: logits [B][V] (f32, f16 or bf16; rows may be strided), u f32 [B] in
+    [0, 1); temperature, top_p, min_p f32 [B], top_k int32 [B], or None (mq_sample says what each does).
+    Returns (token int32 [B], logprob f32 [B])."""
+    torch = _torch or _torch_setup()
+    if stream is not None and (token is None or logprob is None):
+        with torch.cuda.stream(stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, token, logprob)
+    B, V = logits.shape
+    ld, inner = logits.stride()
+    io = _IO.get(logits.dtype)
+    if io is None or (inner != 1 and V > 1):
+        _refuse(f"logits must be f32, f16 or bf16 [B][V] with contiguous rows, not {logits.dtype}, "
+                f"strides {logits.stride()}")
+    if u is None:
+        _refuse("u must be contiguous f32 [B]")
+    f32, shape = torch.float32, (B,)
+    for name, t, dtype in (("u", u, f32), ("temperature", temperature, f32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, f32), ("min_p", min_p, f32), ("token", token, torch.int32),
+                           ("logprob", logprob, f32)):
+        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+            _refuse(f"{name} must be contiguous {'int32' if dtype is torch.int32 else 'f32'} [B]")
+    if token is None:
+        token = _empty_cuda(shape, (1,), torch.int32)
+    if logprob is None:
+        logprob = _empty_cuda(shape, (1,), f32)
+    status = lib().mq_sample(
+        io, logits.data_ptr(), ld if B > 1 else V, B, V, u.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
+        None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(),
+        token.data_ptr(), logprob.data_ptr(),
+        _raw_current_stream(logits.device.index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
+    return token, logprob
 
 
 def stream_status(stream=None):

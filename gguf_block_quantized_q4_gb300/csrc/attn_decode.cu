@@ -161,14 +161,21 @@ __device__ __forceinline__ uint32_t int8_f16(uint32_t biased) {
 }
 
 // The 4-bit numbers n at the bits MASK of each half as f16x2 n - 8: 1024 + n (or 1024 + 16 n) by bits,
-// then an exact subtraction (or multiplication by 1/16 and subtraction).
+// then an exact subtraction (or multiplication by 1/16 and subtraction).  An instruction takes one
+// immediate operand, so 0x6400 and 1/16 come in registers that the compiler does not know to be
+// constants (it would make two instructions of each: 128 more for 16 keys of 128).
+struct Int4Constants {
+  uint32_t magic, sixteenth;
+};
 template <uint32_t MASK>
-__device__ __forceinline__ uint32_t int4_f16(uint32_t v) {
+__device__ __forceinline__ uint32_t int4_f16(uint32_t v, Int4Constants c) {
   static_assert(MASK == 0x000f000fu || MASK == 0x00f000f0u, "bits 0-3 or 4-7");
-  const uint32_t u = (v & MASK) | 0x64006400u, less = MASK == 0x000f000fu ? 0xe408e408u : 0xd480d480u;
-  const __half2 x = *reinterpret_cast<const __half2 *>(&u), c = *reinterpret_cast<const __half2 *>(&less);
-  const uint32_t by = 0x2c002c00u;  // 1/16
-  const __half2 r = MASK == 0x000f000fu ? __hadd2_rn(x, c) : __hfma2(x, *reinterpret_cast<const __half2 *>(&by), c);
+  uint32_t u;  // v & MASK | magic
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(u) : "r"(v), "n"(MASK), "r"(c.magic));
+  const uint32_t less = MASK == 0x000f000fu ? 0xe408e408u : 0xd480d480u;  // -1032, -72
+  const __half2 x = *reinterpret_cast<const __half2 *>(&u), y = *reinterpret_cast<const __half2 *>(&less);
+  const __half2 r = MASK == 0x000f000fu ? __hadd2_rn(x, y)
+                                        : __hfma2(x, *reinterpret_cast<const __half2 *>(&c.sixteenth), y);
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 // The two parts of a pair of weights times a pair of f16 scales, as two parts: the first part's product
@@ -696,6 +703,9 @@ attn_decode_kernel(const __grid_constant__ Params p) {
   // Q8_0: the two chunks of 16 dims side by side, keys 0-7 and 8-15 each; Q4_0: two blocks of 32
   const uint32_t v_lane8 = (C::kKeys + (lane & 7) + (lane & 8)) * C::kStride + (lane >> 4) * 16;
 
+  const uint32_t nil = p.group >> 31;  // (zero)
+  const Int4Constants i4 = {0x64006400u + nil, 0x2c002c00u + nil};
+
   // The query rows of a unit as they are read: warp w has the rows w, w + kWarps, ..., lane i the
   // dims 8 i .. 8 i + 7.
   constexpr int RPW = (C::kRows + C::kWarps - 1) / C::kWarps;
@@ -874,8 +884,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const uint32_t u = x[2 * jj + h], v = u >> 8;
-                  ka[jj][m][0][h] = int4_f16<0x000f000fu>(u), ka[jj][m][0][2 + h] = int4_f16<0x000f000fu>(v);
-                  ka[jj][m][1][h] = int4_f16<0x00f000f0u>(u), ka[jj][m][1][2 + h] = int4_f16<0x00f000f0u>(v);
+                  ka[jj][m][0][h] = int4_f16<0x000f000fu>(u, i4), ka[jj][m][0][2 + h] = int4_f16<0x000f000fu>(v, i4);
+                  ka[jj][m][1][h] = int4_f16<0x00f000f0u>(u, i4), ka[jj][m][1][2 + h] = int4_f16<0x00f000f0u>(v, i4);
                 }
             }
           }
@@ -1009,12 +1019,14 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             float sum = 0.f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              s[m][n][w] = exp2_fast(s[m][n][w] - low) * C::kUnit;
-              s[m][n][w + 2] = exp2_fast(s[m][n][w + 2] - low) * C::kUnit;
+              s[m][n][w] = exp2_fast(s[m][n][w] - low) * (C::kQ4 ? 1.f : C::kUnit);
+              s[m][n][w + 2] = exp2_fast(s[m][n][w + 2] - low) * (C::kQ4 ? 1.f : C::kUnit);
               sum += s[m][n][w] + s[m][n][w + 2];
             }
+            if (C::kQ4) sum *= C::kUnit;
             ls[n][w] = fmaf(ls[n][w], al[n][w], sum);
           }
+        const float weight_unit = C::kUnit * per_unit;  // Q4_0
         // the weights transposed: lane (g, t) gets row g's of the keys 2t, 2t + 1, 2t + 8, 2t + 9;
         // their parts, or for Q8_0 (whose blocks' scales come first) as binary32 in two halves
         uint32_t pw[MT][NT][2][C::kParts];
@@ -1031,7 +1043,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                 s[m][n][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410)) * per_unit;
                 s[m][n][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632)) * per_unit;
               } else {
-                if (C::kQ4) s[m][n][2 * h] *= per_unit, s[m][n][2 * h + 1] *= per_unit;
+                if (C::kQ4) s[m][n][2 * h] *= weight_unit, s[m][n][2 * h + 1] *= weight_unit;
                 split2<C::kBf>(s[m][n][2 * h], s[m][n][2 * h + 1], pw[m][n][h]);
 #pragma unroll
                 for (int k = 0; k < C::kParts; ++k) pw[m][n][h][k] = transpose8x8(pw[m][n][h][k]);
@@ -1065,8 +1077,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
                 for (int q = 0; q < 2; ++q) {
                   // low halves: dims 2g and 2g + 1, high halves: 16 more
                   const uint32_t u = x[2 * jj + q], v = u >> 8;
-                  va[jj][0][2 * q] = int4_f16<0x000f000fu>(u), va[jj][0][2 * q + 1] = int4_f16<0x000f000fu>(v);
-                  va[jj][1][2 * q] = int4_f16<0x00f000f0u>(u), va[jj][1][2 * q + 1] = int4_f16<0x00f000f0u>(v);
+                  va[jj][0][2 * q] = int4_f16<0x000f000fu>(u, i4), va[jj][0][2 * q + 1] = int4_f16<0x000f000fu>(v, i4);
+                  va[jj][1][2 * q] = int4_f16<0x00f000f0u>(u, i4), va[jj][1][2 * q + 1] = int4_f16<0x00f000f0u>(v, i4);
                   const uint32_t d = __byte_perm(vscale[m][2 * q][j0 / 2], vscale[m][2 * q + 1][j0 / 2], jj ? 0x7632 : 0x5410);
 #pragma unroll
                   for (int n = 0; n < NT; ++n) scale_parts(pw[m][n][q], d, pq[jj][n][q]);

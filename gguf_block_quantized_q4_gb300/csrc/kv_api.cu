@@ -1,10 +1,11 @@
-// kv_api.cu -- the C ABI entry points of the paged cache and its decode attention: argument
+// kv_api.cu -- the C ABI entry points of the paged cache, its decode attention and sampling: argument
 // validation ("minfer CUDA Backend Design" §4.9 rule 1: every violation returns a status and a
 // message that names it, before anything is launched).  Indexes that lie in device memory
 // (positions, slots, lengths, pages) are checked by the kernels.
 #include <algorithm>
 
 #include "kv.cuh"
+#include "sample.cuh"
 
 using namespace mq;
 
@@ -322,4 +323,51 @@ extern "C" mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages,
   a.new_len = new_len;
   a.status = st->status;
   return launch_kv_evict(a, (cudaStream_t)stream, st);
+}
+
+extern "C" mq_status mq_sample(mq_type io, const void *logits, int64_t ld, int64_t B, int64_t V, const float *u,
+                               const float *temperature, const int32_t *top_k, const float *top_p,
+                               const float *min_p, int32_t *token, float *logprob, mq_stream stream) {
+  const char *site = "mq_sample";
+  mq_status s;
+  if ((s = check_io(site, io)) != MQ_OK) return s;
+  if (B < 0 || B > 65535) return fail(MQ_ERR_ARG, "%s: B=%lld outside [0, 65535]", site, (long long)B);
+  if (V < 1 || V > (int64_t(1) << 19) - 1)
+    return fail(MQ_ERR_SHAPE, "%s: V=%lld outside [1, 2^19)", site, (long long)V);
+  if (ld < V || ld > (int64_t(1) << 31))
+    return fail(MQ_ERR_SHAPE, "%s: ld=%lld is less than the %lld logits of a row, or beyond 2^31", site,
+                (long long)ld, (long long)V);
+  const int esize = io == MQ_F32 ? 4 : 2;
+  struct In {
+    const char *name;
+    const void *p;
+    uint64_t bytes;
+  } const in[] = {{"logits", logits, uint64_t(B ? (B - 1) * ld + V : 0) * esize}, {"u", u, 4 * uint64_t(B)},
+                  {"temperature", temperature, 4 * uint64_t(B)}, {"top_k", top_k, 4 * uint64_t(B)},
+                  {"top_p", top_p, 4 * uint64_t(B)}, {"min_p", min_p, 4 * uint64_t(B)}};
+  // a row's outputs are written while other rows' inputs are still to be read
+  for (const In &i : in) {
+    if (i.p && overlap(token, 4 * B, i.p, i.bytes))
+      return fail(MQ_ERR_ARG, "%s: token=%p overlaps %s=%p", site, (void *)token, i.name, i.p);
+    if (i.p && logprob && overlap(logprob, 4 * B, i.p, i.bytes))
+      return fail(MQ_ERR_ARG, "%s: logprob=%p overlaps %s=%p", site, (void *)logprob, i.name, i.p);
+  }
+  if (logprob && overlap(logprob, 4 * B, token, 4 * B))
+    return fail(MQ_ERR_ARG, "%s: logprob=%p overlaps token=%p", site, (void *)logprob, (void *)token);
+  DeviceState *st = nullptr;
+  if ((s = current_state(&st, site)) != MQ_OK) return s;
+  if (B == 0) return MQ_OK;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if ((s = check_dev_ptr(site, "logits", logits, dev, esize)) != MQ_OK) return s;
+  if ((s = check_dev_ptr(site, "u", u, dev, 4)) != MQ_OK) return s;
+  for (const In &i : in)
+    if (i.p && i.p != logits && i.p != u && (s = check_dev_ptr(site, i.name, i.p, dev, 4)) != MQ_OK) return s;
+  if ((s = check_dev_ptr(site, "token", token, dev, 4)) != MQ_OK) return s;
+  if (logprob && (s = check_dev_ptr(site, "logprob", logprob, dev, 4)) != MQ_OK) return s;
+  SampleArgs a;
+  a.io = io, a.logits = logits, a.ld = ld, a.B = B, a.V = V;
+  a.u = u, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
+  a.token = token, a.logprob = logprob;
+  return launch_sample(a, (cudaStream_t)stream, st);
 }

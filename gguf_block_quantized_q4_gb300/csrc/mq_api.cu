@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "kv.cuh"
+#include "sample.cuh"
 #include "mq_common.cuh"
 
 namespace mq {
@@ -156,6 +157,7 @@ extern "C" mq_status mq_init(int device) {
   if (s == MQ_OK) s = init_matvec(st);
   if (s == MQ_OK) s = init_attn_decode(st);
   if (s == MQ_OK) s = init_kv_evict(st);
+  if (s == MQ_OK) s = init_sample(st);
   // the static scratch of mq_mmq_fused_static: looking its address up here loads this file's
   // device code (and with it the array) now, outside any stream capture of the caller
   uint8_t *scratch = nullptr;

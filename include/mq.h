@@ -487,6 +487,32 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages, int64_t pa
                       int64_t new_pages_ld, int64_t keep, int64_t sink, int64_t recent,
                       int32_t *kept, int32_t *new_len, mq_stream stream);
 
+/* mq_sample -- the next token of each row of logits, from given uniform numbers (the product of the LM head
+ * ends in such rows, "CUDA Backend Design" §4.3; the pages leave sampling to the host).
+ * For a row l of V logits (device, type io, rows of ld elements, any alignment of the element) with
+ * temperature T, m its largest logit, w_i = exp((l_i - m)/T):
+ *   top_k   of the tokens in the order of falling logits (equal ones by rising index) the first
+ *           top_k stay; all of them if top_k <= 0 or >= V
+ *   top_p   of these the shortest run from the first on whose weights sum to at least top_p times
+ *           the sum of all of them, one token at least; all if top_p >= 1 or NaN
+ *   min_p   of these the ones with w_i >= min(min_p, 1); all if min_p <= 0 or NaN
+ *   token   the first, in the order of the indexes, at which the running sum of the weights that stay
+ *           is above u times their sum (u is taken as in [0, 1): 0 below or NaN, and from 1 on the
+ *           last token that weighs something)
+ *   logprob ln(w_token / that sum); may be NULL
+ * T that is not above 0 (NaN too) is greedy: the token with the largest logit, the first of equal
+ * ones, logprob 0.  T infinite: all finite logits weigh alike.  A NaN logit counts as minus infinity, which
+ * weighs nothing; infinite ones share all weight among themselves; a row with no finite or
+ * infinite logit gives token -1, logprob minus infinity.
+ * u, temperature, top_p, min_p: device f32 [B]; top_k: device int32 [B]; each but u may be NULL
+ * (T = 1, no limit).  token: device int32 [B], logprob: device f32 [B], written; apart from the inputs
+ * and each other.  1 <= V < 2^19.  B = 0 does nothing.
+ * Weights are held to 2^-27 of themselves and in units of 2^-44 of the largest (a token below that is
+ * never drawn), sums of them exactly: results do not depend on the order of execution. */
+mq_status mq_sample(mq_type io, const void *logits, int64_t ld, int64_t B, int64_t V, const float *u,
+                    const float *temperature, const int32_t *top_k, const float *top_p,
+                    const float *min_p, int32_t *token, float *logprob, mq_stream stream);
+
 /* mq_stream_status -- synchronise `stream`, then read and clear the current
  * device's status words.  Returns MQ_OK, or MQ_ERR_TIMEOUT if a bounded
  * device-side wait expired since the last call (the message names the
