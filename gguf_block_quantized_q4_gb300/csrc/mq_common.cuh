@@ -117,9 +117,7 @@ struct DeviceState {
   // mq_kv_evict: the most selection clusters of 1, 2, 4, 8 and 16 thread blocks resident at once
   // (0: that cluster size cannot run)
   int evict_clusters[5] = {};
-  // mq_sample: the same, and the shared memory that a block's slice of a row may take
-  int sample_clusters[5] = {};
-  int sample_smem = 0;
+  int sample_clusters[5] = {};  // mq_sample: the same
   // the stream-ordered pool of the per-call activation fragment planes of the persistent
   // matvec's Q4_K / Q5_K two-tile calls (nullptr: its x warps convert x themselves)
   cudaMemPool_t xpool = nullptr;

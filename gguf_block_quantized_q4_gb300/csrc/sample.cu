@@ -8,9 +8,11 @@
 // running sum of the weights that stay passes u times their sum.
 //
 // What bounds it: the logits are read once (64 rows of 151936: 5.8 us); then latency.  A thread block
-// cluster holds a row in its shared memory, a slice of consecutive tokens per block, so everything
-// behind the reading costs no memory traffic: the maximum (one exchange over the cluster), a cut
-// (each two or three exchanges), the sums and the token (one).
+// cluster has a row, a run of consecutive tokens per block and of those one per warp, read 128 at a time:
+// such a group's maximum stays in shared memory.  What follows the maximum (one exchange over the
+// cluster) reads only the groups that can matter: a cut's tokens, or what a cut or min-p has left, are in
+// the few groups whose maxima reach them.  Only rows without limits, the sum that top-p takes its share of,
+// and flat rows read all logits again, then from the L2 cache.
 //
 // Weights are whole numbers in units of 2^-44 (44 bits for the largest; a token 2^-45 below it weighs
 // nothing, and fewer than 2^19 tokens fit a 64-bit sum).  Sums of whole numbers do not depend on their
@@ -18,14 +20,17 @@
 // (weight) is right to about 2^-27 of itself: binary32's own 2^-24 would move the running sum
 // enough to name another token in one of a few hundred rows of flat logits.
 //
-// A cut: the row's tokens are counted, or their weights added, in 2048 bins of y (45 to each halving),
-// which the cluster's blocks add to rank 0's; a scan names the bin that holds the cut.  The few
-// tokens of that bin (or, for top-k, of all bins up to it) are listed and sorted by each block for
-// itself.  Where they are more than a list holds (equal or nearly equal logits) three more rounds of
-// bins, of the logit's bits, name the logit and a count of equals the index.
+// A cut: the groups' maxima are counted in 2048 bins of y (45 to each halving), which the cluster's blocks
+// add up; a scan names the bin down to which k of them lie.  There are at least k tokens down to that
+// bin and hardly any more: these are listed, and sorted by each block for itself.  Where k is too large for
+// that, or the listed tokens have too small a share, all tokens are counted, or their weights added, in
+// the bins; the few tokens of the bin that holds the cut are listed then.  Where they are more than
+// a list holds (nearly equal logits) the bin is divided in 2048 once more, and where that does not do
+// (equal ones) three rounds of bins, of the logit's bits, name the logit and a count of equals the index.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "kv.cuh"
 #include "sample.cuh"
@@ -39,12 +44,15 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPer = kBins / kThreads;  // bins of a thread in a scan
+constexpr int kSide = 4;                              // tokens of a lane side by side
+constexpr int kGroup = 32 * kSide;                    // of a warp: a group
 constexpr int kList = 1024;                           // tokens listed and sorted
+constexpr int kQuick = kList / 2;                     // groups' maxima that a list's tokens are found by
 constexpr int kMaxRanks = 16;
-constexpr int kUnit = 44;            // weights in units of 2^-kUnit
-constexpr float kDeep = 45.f;        // y from which a token weighs nothing
 constexpr float kBinsPerHalving = 45.f;
 constexpr int kLastBin = kBins - 1;  // (2025 and up weigh nothing)
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added to a number, it leaves the nearest integer in the low bits
+constexpr uint32_t kMagicBits = 0x4b400000u;
 
 struct Shared {
   // the block's bins, low and high words; while a cut's tokens are sorted: its own list, all lists
@@ -52,15 +60,15 @@ struct Shared {
     uint32_t bins[2][kBins];
     u64 list[2][kList];
   };
-  uint32_t total[2][kBins];  // rank 0's: the cluster's bins
   u64 warp_sum[kWarps];
-  uint32_t warp_key[kWarps], warp_index[kWarps];
-  uint32_t rank_key[kMaxRanks], rank_index[kMaxRanks], rank_n[kMaxRanks];
+  uint32_t warp_key[kWarps];
+  uint32_t rank_key[kMaxRanks], rank_n[kMaxRanks];
   u64 rank_sum[kMaxRanks];
   u64 above, inside;  // of the bin that was chosen: what lies before it, and in it
-  uint32_t bin, listed, cut_key, cut_index;
-  float c_hi, c_lo, floor_less;
-  u64 sum;
+  uint32_t bin, listed, cut_index;
+  float c_hi, c_lo, least;
+  double floor_log;  // T ln(min_p)
+  u64 sum, wanted;
 };
 
 // Order of the logits as unsigned numbers (-0 as 0), and back.
@@ -73,25 +81,29 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 }
 
 struct Scale {
-  float top, hi, lo;  // m; log2(e) / T in two parts
+  float top, hi, lo;  // m (finite); log2(e) / T in two parts
+  // Weights are in units of 2^-unit: 44, or 34 in rows of which a quarter or more of the groups of 128 tokens
+  // reach 2^-8 of the largest (these rows' sums are far above that one).  A weight has less than 32
+  // bits from y = unit - 30 (`deep`) on.
+  int unit;
+  float deep;
 };
-// y of a logit, rounded: for the bins (it falls with the logit, never the other way round).
 __device__ __forceinline__ float depth(const Scale &s, float x) { return __fmul_rn(__fsub_rn(s.top, x), s.hi); }
+// The bin of a logit by its y, rounded (which falls with the logit, never the other way round).
 __device__ __forceinline__ int bin_of(const Scale &s, float x) {
-  if (x == s.top) return 0;
-  const float y = depth(s, x);
-  return y < kDeep ? (int)(y * kBinsPerHalving) : kLastBin;  // (NaN: infinite logits, infinite temperatures)
+  return (int)min(__float_as_uint(__fmaf_rn(depth(s, x), kBinsPerHalving, kMagic)) - kMagicBits, (uint32_t)kLastBin);
 }
-// The weight 2^-y in units of 2^-kUnit.  The difference, its product with log2(e) / T and 1 + ln 2 f are
-// carried in two parts; n is y rounded and f = n - y, so that 2^-y = 2^-n e^(f ln 2), whose
-// series runs to the ninth power (|f ln 2| < 0.347: the tenth is 2^-37).
-__device__ __forceinline__ u64 weight(const Scale &s, float x) {
-  if (x == s.top) return u64(1) << kUnit;
-  const float d = __fsub_rn(s.top, x), y = __fmul_rn(d, s.hi);
-  if (!(y < kDeep)) return 0;
-  const float b = __fsub_rn(d, s.top);
-  const float e = __fsub_rn(__fsub_rn(s.top, __fsub_rn(d, b)), __fadd_rn(x, b));  // top - x - d
-  const float less = __fmaf_rn(d, s.hi, -y) + __fmaf_rn(d, s.lo, e * s.hi);       // y's second part
+// The weight 2^-y in units of 2^-unit.  The product of the difference d with log2(e) / T is carried in two
+// parts; n is y rounded and f = n - y, so that 2^-y = 2^-n 2^f.  From y = 8 on (or 4, for the smaller
+// unit; most tokens of most rows) 2^f is the hardware's, and the weight right to 2^-21, with an error that is as
+// often above as below (its mean over f is -8e-9).  Above it (precise) 2^f is the series of e^(f ln 2) to
+// the ninth power (|f ln 2| < 0.347: the tenth is 2^-37), with the rounding of d and 1 + f ln 2 in two
+// parts: 2^-27.
+__device__ __noinline__ u64 precise(float top, float hi, float lo, float x, int unit) {
+  const float d = __fsub_rn(top, x), y = __fmul_rn(d, hi);
+  const float b = __fsub_rn(d, top);
+  const float e = __fsub_rn(__fsub_rn(top, __fsub_rn(d, b)), __fadd_rn(x, b));  // top - x - d
+  const float less = __fmaf_rn(d, hi, -y) + __fmaf_rn(d, lo, e * hi);           // y's second part
   const float n = rintf(y), f = __fsub_rn(n, y);
   constexpr float ln2 = 0.693147182464599609375f, ln2_lo = -1.904654323148236e-9f;
   const float t = __fmul_rn(f, ln2);
@@ -101,10 +113,52 @@ __device__ __forceinline__ u64 weight(const Scale &s, float x) {
   q = fmaf(q, t, 1.f / 120), q = fmaf(q, t, 1.f / 24), q = fmaf(q, t, 1.f / 6), q = fmaf(q, t, 0.5f);
   const float rest = fmaf(t * t, q, fmaf(t, t_lo, t_lo));
   const int mantissa = (1 << 30) + __float2int_rn(t * 0x1p30f) + __float2int_rn(rest * 0x1p30f);
-  return (u64(uint32_t(mantissa)) << (kUnit - 30)) >> (int)n;
+  return (u64(uint32_t(mantissa)) << (unit - 30)) >> (int)n;
+}
+// kSide tokens' weights where all are deep; where not (`any`), those that are by whole().
+struct Weights {
+  uint32_t w[kSide], v[kSide], by[kSide];
+  bool any;
+  __device__ __forceinline__ Weights(const Scale &s, const float (&x)[kSide]) {
+    any = false;
+#pragma unroll
+    for (int q = 0; q < kSide; ++q) {
+      const float d = __fsub_rn(s.top, x[q]), y = __fmul_rn(d, s.hi), m = __fadd_rn(y, kMagic);
+      const float n = __fsub_rn(m, kMagic), f = __fmaf_rn(-d, s.lo, __fmaf_rn(-d, s.hi, n));
+      float r;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
+      // r in [0.70, 1.42] as a whole number of 2^-22, in the low bits of its sum with 2^23; to the left by 8 and
+      // to the right by n - (unit - 30).  (Past 31 the shift leaves zero: all of y from 45 on,
+      // infinities and NaN, whose m are larger or no numbers.)
+      v[q] = __float_as_uint(__fmaf_rn(r, 0x1p22f, 0x1p23f)) << 8;
+      by[q] = __float_as_uint(m) - (kMagicBits + (uint32_t)(s.unit - 30));
+      w[q] = __funnelshift_rc(v[q], 0u, by[q]);
+      any |= y < s.deep;
+    }
+  }
+  __device__ __forceinline__ u64 whole(const Scale &s, const float (&x)[kSide], int q) const {
+    const float y = depth(s, x[q]);
+    return y < fminf(s.deep, 8.f) ? precise(s.top, s.hi, s.lo, x[q], s.unit) : y < s.deep ? (u64)v[q] << -by[q] : w[q];
+  }
+};
+__device__ __noinline__ u64 weight(const Scale &s, float x) {
+  const float in[kSide] = {x, -INFINITY, -INFINITY, -INFINITY};
+  return Weights(s, in).whole(s, in, 0);
 }
 
-__device__ __forceinline__ u64 shfl_up(u64 v, int by) { return __shfl_up_sync(0xffffffffu, v, by); }
+// floor(x v) for 0 < x < 1, and whether x v is more than that.
+__device__ __forceinline__ u64 part_of(float x, u64 v, bool &more) {
+  const uint32_t bits = __float_as_uint(x), e = bits >> 23;
+  const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits;  // x = m 2^-k
+  const int k = 150 - max((int)e, 1);                       // 24 .. 149
+  const u64 lo = m * v, hi = __umul64hi(m, v);
+  if (k < 64) {
+    more = (lo & ((u64(1) << k) - 1)) != 0;
+    return hi << (64 - k) | lo >> k;
+  }
+  more = lo || k - 64 >= 64 || (hi & ((u64(1) << (k - 64)) - 1));
+  return k < 128 ? hi >> (k - 64) : 0;
+}
 
 // Adds to a 64-bit sum kept as two words (a 64-bit atomic on shared memory is a loop of exchanges).
 __device__ __forceinline__ void add_to(uint32_t *lo, uint32_t *hi, u64 v) {
@@ -112,16 +166,171 @@ __device__ __forceinline__ void add_to(uint32_t *lo, uint32_t *hi, u64 v) {
   const uint32_t up = (uint32_t)(v >> 32) + (before + w < before);
   if (up) atomicAdd(hi, up);
 }
+__device__ __forceinline__ void add_to(uint32_t *lo, uint32_t *hi, uint32_t w) {
+  const uint32_t before = atomicAdd(lo, w);
+  if (before + w < before) atomicAdd(hi, 1u);
+}
 
+// What a block's threads do together.  (Functions of their own, called from several places: a row passes
+// through each code only once or twice, and what it costs to fetch counts.)
+
+// Sums over the threads up to this one; over all in sh.sum, for thread 0 at once and for the others
+// behind a barrier.
+__device__ __noinline__ u64 scan(Shared &sh, u64 v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 upto = v;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, upto, i);
+    if (lane >= i) upto += o;
+  }
+  __syncthreads();  // (the sums before have been read)
+  if (lane == 31) sh.warp_sum[warp] = upto;
+  __syncthreads();
+  u64 all = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) before = all;
+    all += sh.warp_sum[w];
+  }
+  if (threadIdx.x == 0) sh.sum = all;
+  return before + upto;
+}
+
+// What a cut asks for: a number, or of the sum the share p (at least something).
+struct Need {
+  u64 fixed;
+  float p;  // used where fixed is 0
+  __device__ __forceinline__ u64 of(u64 all) const {
+    if (fixed) return fixed;
+    if (!(p > 0.f)) return 1;
+    bool more;
+    const u64 n = part_of(p, all, more) + more;
+    return max(n, u64(1));
+  }
+};
+
+// The block's bins added up over the cluster, and the bin at which their sum reaches what is needed
+// (returned): sh.bin, sh.above, sh.inside.
+__device__ __noinline__ u64 choose(Shared &sh, uint32_t *totals, bool counts, Need need) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), tid = threadIdx.x, run = kBins / ranks;
+  // a bin's word in the rank that adds it up
+  auto owner = [&](int bin) { return cluster.map_shared_rank(totals, bin / run) + bin % run; };
+  __syncthreads();
+  const uint32_t *low = &sh.bins[0][kPer * tid], *high = &sh.bins[1][kPer * tid];
+  if (ranks > 1) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = q * kThreads + tid;
+      const uint32_t lo = sh.bins[0][i], hi = counts ? 0 : sh.bins[1][i];
+      if ((lo | hi) == 0) continue;
+      uint32_t *const to = owner(i);
+      if (counts) atomicAdd(to, lo);
+      else add_to(to, to + run, (u64)hi << 32 | lo);
+    }
+    cluster.sync();
+    low = owner(kPer * tid), high = low + run;
+  }
+  static_assert(kPer == 4, "a thread reads four bins at once");
+  const uint4 lo = *reinterpret_cast<const uint4 *>(low), hi = *reinterpret_cast<const uint4 *>(high);
+  const u64 v[kPer] = {(u64)hi.x << 32 | lo.x, (u64)hi.y << 32 | lo.y, (u64)hi.z << 32 | lo.z, (u64)hi.w << 32 | lo.w};
+  const u64 mine = v[0] + v[1] + v[2] + v[3];
+  u64 before = scan(sh, mine) - mine;
+  if (tid == 0) sh.wanted = need.of(sh.sum);
+  __syncthreads();
+  const u64 wanted = sh.wanted;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (before < wanted && wanted <= before + v[q]) sh.bin = kPer * tid + q, sh.above = before, sh.inside = v[q];
+    before += v[q];
+  }
+  __syncthreads();
+  return wanted;
+}
+
+// The lists of the cluster's blocks (sh.listed tokens in sh.list[0]), sorted in sh.list[1]: the largest key
+// first, equal ones by their index.  Their number, or -1 where they are too many.
+__device__ __noinline__ int sort_lists(Shared &sh, int rank) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), tid = threadIdx.x;
+  u64 *const sorted = sh.list[1];
+  __syncthreads();
+  if (tid < ranks) *cluster.map_shared_rank(&sh.rank_n[rank], tid) = sh.listed;
+  cluster.sync();
+  int all = 0;
+  for (int q = 0; q < ranks; ++q) all += (int)min(sh.rank_n[q], (uint32_t)kList + 1);
+  if (tid == 0) sh.listed = 0;
+  if (all > kList) return -1;
+  int size = 32;  // a power of two
+  while (size < all) size *= 2;
+  for (int i = tid; i < size; i += kThreads) {
+    u64 v = 0;
+    int at = i;
+    for (int q = 0; q < ranks; ++q) {
+      const int there = (int)sh.rank_n[q];
+      if (at < there) {
+        v = cluster.map_shared_rank(sh.list[0], q)[at];
+        break;
+      }
+      at -= there;
+    }
+    sorted[i] = v;
+  }
+  __syncthreads();
+  for (int len = 2; len <= size; len *= 2)  // bitonic
+    for (int gap = len / 2; gap; gap /= 2) {
+      for (int t = tid; t < size / 2; t += kThreads) {
+        const int i = 2 * t - (t & (gap - 1)), j = i + gap;
+        const u64 x = sorted[i], y = sorted[j];
+        if ((x < y) == ((i & len) == 0)) sorted[i] = y, sorted[j] = x;
+      }
+      __syncthreads();
+    }
+  return all;
+}
+
+// The place in the sorted list's first `most` tokens at which their weights' sum, from `above` on,
+// reaches what is needed.
+__device__ __noinline__ int place_by_weight(Shared &sh, const Scale &s, int most, u64 above, Need need) {
+  constexpr int N = kList / kThreads;
+  u64 w[N], mine = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int i = N * threadIdx.x + q;
+    w[q] = i < most ? weight(s, logit_of((uint32_t)(sh.list[1][i] >> 32))) : 0;
+    mine += w[q];
+  }
+  u64 before = scan(sh, mine) - mine + above;
+  if (threadIdx.x == 0) sh.wanted = need.of(above + sh.sum);
+  __syncthreads();
+  const u64 wanted = sh.wanted;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    if (before < wanted && wanted <= before + w[q]) sh.bin = N * threadIdx.x + q;
+    before += w[q];
+  }
+  __syncthreads();
+  return (int)sh.bin;
+}
+
+// per_rank: tokens of a block; groups: of a warp (their tokens are consecutive).
 template <int IO>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int per_rank) {
-  extern __shared__ __align__(16) float slice[];  // [per_rank]
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int groups) {
+  extern __shared__ __align__(16) uint32_t totals[];  // the cluster's bins of this rank's run; the groups' maxima
   __shared__ __align__(16) Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.y;
-  for (int i = tid; i < 2 * kBins; i += kThreads) (&sh.bins[0][0])[i] = (&sh.total[0][0])[i] = 0;
+  float *const maxima = reinterpret_cast<float *>(totals + (ranks > 1 ? 2 * kBins / ranks : 0));  // [kWarps][groups]
+  float *const mine = maxima + warp * groups;
+  auto zero = [&] {
+    for (int i = tid; i < 2 * kBins; i += kThreads) (&sh.bins[0][0])[i] = 0;
+    if (ranks > 1)
+      for (int i = tid; i < 2 * kBins / ranks; i += kThreads) totals[i] = 0;
+  };
+  zero();
   if (tid == 0) sh.listed = 0;
   cluster.barrier_arrive();  // (every block's shared memory exists and is clear; waited for below)
   grid_dependency();
@@ -130,368 +339,465 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.f, floor_p = a.min_p ? a.min_p[row] : 0.f;
   const float u = a.u[row];
-  const bool greedy = !(T > 0.f), by_count = k > 0 && k < a.V, by_share = p < 1.f, by_floor = floor_p > 0.f;
-  if (tid == 0 && !greedy) {
-    const double c = 1.4426950408889634 / (double)T;
-    sh.c_hi = (float)c, sh.c_lo = (float)(c - (double)sh.c_hi);
-  }
+  const bool greedy = !(T > 0.f), by_count = k > 0 && k < a.V, by_share = p < 1.f;
+  const bool by_floor = floor_p > 0.f && T < INFINITY;
 
-  // ---- the slice: tokens first .. first + n - 1 ----
-  // The row's 16-byte blocks in order, as it lies in memory; a token that is none is -inf.
+  // ---- the tokens ----
+  // They are counted from the 8 or 16-byte block that the row starts in (`off` before its start), so that
+  // lane i of a group has its tokens 4 i .. 4 i + 3 in one aligned load; what is none is -inf.
   using E = typename std::conditional<IO == MQ_F32, float, uint16_t>::type;
-  constexpr int EB = 16 / sizeof(E);  // elements of a block
   const E *const from = static_cast<const E *>(a.logits) + row * a.ld;
-  const int off = (int)(reinterpret_cast<uintptr_t>(from) % 16 / sizeof(E));
-  const int first = rank * per_rank - off;  // (below 0 in rank 0 where the row starts inside a block)
-  const int n = max(0, min(per_rank, (int)a.V - first));
-  auto read = [&](int i) { return load_io1(from, IO, i); };
-  auto clean = [](float x) { return x == x ? x : -INFINITY; };
-  float top = -INFINITY;
-  {
-    constexpr int U = 4;
-    for (int c0 = tid; c0 * EB < n; c0 += U * kThreads) {
-      uint4 v[U];
+  const int off = (int)(reinterpret_cast<uintptr_t>(from) % (kSide * sizeof(E)) / sizeof(E)), V = (int)a.V;
+  const int first = (rank * kWarps + warp) * groups * kGroup - off + kSide * lane;  // this lane's first token
+  bool infinite = false;  // a row with infinite logits, which share all weight
+  struct Raw {
+    uint4 v;
+  };
+  auto load = [&](int i) {  // four tokens as they are stored
+    Raw r;
+    if (IO == MQ_F32) {
+      r.v = *reinterpret_cast<const uint4 *>(from + i);
+    } else {
+      const uint2 h = *reinterpret_cast<const uint2 *>(from + i);
+      r.v = make_uint4(h.x, h.y, 0, 0);
+    }
+    return r;
+  };
+  auto convert = [&](const Raw &r, float (&x)[kSide]) {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int i = first + (c0 + q * kThreads) * EB;
-        if (i >= 0 && i + EB <= a.V && (c0 + q * kThreads) * EB < n) v[q] = *reinterpret_cast<const uint4 *>(from + i);
-      }
+    for (int q = 0; q < kSide; ++q) {
+      const uint16_t h = (uint16_t)(w[q / 2] >> 16 * (q & 1));
+      x[q] = IO == MQ_F32    ? __uint_as_float(w[q])
+             : IO == MQ_BF16 ? __uint_as_float(uint32_t(h) << 16)
+                             : __half2float(__ushort_as_half(h));
+      if (infinite) x[q] = x[q] == INFINITY ? 0.f : -INFINITY;
+    }
+  };
+  auto fetch = [&](int g) {  // a group's tokens of this lane, where all are in the row
+    const int i = first + g * kGroup;
+    return i >= 0 && i + kSide <= V ? load(i) : Raw();
+  };
+  auto decode = [&](const Raw &r, int g, float (&x)[kSide]) {
+    const int i = first + g * kGroup;
+    convert(r, x);
+    if (!(i >= 0 && i + kSide <= V)) {  // (at the row's ends)
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int at = (c0 + q * kThreads) * EB, i = first + at;
-        if (at >= n) break;
-        float x[EB];
-        if (i >= 0 && i + EB <= a.V) {
-          const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-          for (int e = 0; e < EB; ++e) {
-            if (IO == MQ_F32) {
-              x[e] = __uint_as_float(w[e % 4]);
-            } else {
-              const uint16_t h = (uint16_t)(w[e / 2 % 4] >> 16 * (e & 1));
-              x[e] = IO == MQ_BF16 ? __uint_as_float(uint32_t(h) << 16) : __half2float(__ushort_as_half(h));
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < EB; ++e) x[e] = i + e >= 0 && i + e < a.V ? read(i + e) : -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < EB; ++e) x[e] = clean(x[e]), top = fmaxf(top, x[e]);
-#pragma unroll
-        for (int e = 0; e < EB; e += 4)
-          *reinterpret_cast<float4 *>(slice + at + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      for (int q = 0; q < kSide; ++q) {
+        x[q] = i + q >= 0 && i + q < V ? load_io1(from, IO, i + q) : -INFINITY;
+        if (infinite) x[q] = x[q] == INFINITY ? 0.f : -INFINITY;
       }
     }
-  }
-  // (what the last block of 16 bytes has past the slice's end is -inf and belongs to no token)
-  const int run = ((n + kThreads - 1) / kThreads) | 1;  // a thread's tokens, for passes in order: an
-  const int r0 = min(tid * run, n), r1 = min(r0 + run, n);  // odd number, so no two share a bank
+  };
+  // The groups of warp `of` (from g0 on, every `step`-th) whose maximum reaches `border`: U of them on their way
+  // at a time, then what(tokens, group) each, the group as this warp counts.
+  auto visit = [&](auto U, int of, int g0, int step, float border, auto what) {
+    const float *const best = maxima + of * groups;
+    const int shift = (of - warp) * groups;
+    for (int base = g0; base < groups; base += 32 * step) {
+      const int at = base + lane * step;
+      const float there = at < groups ? best[at] : -INFINITY;
+      unsigned todo = __ballot_sync(0xffffffffu, there >= border && there > -INFINITY);
+      while (todo) {
+        int g[U.value];
+        Raw r[U.value];
+#pragma unroll
+        for (int j = 0; j < U.value; ++j) {
+          g[j] = todo ? base + (__ffs(todo) - 1) * step : -1;
+          todo &= todo - 1;
+          if (g[j] >= 0) r[j] = fetch(g[j] + shift);
+        }
+#pragma unroll
+        for (int j = 0; j < U.value; ++j) {
+          if (g[j] < 0) break;
+          float x[kSide];
+          decode(r[j], g[j] + shift, x);
+          what(x, g[j] + shift);
+        }
+      }
+    }
+  };
+  // All of the warp's groups in order: four loads on their way, without a look at the row's ends where they
+  // are not near.
+  auto each_group = [&](auto what) {
+    constexpr int U = 4;
+    const int start = first - kSide * lane;  // the warp's first token
+    for (int g0 = 0; g0 < groups; g0 += U) {
+      const int at = start + g0 * kGroup;
+      if (at >= V) break;
+      if (at >= 0 && at + U * kGroup <= V && g0 + U <= groups) {
+        Raw r[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) r[j] = load(first + (g0 + j) * kGroup);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          float x[kSide];
+          convert(r[j], x);
+          what(x, g0 + j);
+        }
+      } else {
+#pragma unroll 1
+        for (int g = g0; g < min(g0 + U, groups); ++g) {
+          float x[kSide];
+          decode(fetch(g), g, x);
+          what(x, g);
+        }
+      }
+    }
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  auto each = [&](float border, auto what) { visit(Two(), warp, 0, 1, border, what); };
+  auto each_at_leisure = [&](float border, auto what) { visit(One(), warp, 0, 1, border, what); };
+
+  float top = -INFINITY;
+  for (int g = lane; g < groups; g += 32) mine[g] = -INFINITY;  // (groups behind the row)
+  __syncwarp();
+  each_group([&](const float (&x)[kSide], int g) {
+    // (the maximum takes the number of a number and a NaN)
+    const float t = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), -INFINITY);
+    const float best = logit_of(__reduce_max_sync(0xffffffffu, key_of(t)));
+    if (lane == 0) mine[g] = best;
+    top = fmaxf(top, best);
+  });
 
   // ---- the maximum ----
-  uint32_t top_key = __reduce_max_sync(0xffffffffu, key_of(top));
+  uint32_t top_key = key_of(top);
   if (lane == 0) sh.warp_key[warp] = top_key;
+  if (tid == kThreads - 1 && !greedy) {  // one thread for all
+    // log2(e) / T: the quotient, and its remainder over T
+    constexpr float e_hi = 1.44269502162933349609375f, e_lo = 1.92596299112661746887e-8f;
+    const float c = fminf(__fdiv_rn(e_hi, T), FLT_MAX);  // (finite, so that the largest logit's y is 0)
+    const float rest = __fdiv_rn(__fmaf_rn(-c, T, e_hi) + e_lo, T);
+    sh.c_hi = c, sh.c_lo = c > 0.f && c < FLT_MAX ? rest : 0.f;
+    // (of min-p the border is exact to 64 bits: in flat rows thousands of tokens lie near it)
+    if (by_floor) sh.floor_log = (double)T * log((double)fminf(floor_p, 1.f));
+  }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top_key = max(top_key, sh.warp_key[w]);
-  uint32_t top_index = 0xffffffffu;
-  if (greedy) {  // the block's first token with its maximum
-    for (int i = r0; i < r1; ++i)
-      if (key_of(slice[i]) == top_key) {
-        top_index = first + i;
-        break;
-      }
-    top_index = __reduce_min_sync(0xffffffffu, top_index);
-    if (lane == 0) sh.warp_index[warp] = top_index;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) top_index = min(top_index, sh.warp_index[w]);
-  }
   cluster.barrier_wait();
-  if (tid < ranks) {
-    *cluster.map_shared_rank(&sh.rank_key[rank], tid) = top_key;
-    *cluster.map_shared_rank(&sh.rank_index[rank], tid) = top_index;
-  }
+  if (tid < ranks) *cluster.map_shared_rank(&sh.rank_key[rank], tid) = top_key;
   cluster.sync();
-  for (int q = 0; q < ranks; ++q) {
-    const uint32_t key = sh.rank_key[q];
-    if (key > top_key) top_key = key, top_index = sh.rank_index[q];
-    else if (key == top_key) top_index = min(top_index, sh.rank_index[q]);
-  }
-  const Scale s = {logit_of(top_key), sh.c_hi, sh.c_lo};
+  int winner = 0;  // the first rank with the row's maximum
+  top_key = sh.rank_key[0];
+  for (int q = 1; q < ranks; ++q)
+    if (sh.rank_key[q] > top_key) top_key = sh.rank_key[q], winner = q;
+  Scale s = {logit_of(top_key), sh.c_hi, sh.c_lo, 44, 14.f};
   auto finish = [&](int token, float logprob) {
     a.token[row] = token;
     if (a.logprob) a.logprob[row] = logprob;
   };
-  if (greedy || s.top == -INFINITY) {
-    if (rank == 0 && tid == 0) {
-      if (s.top == -INFINITY)
-        finish(-1, -INFINITY);
-      else
-        finish((int)top_index, 0.f);
-    }
+  if (s.top == -INFINITY) {
+    if (rank == 0 && tid == 0) finish(-1, -INFINITY);
     return;
+  }
+  if (greedy) {  // the first token with the maximum: of its rank the first warp's
+    if (rank != winner) return;
+    int w = 0;
+    while (sh.warp_key[w] != top_key) ++w;
+    if (w != warp) return;
+    uint32_t index = 0xffffffffu;
+    each_at_leisure(s.top, [&](const float (&x)[kSide], int g) {
+#pragma unroll
+      for (int q = 0; q < kSide; ++q)
+        if (x[q] == s.top) index = min(index, (uint32_t)(first + g * kGroup + q));
+    });
+    index = __reduce_min_sync(0xffffffffu, index);
+    if (lane == 0) finish((int)index, 0.f);
+    return;
+  }
+  if (s.top == INFINITY) {
+    infinite = true, s.top = 0.f;
+    for (int g = lane; g < groups; g += 32) mine[g] = mine[g] == INFINITY ? 0.f : -INFINITY;
+    __syncthreads();
   }
 
   // ---- the cuts ----
-  uint32_t cut_key = 0, cut_index = 0xffffffffu;  // the last that stays: no cut yet
-  auto stays = [&](uint32_t key, int i) { return key > cut_key || (key == cut_key && (uint32_t)(first + i) <= cut_index); };
-
-  // Sums over the threads up to this one, and over all (sh.sum).
-  auto scan = [&](u64 v) {
-    u64 upto = v;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-      const u64 o = shfl_up(upto, i);
-      if (lane >= i) upto += o;
-    }
-    __syncthreads();  // (the sums before have been read)
-    if (lane == 31) sh.warp_sum[warp] = upto;
-    __syncthreads();
-    u64 all = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) before = all;
-      all += sh.warp_sum[w];
-    }
-    if (tid == 0) sh.sum = all;
-    return before + upto;
-  };
+  // What stays: larger logits than cut, and equal ones up to cut_index.
+  float cut = -INFINITY;
+  int cut_index = -1;
+  auto stays = [&](float x, int i) { return x > cut || (x == cut && i <= cut_index); };
   bool fresh = true;  // the bins are clear
   auto clear = [&] {
     if (!fresh) {
       cluster.sync();  // (the totals, and what is listed in the bins' place, have been read)
-      for (int i = tid; i < 2 * kBins; i += kThreads) (&sh.bins[0][0])[i] = (&sh.total[0][0])[i] = 0;
+      zero();
       cluster.sync();
     }
     fresh = false;
   };
-  // The bins, filled by add(), over the cluster; then the bin at which their sum reaches need(sum of all):
-  // sh.bin, sh.above, sh.inside.
-  auto choose = [&](auto add, auto need) {
-    clear();
-    add();
-    __syncthreads();
-    uint32_t(*total)[kBins] = sh.bins;
-    if (ranks > 1) {
-      total = reinterpret_cast<uint32_t(*)[kBins]>(cluster.map_shared_rank(&sh.total[0][0], 0));
-      for (int i = tid; i < kBins; i += kThreads) {
-        const u64 v = (u64)sh.bins[1][i] << 32 | sh.bins[0][i];
-        if (v) add_to(&total[0][i], &total[1][i], v);
-      }
-      cluster.sync();
-    }
-    const uint4 lo = *reinterpret_cast<const uint4 *>(&total[0][kPer * tid]);
-    const uint4 hi = *reinterpret_cast<const uint4 *>(&total[1][kPer * tid]);
-    const u64 v[kPer] = {(u64)hi.x << 32 | lo.x, (u64)hi.y << 32 | lo.y, (u64)hi.z << 32 | lo.z, (u64)hi.w << 32 | lo.w};
-    const u64 mine = v[0] + v[1] + v[2] + v[3];
-    u64 before = scan(mine) - mine;
-    __syncthreads();
-    const u64 wanted = need(sh.sum);
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      if (before < wanted && wanted <= before + v[q]) sh.bin = kPer * tid + q, sh.above = before, sh.inside = v[q];
-      before += v[q];
-    }
-    __syncthreads();
-    return wanted;
-  };
-  static_assert(kPer == 4, "a thread reads four bins at once");
-
-  // Lists the cluster's tokens that wanted() names, sorted: the largest key first, equal ones by their
-  // index.  False where they are too many.
-  u64 *const sorted = sh.list[1];
-  auto list = [&](auto wanted) -> int {
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = slice[i];
-      if (!wanted(x, i)) continue;
-      const uint32_t at = atomicAdd(&sh.listed, 1u);
-      if (at < kList) sh.list[0][at] = (u64)key_of(x) << 32 | ~(uint32_t)(first + i);
-    }
-    __syncthreads();
-    if (tid < ranks) *cluster.map_shared_rank(&sh.rank_n[rank], tid) = sh.listed;
-    cluster.sync();
-    int all = 0;
-    for (int q = 0; q < ranks; ++q) all += (int)min(sh.rank_n[q], (uint32_t)kList + 1);
-    if (tid == 0) sh.listed = 0;
-    if (all > kList) return -1;
-    int size = 32;  // a power of two
-    while (size < all) size *= 2;
-    for (int i = tid; i < size; i += kThreads) {
-      u64 v = 0;
-      int at = i;
-      for (int q = 0; q < ranks && at >= 0; ++q) {
-        const int there = (int)sh.rank_n[q];
-        if (at < there) v = cluster.map_shared_rank(sh.list[0], q)[at], at = -1;
-        else at -= there;
-      }
-      sorted[i] = v;
-    }
-    __syncthreads();
-    for (int len = 2; len <= size; len *= 2)  // bitonic
-      for (int gap = len / 2; gap; gap /= 2) {
-        for (int t = tid; t < size / 2; t += kThreads) {
-          const int i = 2 * t - (t & (gap - 1)), j = i + gap;
-          const u64 x = sorted[i], y = sorted[j];
-          if ((x < y) == ((i & len) == 0)) sorted[i] = y, sorted[j] = x;
-        }
-        __syncthreads();
-      }
-    return all;
-  };
-  auto cut_at = [&](int at) { cut_key = (uint32_t)(sorted[at] >> 32), cut_index = ~(uint32_t)sorted[at]; };
-  // The cut in the sorted list's first `most` tokens at which the weights' sum, from `above` on,
-  // reaches need(its sum over them).
-  auto cut_by_weight = [&](int most, u64 above, auto need) {
-    u64 w[kList / kThreads], mine = 0;
-#pragma unroll
-    for (int q = 0; q < kList / kThreads; ++q) {
-      const int i = kList / kThreads * tid + q;
-      w[q] = i < most ? weight(s, logit_of((uint32_t)(sorted[i] >> 32))) : 0;
-      mine += w[q];
-    }
-    u64 before = scan(mine) - mine + above;
-    __syncthreads();
-    const u64 wanted = need(above + sh.sum);
-#pragma unroll
-    for (int q = 0; q < kList / kThreads; ++q) {
-      if (before < wanted && wanted <= before + w[q]) sh.bin = kList / kThreads * tid + q;
-      before += w[q];
-    }
-    __syncthreads();
-    cut_at(sh.bin);
-  };
-  // The first token in order at which the sum of amount(), over the cluster's blocks in order, passes
-  // `target`: true in the block that has it, whose thread calls found(index).
-  auto find = [&](auto amount, auto target, auto found) {
-    u64 mine = 0;
-    for (int i = r0; i < r1; ++i) mine += amount(i);
-    const u64 before = scan(mine) - mine;
+  // A block's sum, to the cluster's ranks (behind their next barrier).
+  auto publish = [&](u64 mine) {
+    scan(sh, mine);
     __syncthreads();
     if (tid < ranks) *cluster.map_shared_rank(&sh.rank_sum[rank], tid) = sh.sum;
-    cluster.sync();
-    u64 all = 0, lead = 0;
-    for (int q = 0; q < ranks; ++q) {
-      if (q == rank) lead = all;
-      all += sh.rank_sum[q];
+  };
+  auto sum_of_ranks = [&](int upto) {
+    u64 all = 0;
+    for (int q = 0; q < upto; ++q) all += sh.rank_sum[q];
+    return all;
+  };
+  // The sum of the weights of what stays; each of them to one(which, weight), an uint32_t or u64.
+  auto kept = [&](const float (&x)[kSide], int g, auto one) {
+    const Weights w(s, x);
+    u64 sum = 0;
+    const bool all = cut == -INFINITY;
+    if (!w.any) {
+#pragma unroll
+      for (int q = 0; q < kSide; ++q) {
+        const uint32_t v = all || stays(x[q], first + g * kGroup + q) ? w.w[q] : 0;
+        one(q, v), sum += v;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kSide; ++q) {
+        const u64 v = all || stays(x[q], first + g * kGroup + q) ? w.whole(s, x, q) : 0;
+        one(q, v), sum += v;
+      }
     }
-    const u64 at = target(all);
-    u64 sum = lead + before;
-    if (at < sum || at >= sum + mine) return;
-    for (int i = r0; i < r1; ++i) {
-      sum += amount(i);
-      if (at < sum) {
-        found(i, all);
+    return sum;
+  };
+  auto nothing = [](int, auto) {};
+  auto of_warp = [&](u64 v) {
+#pragma unroll
+    for (int q = 16; q; q >>= 1) v += __shfl_xor_sync(0xffffffffu, v, q);
+    return v;
+  };
+  // The first token in order at which the sum of amount(), over the cluster's blocks in order, passes
+  // target(sum of all): its lane calls found(token, logit, sum).  The block that has it narrows it down to a
+  // warp's run, then, all warps together, to a group, and one warp to the token.
+  auto find = [&](float border, auto amount, auto target, auto found) {
+    u64 sum = 0;
+    auto add = [&](const float (&x)[kSide], int g) { sum += amount(x, g, nothing); };
+    if (border == -INFINITY) each_group(add);
+    else each(border, add);
+    publish(sum);
+    u64 before = 0;  // of the block's warps
+    int run = 0;
+    cluster.sync();
+    const u64 lead = sum_of_ranks(rank), all = sum_of_ranks(ranks), at = target(all);
+    if (at < lead || at >= lead + sh.sum) return;
+    before = lead;
+    while (at >= before + sh.warp_sum[run]) before += sh.warp_sum[run++];
+    // the run's groups' sums, in the bins' place
+    u64 *const sums = &sh.list[0][0];
+    for (int i = tid; i < groups; i += kThreads) sums[i] = 0;
+    __syncthreads();
+    visit(One(), run, warp, kWarps, border, [&](const float (&x)[kSide], int g) {
+      const u64 side = of_warp(amount(x, g, nothing));
+      if (lane == 0) sums[g - (run - warp) * groups] = side;
+    });
+    __syncthreads();
+    if (warp) return;
+    auto upto_lane = [&](u64 v) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+      }
+      return v;
+    };
+    int g = 0;
+    for (;; g += 32) {
+      const u64 upto = upto_lane(g + lane < groups ? sums[g + lane] : 0);
+      const unsigned past = __ballot_sync(0xffffffffu, at < before + upto);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        if (l) before += __shfl_sync(0xffffffffu, upto, l - 1);
+        g += l + run * groups;
         break;
       }
+      before += __shfl_sync(0xffffffffu, upto, 31);
     }
-  };
-  // The cut by the logits' bits where a list is too long: among the tokens of the chosen bin that stay
-  // so far, the one at which their count or weight reaches `need`.
-  auto cut_by_bits = [&](int bin, bool weights, u64 need) {
-    uint32_t prefix = 0;
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-      choose(
-          [&] {
-            for (int i = tid; i < n; i += kThreads) {
-              const float x = slice[i];
-              const uint32_t key = key_of(x), rev = ~key;
-              if (bin_of(s, x) != bin || !stays(key, i) || (level && rev >> (shift + bits) != prefix)) continue;
-              const uint32_t digit = rev >> shift & ((1u << bits) - 1);
-              if (weights) add_to(&sh.bins[0][digit], &sh.bins[1][digit], weight(s, x));
-              else atomicAdd(&sh.bins[0][digit], 1u);
-            }
-          },
-          [&](u64) { return need; });
-      need -= sh.above;
-      prefix = prefix << bits | sh.bin;
-      __syncthreads();
+    float x[kSide];
+    u64 w[kSide];
+    decode(fetch(g), g, x);
+    const u64 own = amount(x, g, [&](int q, auto v) { w[q] = v; });
+    u64 from = before + upto_lane(own) - own;
+#pragma unroll
+    for (int q = 0; q < kSide; ++q) {
+      if (at >= from && at < from + w[q]) found(first + g * kGroup + q, x[q], all);
+      from += w[q];
     }
-    const uint32_t key = ~prefix;
-    if (weights) {
-      const u64 w = weight(s, logit_of(key));
-      need = (need + w - 1) / w;
-    }
-    find([&](int i) -> u64 { return key_of(slice[i]) == key && stays(key, i); }, [&](u64) { return need - 1; },
-         [&](int i, u64) {
-           for (int q = 0; q < ranks; ++q) *cluster.map_shared_rank(&sh.cut_index, q) = first + i;
-         });
-    cluster.sync();
-    cut_key = key, cut_index = sh.cut_index;
-  };
-  auto share = [&](u64 all) {
-    const double x = ceil((double)p * (double)all);
-    return x >= 1.0 ? min((u64)x, all) : u64(1);
   };
 
-  bool shared_out = !by_share;
-  if (by_count) {
-    choose(
-        [&] {
-          for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.bins[0][bin_of(s, slice[i])], 1u);
-        },
-        [&](u64) { return (u64)k; });
-    const int bin = (int)sh.bin, above = (int)sh.above;
-    const u64 upto = sh.above + sh.inside;
-    if (bin < kLastBin) {  // (else all that weighs something stays)
-      if (upto <= kList) {
-        list([&](float x, int) { return bin_of(s, x) <= bin; });
-        if (by_share) cut_by_weight(k, 0, share);
-        else cut_at(k - 1);
-        shared_out = true;
-      } else if (list([&](float x, int) { return bin_of(s, x) == bin; }) >= 0) {
-        cut_at(k - above - 1);
+  // Rows without limits and top-p read all tokens: the unit for them.  (By the groups, not the warps or
+  // blocks, so that a row's results do not depend on their number.)
+  if (!by_count && !by_floor) {
+    int near = 0;
+    for (int g = lane; g < groups; g += 32) near += depth(s, mine[g]) < 8.f;
+    publish(near);
+    cluster.sync();
+    if (sum_of_ranks(ranks) * kGroup * 4 > V) s.unit = 34, s.deep = 4.f;
+    cluster.sync();  // (read by all)
+  }
+
+  // Top-k, then top-p.  Top-k is tried first on the tokens above the k-th of the groups' maxima, and if that
+  // does not do, on all; top-p on all.
+  const int some = min(kQuick, (V + 2 * kGroup - 1) / (2 * kGroup));
+  bool share_left = by_share;
+  for (int phase = by_count ? 0 : 1; phase < 2; ++phase) {
+    const bool counts = phase == 0;
+    if (!counts && !share_left) break;
+    for (int tries = counts && k <= some ? 0 : 1; tries < 2; ++tries) {
+      clear();
+      const bool of_maxima = tries == 0;
+      if (of_maxima) {
+        for (int i = tid; i < kWarps * groups; i += kThreads) {
+          const int bin = bin_of(s, maxima[i]);
+          if (bin < kLastBin) atomicAdd(&sh.bins[0][bin], 1u);
+        }
+      } else if (counts) {
+        each_group([&](const float (&x)[kSide], int g) {
+#pragma unroll
+          for (int q = 0; q < kSide; ++q) {
+            const int bin = bin_of(s, x[q]);
+            if (bin < kLastBin) atomicAdd(&sh.bins[0][bin], 1u);
+          }
+        });
       } else {
-        cut_by_bits(bin, false, k - above);
+        each_group([&](const float (&x)[kSide], int g) {
+          kept(x, g, [&](int q, auto w) {
+            const int bin = bin_of(s, x[q]);
+            if (w) add_to(&sh.bins[0][bin], &sh.bins[1][bin], w);
+          });
+        });
       }
+      if (counts && tid == 0) sh.bins[0][kLastBin] = (uint32_t)V;  // (what is left, or more)
+      u64 wanted = choose(sh, totals, counts, {counts ? (u64)k : 0, p});
+      const int bin = (int)sh.bin;
+      u64 above = sh.above;
+      if (bin == kLastBin) continue;  // (at the second try: all that weighs something stays)
+      // the list: top-k's of all tokens up to the bin where it holds them (top-p's cut is then in it too)
+      const bool whole = of_maxima || (counts && above + sh.inside <= kList);
+      const float border = s.top - (float)(bin + 1) / kBinsPerHalving / s.hi * 1.0001f;  // (a little below the bin)
+      int sub = -1;  // the part of the bin, where the tokens of all of it are too many
+      auto part = [&](float x) {  // (as bin_of: falls with the logit)
+        const float t = __fmaf_rn(depth(s, x), kBinsPerHalving, 0.5f - (float)bin);
+        return min(max((int)(t * (float)kBins), 0), kBins - 1);
+      };
+      auto inside = [&](float x, int i) {
+        if (!(x >= border)) return false;
+        const int b = bin_of(s, x);
+        return (b == bin ? sub < 0 || part(x) == sub : whole && b < bin) && stays(x, i);
+      };
+      int listed;
+      for (;;) {
+        __syncthreads();
+        each(border, [&](const float (&x)[kSide], int g) {
+#pragma unroll
+          for (int q = 0; q < kSide; ++q) {
+            const int i = first + g * kGroup + q;
+            if (!inside(x[q], i)) continue;
+            const uint32_t at = atomicAdd(&sh.listed, 1u);
+            if (at < kList) sh.list[0][at] = (u64)key_of(x[q]) << 32 | ~(uint32_t)i;
+          }
+        });
+        listed = sort_lists(sh, rank);
+        if (listed >= 0 || sub >= 0 || whole) break;
+        wanted -= above;
+        clear();
+        each_at_leisure(border, [&](const float (&x)[kSide], int g) {
+#pragma unroll
+          for (int q = 0; q < kSide; ++q) {
+            if (!inside(x[q], first + g * kGroup + q)) continue;
+            const int b = part(x[q]);
+            if (counts) atomicAdd(&sh.bins[0][b], 1u);
+            else add_to(&sh.bins[0][b], &sh.bins[1][b], weight(s, x[q]));
+          }
+        });
+        choose(sh, totals, counts, {wanted, 0.f});
+        sub = (int)sh.bin, above = sh.above;
+      }
+      if (listed >= 0) {
+        int at = whole ? k - 1 : (int)(wanted - above) - 1;
+        if (!counts || (whole && by_share)) {
+          at = place_by_weight(sh, s, counts ? k : listed, counts ? 0 : above, {counts ? 0 : wanted, p});
+          share_left = false;
+        }
+        cut = logit_of((uint32_t)(sh.list[1][at] >> 32)), cut_index = (int)~(uint32_t)sh.list[1][at];
+        break;
+      }
+      if (whole) continue;  // (the first try's: more tokens above the maxima than a list holds)
+      // still too many (equal logits among them): by the logits' bits, then by the index
+      wanted -= above;
+      uint32_t prefix = 0;
+      for (int level = 0; level < 3; ++level) {
+        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+        clear();
+        each_at_leisure(border, [&](const float (&x)[kSide], int g) {
+#pragma unroll
+          for (int q = 0; q < kSide; ++q) {
+            if (!inside(x[q], first + g * kGroup + q)) continue;
+            const uint32_t rev = ~key_of(x[q]);
+            if (level && rev >> (shift + bits) != prefix) continue;
+            const uint32_t digit = rev >> shift & ((1u << bits) - 1);
+            if (counts) atomicAdd(&sh.bins[0][digit], 1u);
+            else add_to(&sh.bins[0][digit], &sh.bins[1][digit], weight(s, x[q]));
+          }
+        });
+        choose(sh, totals, counts, {wanted, 0.f});
+        wanted -= sh.above;
+        prefix = prefix << bits | sh.bin;
+        __syncthreads();
+      }
+      const float at = logit_of(~prefix);
+      if (!counts) {
+        const u64 w = weight(s, at);
+        wanted = (wanted + w - 1) / w;
+        share_left = false;
+      }
+      find(
+          at,
+          [&](const float (&x)[kSide], int g, auto one) {
+            u64 sum = 0;
+#pragma unroll
+            for (int q = 0; q < kSide; ++q) {
+              const uint32_t v = x[q] == at && stays(x[q], first + g * kGroup + q);
+              one(q, v), sum += v;
+            }
+            return sum;
+          },
+          [&](u64) { return wanted - 1; },
+          [&](int i, float, u64) {
+            for (int q = 0; q < ranks; ++q) *cluster.map_shared_rank(&sh.cut_index, q) = i;
+          });
+      cluster.sync();
+      cut = at, cut_index = (int)sh.cut_index;
+      break;
     }
   }
-  if (!shared_out) {
-    const u64 need = choose(
-        [&] {
-          for (int i = tid; i < n; i += kThreads) {
-            const float x = slice[i];
-            const int bin = bin_of(s, x);
-            if (bin < kLastBin && stays(key_of(x), i)) add_to(&sh.bins[0][bin], &sh.bins[1][bin], weight(s, x));
-          }
-        },
-        share);
-    const int bin = (int)sh.bin;
-    const u64 above = sh.above;
-    const int listed = list([&](float x, int i) { return bin_of(s, x) == bin && stays(key_of(x), i); });
-    if (listed >= 0) cut_by_weight(listed, above, [&](u64) { return need; });
-    else cut_by_bits(bin, true, need - above);
+  if (by_floor) {  // min-p: w < min_p is l < m + T ln(min_p)
+    if (tid == 0) sh.least = __double2float_ru((double)s.top + sh.floor_log);
+    __syncthreads();
+    if (sh.least > cut) cut = sh.least, cut_index = 0x7fffffff;
   }
 
   // ---- the token ----
-  float least = -INFINITY;  // min-p: w < min_p is l < m + T ln(min_p)
-  if (by_floor && T < INFINITY) least = __double2float_ru((double)s.top + (double)T * log((double)fminf(floor_p, 1.f)));
   find(
-      [&](int i) -> u64 {
-        const float x = slice[i];
-        return x >= least && stays(key_of(x), i) ? weight(s, x) : 0;
-      },
+      cut, kept,
       [&](u64 all) {
-        const double x = (double)u * (double)all;
-        return x > 0.0 ? min((u64)x, all - 1) : u64(0);
+        bool more;
+        return !(u > 0.f) ? u64(0) : u < 1.f ? part_of(u, all, more) : all - 1;
       },
-      [&](int i, u64 all) {
-        // ln w - ln(sum): of the sum the part past the largest weight where it is small
-        const float x = slice[i], one = 0x1p-44f;
-        const float l = x == s.top ? 0.f : -(float)(((double)s.top - (double)x) / (double)T);
-        const u64 rest = all - min(all, u64(1) << kUnit);
-        finish(first + i, l - log1pf((float)rest * one));
+      [&](int i, float x, u64 all) {
+        // ln w - ln(sum): the sum is the largest weight and what is beside it
+        const u64 rest = all - min(all, u64(1) << s.unit);
+        const float l = x == s.top ? 0.f : -__fdiv_rn(__fsub_rn(s.top, x), T);
+        finish(i, l - log1pf((float)rest * (s.unit == 44 ? 0x1p-44f : 0x1p-34f)));
       });
 }
 
 }  // namespace
 
 namespace {
-// The slice of a block, in floats (whole 16-byte blocks of logits, one more for a row that starts
-// inside one), and its shared memory.
-int per_rank_of(int64_t V, int ranks) { return (int)((V + 8 + ranks - 1) / ranks + 7) / 8 * 8; }
-size_t smem_of(int per_rank) { return size_t(per_rank) * 4; }
+// A warp's groups of a row (a row may start inside a group's first load), and a block's shared memory.
+int groups_of(int64_t V, int ranks) {
+  const int64_t run = int64_t(ranks) * kWarps * kGroup;
+  return (int)((V + kSide - 1 + run - 1) / run);
+}
+size_t smem_of(int groups, int ranks) { return (ranks > 1 ? 2 * kBins / ranks * 4 : 0) + size_t(kWarps) * groups * 4; }
 }  // namespace
 
 mq_status init_sample(DeviceState *st) {
@@ -501,11 +807,14 @@ mq_status init_sample(DeviceState *st) {
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return;
-    const int most = st->smem_optin - (int)fa.sharedSizeBytes;
+    const int most = (int)smem_of(groups_of((1 << 19) - 1, 1), 1);  // (the largest row in one block)
+    if (most + (int)fa.sharedSizeBytes > st->smem_optin) {
+      e = cudaErrorInvalidConfiguration;
+      return;
+    }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return;
-    st->sample_smem = most;
     for (int i = 0; i < 5; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(1 << i);
@@ -529,19 +838,15 @@ mq_status init_sample(DeviceState *st) {
 }
 
 mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *st) {
-  // Blocks of a cluster: so many that two blocks fit an SM (slices of 20 thousand logits), and where
-  // the rows are few, twice as many as long as all blocks have an SM and 2048 logits of their own.
+  // Blocks of a cluster: as many as are resident at once for all rows (two to an SM), with 2048 logits or more
+  // each.
   int r = 0;
-  while (r < 4 && per_rank_of(a.V, 1 << r) > 20 * 1024) ++r;
-  while (r < 4 && a.B << (r + 1) <= st->sms && a.V >> (r + 1) >= 2048) ++r;
-  while (r > 0 && st->sample_clusters[r] == 0) --r;
-  const int ranks = 1 << r, per_rank = per_rank_of(a.V, ranks);
-  if (st->sample_clusters[r] == 0 || smem_of(per_rank) > (size_t)st->sample_smem)
-    return fail(MQ_ERR_SHAPE, "mq_sample: V=%lld does not fit the shared memory of a cluster of %d blocks",
-                (long long)a.V, ranks);
+  while (r < 4 && a.B << (r + 1) <= 2 * st->sms && a.V >> (r + 1) >= 2048 && st->sample_clusters[r + 1]) ++r;
+  const int ranks = 1 << r, groups = groups_of(a.V, ranks);
   auto *kernel = a.io == MQ_F32 ? sample_kernel<MQ_F32> : a.io == MQ_F16 ? sample_kernel<MQ_F16> : sample_kernel<MQ_BF16>;
-  return launch_cluster("sample_kernel", kernel, dim3(ranks, (unsigned)a.B, 1), dim3(kThreads, 1, 1), smem_of(per_rank),
-                        s, ranks, a, per_rank);
+  return launch_cluster("sample_kernel", kernel, dim3(ranks, (unsigned)a.B, 1), dim3(kThreads, 1, 1),
+                        smem_of(groups, ranks),
+                        s, ranks, a, groups);
 }
 
 }  // namespace mq
