@@ -48,6 +48,8 @@ constexpr int kSide = 4;                              // tokens of a lane side b
 constexpr int kGroup = 32 * kSide;                    // of a warp: a group
 constexpr int kList = 1024;                           // tokens listed and sorted
 constexpr int kQuick = kList / 2;                     // groups' maxima that a list's tokens are found by
+constexpr int kCounted = kThreads / 2;                // listed tokens that are sorted by counting
+constexpr int kFew = 4;                               // groups that a warp goes through alone
 constexpr int kMaxRanks = 16;
 constexpr float kBinsPerHalving = 45.f;
 constexpr int kLastBin = kBins - 1;  // (2025 and up weigh nothing)
@@ -66,9 +68,9 @@ struct Shared {
   u64 rank_sum[kMaxRanks];
   u64 above, inside;  // of the bin that was chosen: what lies before it, and in it
   uint32_t bin, listed, cut_index;
-  float c_hi, c_lo, least;
+  float least;
   double floor_log;  // T ln(min_p)
-  u64 sum, wanted;
+  u64 sum;
 };
 
 // Order of the logits as unsigned numbers (-0 as 0), and back.
@@ -82,8 +84,8 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 
 struct Scale {
   float top, hi, lo;  // m (finite); log2(e) / T in two parts
-  // Weights are in units of 2^-unit: 44, or 34 in rows of which a quarter or more of the groups of 128 tokens
-  // reach 2^-8 of the largest (these rows' sums are far above that one).  A weight has less than 32
+  // Weights are in units of 2^-unit: 44, or 34 in rows of 2^14 tokens or more whose groups of 128 tokens have
+  // maxima of 2^-8 of the largest weight or more on average (their sums are far above that one).  A weight has less than 32
   // bits from y = unit - 30 (`deep`) on.
   int unit;
   float deep;
@@ -174,8 +176,7 @@ __device__ __forceinline__ void add_to(uint32_t *lo, uint32_t *hi, uint32_t w) {
 // What a block's threads do together.  (Functions of their own, called from several places: a row passes
 // through each code only once or twice, and what it costs to fetch counts.)
 
-// Sums over the threads up to this one; over all in sh.sum, for thread 0 at once and for the others
-// behind a barrier.
+// Sums over the threads up to this one; over all in sh.sum, behind a barrier.
 __device__ __noinline__ u64 scan(Shared &sh, u64 v) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   u64 upto = v;
@@ -187,14 +188,16 @@ __device__ __noinline__ u64 scan(Shared &sh, u64 v) {
   __syncthreads();  // (the sums before have been read)
   if (lane == 31) sh.warp_sum[warp] = upto;
   __syncthreads();
-  u64 all = 0, before = 0;
+  static_assert(kWarps == 16, "half a warp adds the warps' sums up");
+  const u64 own = lane < kWarps ? sh.warp_sum[lane] : 0;
+  u64 sums = own;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = all;
-    all += sh.warp_sum[w];
+  for (int i = 1; i < kWarps; i <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, sums, i);
+    if (lane >= i) sums += o;
   }
-  if (threadIdx.x == 0) sh.sum = all;
-  return before + upto;
+  if (threadIdx.x == kWarps - 1) sh.sum = sums;
+  return __shfl_sync(0xffffffffu, sums - own, warp) + upto;
 }
 
 // What a cut asks for: a number, or of the sum the share p (at least something).
@@ -237,9 +240,8 @@ __device__ __noinline__ u64 choose(Shared &sh, uint32_t *totals, bool counts, Ne
   const u64 v[kPer] = {(u64)hi.x << 32 | lo.x, (u64)hi.y << 32 | lo.y, (u64)hi.z << 32 | lo.z, (u64)hi.w << 32 | lo.w};
   const u64 mine = v[0] + v[1] + v[2] + v[3];
   u64 before = scan(sh, mine) - mine;
-  if (tid == 0) sh.wanted = need.of(sh.sum);
   __syncthreads();
-  const u64 wanted = sh.wanted;
+  const u64 wanted = need.of(sh.sum);
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     if (before < wanted && wanted <= before + v[q]) sh.bin = kPer * tid + q, sh.above = before, sh.inside = v[q];
@@ -248,6 +250,16 @@ __device__ __noinline__ u64 choose(Shared &sh, uint32_t *totals, bool counts, Ne
   __syncthreads();
   return wanted;
 }
+
+// A thread's share of something about each of n <= kCounted things: `parts` threads side by side to each.
+struct Share {
+  int parts, at, part;
+  __device__ __forceinline__ explicit Share(int n) {
+    parts = 2;
+    while (parts < 32 && parts * 2 * n <= kThreads) parts *= 2;
+    at = threadIdx.x / parts, part = threadIdx.x % parts;
+  }
+};
 
 // The lists of the cluster's blocks (sh.listed tokens in sh.list[0]), sorted in sh.list[1]: the largest key
 // first, equal ones by their index.  Their number, or -1 where they are too many.
@@ -262,21 +274,30 @@ __device__ __noinline__ int sort_lists(Shared &sh, int rank) {
   for (int q = 0; q < ranks; ++q) all += (int)min(sh.rank_n[q], (uint32_t)kList + 1);
   if (tid == 0) sh.listed = 0;
   if (all > kList) return -1;
-  int size = 32;  // a power of two
-  while (size < all) size *= 2;
-  for (int i = tid; i < size; i += kThreads) {
-    u64 v = 0;
-    int at = i;
+  auto listed = [&](int i) {  // the i-th of the lists one behind the other
     for (int q = 0; q < ranks; ++q) {
       const int there = (int)sh.rank_n[q];
-      if (at < there) {
-        v = cluster.map_shared_rank(sh.list[0], q)[at];
-        break;
-      }
-      at -= there;
+      if (i < there) return (u64)cluster.map_shared_rank(sh.list[0], q)[i];
+      i -= there;
     }
-    sorted[i] = v;
+    return u64(0);
+  };
+  if (all <= kCounted) {  // each token's place is the number of those before it
+    u64 *const unsorted = sorted + kCounted;
+    for (int i = tid; i < all; i += kThreads) unsorted[i] = listed(i);
+    __syncthreads();
+    const Share e(all);
+    const u64 own = e.at < all ? unsorted[e.at] : 0;
+    int place = 0;
+    for (int j = e.part; j < all; j += e.parts) place += unsorted[j] > own;
+    for (int d = 1; d < e.parts; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+    if (e.at < all && e.part == 0) sorted[place] = own;
+    __syncthreads();
+    return all;
   }
+  int size = 32;  // a power of two
+  while (size < all) size *= 2;
+  for (int i = tid; i < size; i += kThreads) sorted[i] = listed(i);
   __syncthreads();
   for (int len = 2; len <= size; len *= 2)  // bitonic
     for (int gap = len / 2; gap; gap /= 2) {
@@ -302,9 +323,8 @@ __device__ __noinline__ int place_by_weight(Shared &sh, const Scale &s, int most
     mine += w[q];
   }
   u64 before = scan(sh, mine) - mine + above;
-  if (threadIdx.x == 0) sh.wanted = need.of(above + sh.sum);
   __syncthreads();
-  const u64 wanted = sh.wanted;
+  const u64 wanted = need.of(above + sh.sum);
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     if (before < wanted && wanted <= before + w[q]) sh.bin = N * threadIdx.x + q;
@@ -417,10 +437,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   };
-  // All of the warp's groups in order: four loads on their way, without a look at the row's ends where they
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  using Four = std::integral_constant<int, 4>;
+  // All of the warp's groups in order: `side` loads on their way, without a look at the row's ends where they
   // are not near.
-  auto each_group = [&](auto what) {
-    constexpr int U = 4;
+  auto each_group = [&](auto side, auto what) {
+    constexpr int U = side.value;
     const int start = first - kSide * lane;  // the warp's first token
     for (int g0 = 0; g0 < groups; g0 += U) {
       const int at = start + g0 * kGroup;
@@ -445,15 +468,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   };
-  using One = std::integral_constant<int, 1>;
-  using Two = std::integral_constant<int, 2>;
   auto each = [&](float border, auto what) { visit(Two(), warp, 0, 1, border, what); };
   auto each_at_leisure = [&](float border, auto what) { visit(One(), warp, 0, 1, border, what); };
 
   float top = -INFINITY;
   for (int g = lane; g < groups; g += 32) mine[g] = -INFINITY;  // (groups behind the row)
   __syncwarp();
-  each_group([&](const float (&x)[kSide], int g) {
+  each_group(Four(), [&](const float (&x)[kSide], int g) {
     // (the maximum takes the number of a number and a NaN)
     const float t = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), -INFINITY);
     const float best = logit_of(__reduce_max_sync(0xffffffffu, key_of(t)));
@@ -464,26 +485,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the maximum ----
   uint32_t top_key = key_of(top);
   if (lane == 0) sh.warp_key[warp] = top_key;
-  if (tid == kThreads - 1 && !greedy) {  // one thread for all
-    // log2(e) / T: the quotient, and its remainder over T
+  // log2(e) / T: the quotient (finite, so that the largest logit's y is 0), and its remainder over T
+  float c = 0.f, c_lo = 0.f;
+  if (!greedy) {
     constexpr float e_hi = 1.44269502162933349609375f, e_lo = 1.92596299112661746887e-8f;
-    const float c = fminf(__fdiv_rn(e_hi, T), FLT_MAX);  // (finite, so that the largest logit's y is 0)
-    const float rest = __fdiv_rn(__fmaf_rn(-c, T, e_hi) + e_lo, T);
-    sh.c_hi = c, sh.c_lo = c > 0.f && c < FLT_MAX ? rest : 0.f;
-    // (of min-p the border is exact to 64 bits: in flat rows thousands of tokens lie near it)
-    if (by_floor) sh.floor_log = (double)T * log((double)fminf(floor_p, 1.f));
+    c = fminf(__fdiv_rn(e_hi, T), FLT_MAX);
+    if (c > 0.f && c < FLT_MAX) c_lo = __fdiv_rn(__fmaf_rn(-c, T, e_hi) + e_lo, T);
+  }
+  // (of min-p the border is exact to 64 bits: in flat rows thousands of tokens lie near it)
+  if (tid == kThreads - 1 && by_floor) sh.floor_log = (double)T * log((double)fminf(floor_p, 1.f));
+  // Rows without limits and top-p read all tokens again: for the unit of their weights, the mean of the groups'
+  // maxima in sixteenths of y, as a sum and a number.  (Of the groups, not the warps or blocks, so that
+  // a row's results do not depend on their number.)
+  const bool looks = !greedy && !by_count && !by_floor && V >= 1 << 14;
+  u64 look = 0;
+  if (looks) {
+    for (int g = lane; g < groups; g += 32)
+      if (mine[g] > -INFINITY) look += (u64)((int64_t)__float2int_rn(fminf(fmaxf(mine[g] * c * 16.f, -1e9f), 1e9f)) << 20) + 1;
+    scan(sh, look);
   }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top_key = max(top_key, sh.warp_key[w]);
   cluster.barrier_wait();
-  if (tid < ranks) *cluster.map_shared_rank(&sh.rank_key[rank], tid) = top_key;
+  if (tid < ranks) {
+    *cluster.map_shared_rank(&sh.rank_key[rank], tid) = top_key;
+    if (looks) *cluster.map_shared_rank(&sh.rank_sum[rank], tid) = sh.sum;
+  }
   cluster.sync();
   int winner = 0;  // the first rank with the row's maximum
   top_key = sh.rank_key[0];
   for (int q = 1; q < ranks; ++q)
     if (sh.rank_key[q] > top_key) top_key = sh.rank_key[q], winner = q;
-  Scale s = {logit_of(top_key), sh.c_hi, sh.c_lo, 44, 14.f};
+  Scale s = {logit_of(top_key), c, c_lo, 44, 14.f};
+  if (looks) {
+    look = 0;
+    for (int q = 0; q < ranks; ++q) look += sh.rank_sum[q];
+    const float mean = (float)((int64_t)look >> 20) / (float)(look & 0xfffff);
+    if (s.top * c * 16.f - mean < 8.f * 16.f) s.unit = 34, s.deep = 4.f;
+  }
   auto finish = [&](int token, float logprob) {
     a.token[row] = token;
     if (a.logprob) a.logprob[row] = logprob;
@@ -570,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto find = [&](float border, auto amount, auto target, auto found) {
     u64 sum = 0;
     auto add = [&](const float (&x)[kSide], int g) { sum += amount(x, g, nothing); };
-    if (border == -INFINITY) each_group(add);
+    if (border == -INFINITY) each_group(Four(), add);
     else each(border, add);
     publish(sum);
     u64 before = 0;  // of the block's warps
@@ -580,16 +620,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (at < lead || at >= lead + sh.sum) return;
     before = lead;
     while (at >= before + sh.warp_sum[run]) before += sh.warp_sum[run++];
-    // the run's groups' sums, in the bins' place
+    // the group: that warp alone through a few, or all warps add up a share of them each (in the bins' place)
     u64 *const sums = &sh.list[0][0];
-    for (int i = tid; i < groups; i += kThreads) sums[i] = 0;
-    __syncthreads();
-    visit(One(), run, warp, kWarps, border, [&](const float (&x)[kSide], int g) {
-      const u64 side = of_warp(amount(x, g, nothing));
-      if (lane == 0) sums[g - (run - warp) * groups] = side;
-    });
-    __syncthreads();
-    if (warp) return;
+    auto group_sum = [&](const float (&x)[kSide], int g) { return of_warp(amount(x, g, nothing)); };
+    if (groups <= kFew) {
+      if (warp != run) return;
+      for (int g = lane; g < groups; g += 32) sums[g] = 0;
+      __syncwarp();
+      each_at_leisure(border, [&](const float (&x)[kSide], int g) {
+        const u64 side = group_sum(x, g);
+        if (lane == 0) sums[g] = side;
+      });
+      __syncwarp();
+    } else {
+      for (int i = tid; i < groups; i += kThreads) sums[i] = 0;
+      __syncthreads();
+      visit(One(), run, warp, kWarps, border, [&](const float (&x)[kSide], int g) {
+        const u64 side = group_sum(x, g);
+        if (lane == 0) sums[g - (run - warp) * groups] = side;
+      });
+      __syncthreads();
+      if (warp) return;
+    }
     auto upto_lane = [&](u64 v) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -605,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (past) {
         const int l = __ffs(past) - 1;
         if (l) before += __shfl_sync(0xffffffffu, upto, l - 1);
-        g += l + run * groups;
+        g += l + (run - warp) * groups;
         break;
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
@@ -622,21 +674,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
   };
 
-  // Rows without limits and top-p read all tokens: the unit for them.  (By the groups, not the warps or
-  // blocks, so that a row's results do not depend on their number.)
-  if (!by_count && !by_floor) {
-    int near = 0;
-    for (int g = lane; g < groups; g += 32) near += depth(s, mine[g]) < 8.f;
-    publish(near);
-    cluster.sync();
-    if (sum_of_ranks(ranks) * kGroup * 4 > V) s.unit = 34, s.deep = 4.f;
-    cluster.sync();  // (read by all)
-  }
-
   // Top-k, then top-p.  Top-k is tried first on the tokens above the k-th of the groups' maxima, and if that
   // does not do, on all; top-p on all.
   const int some = min(kQuick, (V + 2 * kGroup - 1) / (2 * kGroup));
   bool share_left = by_share;
+  int held = 0;  // tokens that stay, where all of them are in the sorted list
   for (int phase = by_count ? 0 : 1; phase < 2; ++phase) {
     const bool counts = phase == 0;
     if (!counts && !share_left) break;
@@ -649,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (bin < kLastBin) atomicAdd(&sh.bins[0][bin], 1u);
         }
       } else if (counts) {
-        each_group([&](const float (&x)[kSide], int g) {
+        each_group(Two(), [&](const float (&x)[kSide], int g) {
 #pragma unroll
           for (int q = 0; q < kSide; ++q) {
             const int bin = bin_of(s, x[q]);
@@ -657,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           }
         });
       } else {
-        each_group([&](const float (&x)[kSide], int g) {
+        each_group(Two(), [&](const float (&x)[kSide], int g) {
           kept(x, g, [&](int q, auto w) {
             const int bin = bin_of(s, x[q]);
             if (w) add_to(&sh.bins[0][bin], &sh.bins[1][bin], w);
@@ -717,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           share_left = false;
         }
         cut = logit_of((uint32_t)(sh.list[1][at] >> 32)), cut_index = (int)~(uint32_t)sh.list[1][at];
+        held = whole && !share_left ? at + 1 : 0;
         break;
       }
       if (whole) continue;  // (the first try's: more tokens above the maxima than a list holds)
@@ -775,18 +818,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   // ---- the token ----
-  find(
-      cut, kept,
-      [&](u64 all) {
-        bool more;
-        return !(u > 0.f) ? u64(0) : u < 1.f ? part_of(u, all, more) : all - 1;
-      },
-      [&](int i, float x, u64 all) {
-        // ln w - ln(sum): the sum is the largest weight and what is beside it
-        const u64 rest = all - min(all, u64(1) << s.unit);
-        const float l = x == s.top ? 0.f : -__fdiv_rn(__fsub_rn(s.top, x), T);
-        finish(i, l - log1pf((float)rest * (s.unit == 44 ? 0x1p-44f : 0x1p-34f)));
-      });
+  auto target = [&](u64 all) {
+    bool more;
+    return !(u > 0.f) ? u64(0) : u < 1.f ? part_of(u, all, more) : all - 1;
+  };
+  auto drawn = [&](int i, float x, u64 all) {
+    // ln w - ln(sum): the sum is the largest weight and what is beside it
+    const u64 rest = all - min(all, u64(1) << s.unit);
+    const float l = x == s.top ? 0.f : -__fdiv_rn(__fsub_rn(s.top, x), T);
+    finish(i, l - log1pf((float)rest * (s.unit == 44 ? 0x1p-44f : 0x1p-34f)));
+  };
+  if (held && held <= kCounted) {
+    // every block has all that stays: each token's sum of the weights before it, by its index
+    cluster.barrier_arrive();  // (the lists have been read)
+    const u64 *const sorted = sh.list[1];
+    u64 *const w = sh.list[1] + kCounted;
+    for (int i = tid; i < held; i += kThreads) {
+      const float x = logit_of((uint32_t)(sorted[i] >> 32));
+      w[i] = x >= cut ? weight(s, x) : 0;  // (min-p)
+    }
+    __syncthreads();
+    const Share e(held);
+    const u64 own = e.at < held ? sorted[e.at] : 0;
+    u64 before = 0, all = 0;
+    for (int j = e.part; j < held; j += e.parts) {
+      all += w[j];
+      if (~(uint32_t)sorted[j] < ~(uint32_t)own) before += w[j];
+    }
+    for (int d = 1; d < e.parts; d <<= 1)
+      before += __shfl_xor_sync(0xffffffffu, before, d), all += __shfl_xor_sync(0xffffffffu, all, d);
+    const u64 at = target(all);
+    if (rank == 0 && e.part == 0 && e.at < held && at >= before && at < before + w[e.at])
+      drawn((int)~(uint32_t)own, logit_of((uint32_t)(own >> 32)), all);
+    cluster.barrier_wait();
+    return;
+  }
+  find(cut, kept, target, drawn);
 }
 
 }  // namespace
@@ -839,9 +906,12 @@ mq_status init_sample(DeviceState *st) {
 
 mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *st) {
   // Blocks of a cluster: as many as are resident at once for all rows (two to an SM), with 2048 logits or more
-  // each.
+  // each.  Twice as many where top-p without top-k, or min-p, can make some rows far longer than others,
+  // whose few blocks would be left alone at the end (64 rows of 151936 with settings of their own 71 us, 57
+  // by twice as many; 256 with min-p 85, 70; but 64 with top-k and top-p 22, 36).
+  const int per_sm = a.min_p || (a.top_p && !a.top_k) ? 4 : 2;
   int r = 0;
-  while (r < 4 && a.B << (r + 1) <= 2 * st->sms && a.V >> (r + 1) >= 2048 && st->sample_clusters[r + 1]) ++r;
+  while (r < 4 && a.B << (r + 1) <= per_sm * st->sms && a.V >> (r + 1) >= 2048 && st->sample_clusters[r + 1]) ++r;
   const int ranks = 1 << r, groups = groups_of(a.V, ranks);
   auto *kernel = a.io == MQ_F32 ? sample_kernel<MQ_F32> : a.io == MQ_F16 ? sample_kernel<MQ_F16> : sample_kernel<MQ_BF16>;
   return launch_cluster("sample_kernel", kernel, dim3(ranks, (unsigned)a.B, 1), dim3(kThreads, 1, 1),
