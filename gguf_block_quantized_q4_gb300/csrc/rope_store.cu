@@ -30,6 +30,7 @@ namespace mq {
 namespace {
 
 constexpr int kThreads = 256;  // at most
+constexpr int kNormBlocks = 5;  // of 256 threads per SM, of the kernels with norms
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z),
@@ -84,43 +85,51 @@ __device__ __forceinline__ uint32_t numbers4(float4 v, float d) {
                      __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040), 0x5410);
 }
 
-// A sum of squares as hi + lo: what a sum rounds off goes to lo (Knuth's two-sum), and what a square
-// does (by fma).
-struct Wide {
-  float hi, lo;
+// The norm's factor g = 1 / sqrt(mean(a^2) + eps), to the nearest binary32 number but for values very near the
+// middle of two: a stored row is rounded to few bits, so a last place of g would show in them.  In units
+// of a power of two q, 2^-7 of the head's largest element or so, an element is h + l, h a whole number of
+// at most 2^8 and |l| <= 1/2.  Then sum h^2 is exact (a whole number below 2^24), and sum (2 h + l) l is
+// 2^-8 of it and keeps 2^-31 of the whole in binary32.  (Sums of squares and what they round off as pairs
+// took half as many operations again.)  One step of Newton's from the approximate root, with its residual in
+// parts, does the rest.
+struct Unit {
+  float q, inv;  // and 1 / q
 };
-__device__ __forceinline__ Wide add_wide(Wide a, Wide b) {
-  const float s = __fadd_rn(a.hi, b.hi), v = __fsub_rn(s, a.hi);
-  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, v)), __fsub_rn(b.hi, v));
-  return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), e)};
+// top: the bits of the largest magnitude; least: the exponent that q has at least (elements that small beside
+// sqrt(eps) do not count).
+__device__ __forceinline__ Unit unit_of(uint32_t top, int least) {
+  const int e = min(max((int)(top >> 23) - 7, least), 247);
+  return {__uint_as_float((uint32_t)e << 23), __uint_as_float((uint32_t)(254 - e) << 23)};
 }
-__device__ __forceinline__ Wide squares(float4 x, float4 y) {
-  const float2 neg = make_float2(-1.f, -1.f);
+// The two sums of a thread's elements.
+__device__ __forceinline__ float2 squares(float4 x, float4 y, Unit u) {
+  const float2 inv = make_float2(u.inv, u.inv), up = make_float2(kQuantMagic, kQuantMagic);
+  const float2 down = make_float2(-kQuantMagic, -kQuantMagic), neg = make_float2(-1.f, -1.f);
   const float2 v[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)};
-  float2 hi, lo;
+  float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // (pairs side by side)
-    const float2 p = __fmul2_rn(v[i], v[i]), e = __ffma2_rn(v[i], v[i], __fmul2_rn(p, neg));
-    if (i == 0) {
-      hi = p, lo = e;
-      continue;
-    }
-    const float2 s = __fadd2_rn(hi, p), w = __ffma2_rn(hi, neg, s);
-    const float2 a = __fadd2_rn(hi, __ffma2_rn(s, neg, w)), b = __ffma2_rn(w, neg, p);
-    lo = __fadd2_rn(lo, __fadd2_rn(e, __fadd2_rn(a, b))), hi = s;
+    const float2 t = __fmul2_rn(v[i], inv), h = __fadd2_rn(__fadd2_rn(t, up), down), l = __ffma2_rn(h, neg, t);
+    a = __ffma2_rn(h, h, a);
+    b = __ffma2_rn(__fadd2_rn(__fadd2_rn(h, h), l), l, b);
   }
-  return add_wide({hi.x, lo.x}, {hi.y, lo.y});
+  return make_float2(__fadd_rn(a.x, a.y), __fadd_rn(b.x, b.y));
 }
-// 1 / sqrt(S / dim + eps): the approximate root y, and one step of Newton's with its residual dim - y^2
-// (S + dim eps) in two parts, so that the result is the rounded one but for values very near a tie.
-__device__ __forceinline__ float inverse_rms(Wide s, float dim, float eps) {
-  const float p = __fmul_rn(dim, eps);
-  const Wide m = add_wide(s, {p, __fmaf_rn(dim, eps, -p)});
-  const float y = rsqrtf(__fdividef(m.hi, dim));
+// 1 / (q sqrt(S / dim + eps / q^2)), S = s.x + s.y.
+__device__ __forceinline__ float inverse_rms(float2 s, uint32_t top, Unit u, float dim, float eps) {
+  const float w = eps * u.inv * u.inv, p = __fmul_rn(dim, w), p_lo = __fmaf_rn(dim, w, -p);
+  // M = S + dim eps / q^2 as hi + lo (Knuth's two-sum of s.x and p; s.y is small beside the first)
+  const float c = __fadd_rn(s.x, p), v = __fsub_rn(c, s.x);
+  const float c_lo = __fadd_rn(__fsub_rn(s.x, __fsub_rn(c, v)), __fsub_rn(p, v));
+  const float hi = __fadd_rn(c, s.y), z = __fsub_rn(hi, c);
+  const float lo = __fadd_rn(__fadd_rn(__fadd_rn(__fsub_rn(c, __fsub_rn(hi, z)), __fsub_rn(s.y, z)), c_lo), p_lo);
+  const float y = rsqrtf(__fdividef(hi, dim));
+  // the residual dim - y^2 M
   const float a = __fmul_rn(y, y), b = __fmaf_rn(y, y, -a);
-  const float c = __fmul_rn(a, m.hi), d = __fmaf_rn(a, m.hi, -c);
-  const float e = __fsub_rn(__fsub_rn(__fsub_rn(dim, c), d), __fmaf_rn(a, m.lo, __fmul_rn(b, m.hi)));
-  return __fmaf_rn(y, __fmul_rn(e, __fdividef(0.5f, dim)), y);
+  const float d = __fmul_rn(a, hi), d_lo = __fmaf_rn(a, hi, -d);
+  const float e = __fsub_rn(__fsub_rn(__fsub_rn(dim, d), d_lo), __fmaf_rn(a, lo, __fmul_rn(b, hi)));
+  const float r = __fmaf_rn(y, __fmul_rn(e, __fdividef(0.5f, dim)), y);
+  return top < 0x7f800000u ? r * u.inv : top == 0x7f800000u ? 0.f : __uint_as_float(0x7fffffffu);
 }
 
 // How a cache's rows are stored.
@@ -129,14 +138,18 @@ enum Store : int { kStore16, kStoreQ8, kStoreQ4 };
 // per_pass: heads that the block's threads take at once; passes: the rounds of a token, of which NP
 // are loaded at a time; gridDim.y blocks share them.  A token's first loads need nothing but its
 // number, its positions and slot were read with the token before, so one latency covers a token.
-template <int STORE, bool NORM, int NP, int IO>
-__global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_constant__ RopeArgs a,
-                                                              int per_pass, int passes) {
+// D: the heads' size, with their norms; 0: no norms, any size.
+template <int STORE, int D, int NP, int IO>
+__global__ void __launch_bounds__(kThreads, D ? kNormBlocks : 4)
+rope_store_kernel(const __grid_constant__ RopeArgs a, int per_pass, int passes) {
+  constexpr bool NORM = D > 0;
   constexpr bool Q8 = STORE == kStoreQ8, Q4 = STORE == kStoreQ4, QUANT = Q8 || Q4;
   __shared__ uint32_t amax[QUANT ? NP : 1][kThreads];  // [round][head of the round][32-element block]
   __shared__ uint32_t numbers[Q4 ? NP : 1][Q4 ? 2 * kThreads : 1];  // [round][head of the round][dim], a byte each
-  __shared__ Wide quads[NORM ? NP : 1][NORM ? kThreads / 4 : 1];  // sums of four threads, where a head's are no power of two
-  const int dim = a.c.dim, units = dim / 8, hkv = a.c.hkv, heads = a.hq + 2 * hkv, nb = dim / 32;
+  // what four threads have, where a head's threads are no power of two
+  __shared__ uint32_t quad_top[NORM ? NP : 1][NORM ? kThreads / 4 : 1];
+  __shared__ float2 quad_sum[NORM ? NP : 1][NORM ? kThreads / 4 : 1];
+  const int dim = NORM ? D : a.c.dim, units = dim / 8, hkv = a.c.hkv, heads = a.hq + 2 * hkv, nb = dim / 32;
   const int u = threadIdx.x % units, sub = threadIdx.x / units;
   const int half = a.rope.rot_dim / 2;
   const bool turns = 4 * u < half;
@@ -226,8 +239,6 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
       if (pass0 != blockIdx.y * NP) load(row, pass0);
       if constexpr (NORM) {
         // bias, then the norm of the rounds' query and key heads
-        Wide sum[NP];
-        bool far = false;  // a sum past binary32
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
           const int head = head_of(pass0 + k);
@@ -236,56 +247,64 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
             y[k] = add4(y[k], *reinterpret_cast<const float4 *>(a.bias + head * dim + d0 + gap));
           }
         }
-        auto meet = [&](Wide (&sum)[NP]) {  // sums over a head's threads, for all of them
-          const bool whole = (units & (units - 1)) == 0;
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-            for (int i = 1; i < (whole ? units : 4); i <<= 1)
-              sum[k] = add_wide(sum[k], {__shfl_xor_sync(0xffffffffu, sum[k].hi, i),
-                                         __shfl_xor_sync(0xffffffffu, sum[k].lo, i)});
-          if (whole) return;
-          __syncthreads();  // (the sums before have been read)
-          if (threadIdx.x % 4 == 0) {
-#pragma unroll
-            for (int k = 0; k < NP; ++k) quads[NORM ? k : 0][threadIdx.x / 4] = sum[k];
-          }
-          __syncthreads();
-          const int first = min(sub, per_pass - 1) * (units / 4);
+        auto apply = [&](int k, uint32_t top, Unit unit, float2 sum) {
+          const int head = head_of(pass0 + k);
+          if (head >= a.hq + hkv) return;
+          const float by = inverse_rms(sum, top, unit, (float)dim, a.eps);
+          const float *const w = (head < a.hq ? a.norm_q : a.norm_k) + d0;
+          x[k] = normed4(x[k], by, *reinterpret_cast<const float4 *>(w));
+          y[k] = normed4(y[k], by, *reinterpret_cast<const float4 *>(w + gap));
+        };
+        const int least = ((int)(__float_as_uint(a.eps) >> 23) - 127) / 2 + 127 - 30;
+        constexpr int W = D / 8;  // threads of a head
+        if constexpr ((W & (W - 1)) == 0) {
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
-            sum[k] = quads[NORM ? k : 0][first];
-            for (int i = 1; i < units / 4; ++i) sum[k] = add_wide(sum[k], quads[NORM ? k : 0][first + i]);
+            uint32_t top = max(top4(x[k]), top4(y[k]));
+#pragma unroll
+            for (int i = 1; i < W; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+            const Unit unit = unit_of(top, least);
+            float2 sum = squares(x[k], y[k], unit);
+#pragma unroll
+            for (int i = 1; i < W; i <<= 1) {
+              sum.x += __shfl_xor_sync(0xffffffffu, sum.x, i);
+              sum.y += __shfl_xor_sync(0xffffffffu, sum.y, i);
+            }
+            apply(k, top, unit, sum);
           }
-        };
+        } else {  // heads of 96 and 192: their threads' fours meet in shared memory
+          const int first = min(sub, per_pass - 1) * (W / 4);
+          uint32_t top[NP];
 #pragma unroll
-        for (int k = 0; k < NP; ++k) sum[k] = squares(x[k], y[k]);
-        meet(sum);
-        float by[NP];
+          for (int k = 0; k < NP; ++k) {
+            top[k] = max(top4(x[k]), top4(y[k]));
+            for (int i = 1; i < 4; i <<= 1) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], i));
+            if (threadIdx.x % 4 == 0) quad_top[NORM ? k : 0][threadIdx.x / 4] = top[k];
+          }
+          __syncthreads();
+          Unit unit[NP];
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          by[k] = inverse_rms(sum[k], (float)dim, a.eps);
-          far |= !(sum[k].hi < 0x1p100f);
-        }
-        if (__syncthreads_or(far)) {  // once more in units of 2^70 (of 2^140 the squares)
-          constexpr float less = 0x1p-70f;
-          Wide small[NP];
+          for (int k = 0; k < NP; ++k) {
+            for (int i = 0; i < W / 4; ++i) top[k] = max(top[k], quad_top[NORM ? k : 0][first + i]);
+            unit[k] = unit_of(top[k], least);
+            float2 sum = squares(x[k], y[k], unit[k]);
 #pragma unroll
-          for (int k = 0; k < NP; ++k)
-            small[k] = squares(make_float4(x[k].x * less, x[k].y * less, x[k].z * less, x[k].w * less),
-                               make_float4(y[k].x * less, y[k].y * less, y[k].z * less, y[k].w * less));
-          meet(small);
+            for (int i = 1; i < 4; i <<= 1) {
+              sum.x += __shfl_xor_sync(0xffffffffu, sum.x, i);
+              sum.y += __shfl_xor_sync(0xffffffffu, sum.y, i);
+            }
+            if (threadIdx.x % 4 == 0) quad_sum[NORM ? k : 0][threadIdx.x / 4] = sum;
+          }
+          __syncthreads();
 #pragma unroll
-          for (int k = 0; k < NP; ++k)
-            if (!(sum[k].hi < 0x1p100f))
-              by[k] = small[k].hi < INFINITY ? inverse_rms(small[k], (float)dim, 0.f) * less : 1.f / small[k].hi;
-        }
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const int head = head_of(pass0 + k);
-          if (head >= a.hq + hkv) continue;
-          const float *const w = (head < a.hq ? a.norm_q : a.norm_k) + d0;
-          x[k] = normed4(x[k], by[k], *reinterpret_cast<const float4 *>(w));
-          y[k] = normed4(y[k], by[k], *reinterpret_cast<const float4 *>(w + gap));
+          for (int k = 0; k < NP; ++k) {
+            float2 sum = make_float2(0.f, 0.f);
+            for (int i = 0; i < W / 4; ++i) {
+              const float2 v = quad_sum[NORM ? k : 0][first + i];
+              sum.x += v.x, sum.y += v.y;
+            }
+            apply(k, top[k], unit[k], sum);
+          }
         }
       }
       const bool quantises = QUANT && (pass0 + NP) * per_pass > a.hq;  // (the same for the whole block)
@@ -385,26 +404,27 @@ __global__ void __launch_bounds__(kThreads, 4) rope_store_kernel(const __grid_co
 
 // (IO is a template argument so that the loads of a group stand together, without a branch on the
 // type at each)
-template <int STORE, bool NORM, int NP>
+template <int STORE, int D, int NP>
 mq_status launch_io(const RopeArgs &a, dim3 grid, dim3 block, int per_pass, int passes, cudaStream_t s) {
-  auto *kernel = a.io == MQ_F32   ? rope_store_kernel<STORE, NORM, NP, MQ_F32>
-                 : a.io == MQ_F16 ? rope_store_kernel<STORE, NORM, NP, MQ_F16>
-                                  : rope_store_kernel<STORE, NORM, NP, MQ_BF16>;
+  auto *kernel = a.io == MQ_F32   ? rope_store_kernel<STORE, D, NP, MQ_F32>
+                 : a.io == MQ_F16 ? rope_store_kernel<STORE, D, NP, MQ_F16>
+                                  : rope_store_kernel<STORE, D, NP, MQ_BF16>;
   return launch_dependent("rope_store_kernel", kernel, grid, block, 0, s, a, per_pass, passes);
 }
-template <int STORE, bool NORM>
-mq_status launch_rounds(const RopeArgs &a, int np, dim3 grid, dim3 block, int per_pass, int passes,
-                        cudaStream_t s) {
-  switch (np) {
-    case 1: return launch_io<STORE, NORM, 1>(a, grid, block, per_pass, passes, s);
-    case 2: return launch_io<STORE, NORM, 2>(a, grid, block, per_pass, passes, s);
-    default: return launch_io<STORE, NORM, 3>(a, grid, block, per_pass, passes, s);
-  }
-}
 template <int STORE>
-mq_status launch_norm(const RopeArgs &a, int np, dim3 grid, dim3 block, int per_pass, int passes, cudaStream_t s) {
-  return a.norm_q ? launch_rounds<STORE, true>(a, np, grid, block, per_pass, passes, s)
-                  : launch_rounds<STORE, false>(a, np, grid, block, per_pass, passes, s);
+mq_status launch_store(const RopeArgs &a, int np, dim3 grid, dim3 block, int per_pass, int passes, cudaStream_t s) {
+  if (a.norm_q) switch (a.c.dim) {
+      case 64: return launch_io<STORE, 64, 1>(a, grid, block, per_pass, passes, s);
+      case 96: return launch_io<STORE, 96, 1>(a, grid, block, per_pass, passes, s);
+      case 128: return launch_io<STORE, 128, 1>(a, grid, block, per_pass, passes, s);
+      case 192: return launch_io<STORE, 192, 1>(a, grid, block, per_pass, passes, s);
+      default: return launch_io<STORE, 256, 1>(a, grid, block, per_pass, passes, s);
+    }
+  switch (np) {
+    case 1: return launch_io<STORE, 0, 1>(a, grid, block, per_pass, passes, s);
+    case 2: return launch_io<STORE, 0, 2>(a, grid, block, per_pass, passes, s);
+    default: return launch_io<STORE, 0, 3>(a, grid, block, per_pass, passes, s);
+  }
 }
 
 }  // namespace
@@ -417,13 +437,15 @@ mq_status launch_rope_store(const RopeArgs &a, cudaStream_t s, const DeviceState
   // fewer tokens than fill the SMs: the rounds go to blocks of their own
   const bool split = a.T * passes <= 8 * st->sms;
   const int np = split ? 1 : std::min(passes, 3);
-  // blocks of up to 256 threads with 64 registers: as many as are resident at once
-  const int64_t resident = int64_t(st->sms) * std::max(1, std::min(2048 / (int)threads, 65536 / (64 * (int)threads)));
+  // blocks of up to 256 threads with 64 registers (48 with norms): as many as are resident at once
+  const int registers = a.norm_q ? 65536 / (kThreads * kNormBlocks) / 8 * 8 : 64;
+  const int64_t resident =
+      int64_t(st->sms) * std::max(1, std::min(2048 / (int)threads, 65536 / (registers * (int)threads)));
   const dim3 grid((unsigned)std::min(a.T, resident), split ? passes : 1, 1), block(threads, 1, 1);
   switch (a.c.type) {
-    case MQ_Q8_0: return launch_norm<kStoreQ8>(a, np, grid, block, per_pass, passes, s);
-    case MQ_Q4_0: return launch_norm<kStoreQ4>(a, np, grid, block, per_pass, passes, s);
-    default: return launch_norm<kStore16>(a, np, grid, block, per_pass, passes, s);
+    case MQ_Q8_0: return launch_store<kStoreQ8>(a, np, grid, block, per_pass, passes, s);
+    case MQ_Q4_0: return launch_store<kStoreQ4>(a, np, grid, block, per_pass, passes, s);
+    default: return launch_store<kStore16>(a, np, grid, block, per_pass, passes, s);
   }
 }
 
