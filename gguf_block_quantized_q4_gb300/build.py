@@ -19,10 +19,11 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmq.so")
 SOURCES = ["mq_api.cu", "repack.cu", "matvec.cu", "matvec_kq.cu", "xplane.cu", "quantize.cu",
-           "mmq.cu", "host_io.cu", "kv_api.cu", "rope_store.cu", "attn_decode.cu", "kv_evict.cu",
-           "sample.cu"]
+           "mmq.cu", "host_io.cu", "kv_api.cu", "rope_store.cu", "attn_decode.cu",
+           "attn_decode_q4.cu", "kv_evict.cu", "sample.cu"]
 HEADERS = [os.path.join(CSRC, "mq_common.cuh"), os.path.join(CSRC, "quant_row.cuh"),
            os.path.join(CSRC, "mv_device.cuh"), os.path.join(CSRC, "kv.cuh"),
+           os.path.join(CSRC, "attn_decode.cuh"),
            os.path.join(CSRC, "sample.cuh"),
            os.path.join(ROOT, "include", "mq.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -43,11 +43,13 @@ def attn_bound4(p, q, ref, mass, reach, scale, window, io):
     loses at most 2^-22 of 8 sum |q| |d| (the tensor cores may truncate), and the query's parts
     2^-22 of it; the blocks' sums, scaled in binary32, lose 2^-23 of sum |q| |k| each.  Twice that in
     the weights' quotient; the weights' parts, exp, and the sums over tiles, warps and pieces 2^-17
-    as for other rows; then the rounding to the output's type.  And what f16 parts cannot hold of
-    small weights: a weight p (at most 2^15) and its product with a scale d below 1 (in units of
-    `unit`, a power of two up to twice the largest scale) end in three roundings to steps of 2^-24,
-    half a step each, so an element of a key with a number of at most 8 loses 8 * 3 * 2^-25 of
-    2^15, which matters where the heavy keys' numbers are 0."""
+    as for other rows; then the rounding to the output's type.  For bf16 activations the weights are one
+    f16 part, rounded by 2^-12 of themselves, and their products with the scales once more: 2^-11 of
+    mass.  And what f16 parts cannot hold of small weights: a weight p (2^7 for one that is the
+    reference's, up to 2^15) and its product with a scale d below 1 (in units of `unit`, a power of two
+    up to twice the largest scale) end in three roundings to steps of 2^-24, half a step each, so an
+    element of a key with a number of at most 8 loses 8 * 3 * 2^-25 of 2^7 (the sum of the weights is
+    at least that), which matters where the heavy keys' numbers are 0."""
     S, hq, dim = q.shape
     hkv = p.host["k"].shape[1]
     wide = np.zeros((S, hq))
@@ -63,5 +65,6 @@ def attn_bound4(p, q, ref, mass, reach, scale, window, io):
             wide[s, a] = abs(scale) * 8 * (d @ sums).max()
     rel = 2 * (wide * 5 * 2.0 ** -22 + reach * (dim / 32 + 2) * 2.0 ** -23) + 2.0 ** -17
     unit = max(1.0, 2 * float(np.nanmax(np.abs(p.host["v_scale"].astype(np.float64)))))
-    floor = np.array([24 * n * 2.0 ** -40 * unit for n in p.lens_list])[:, None, None]
-    return floor + np.expm1(rel)[..., None] * mass + half_ulp(io) * 1.01 * np.abs(ref) + tiny(io), rel
+    floor = np.array([24 * n * 2.0 ** -32 * unit for n in p.lens_list])[:, None, None]
+    parts = 2.0 ** -11 if io == "bf16" else 0.0
+    return floor + (np.expm1(rel)[..., None] + parts) * mass + half_ulp(io) * 1.01 * np.abs(ref) + tiny(io), rel
