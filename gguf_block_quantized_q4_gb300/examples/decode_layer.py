@@ -18,15 +18,17 @@ class DecodeLayer:
     """Attention of `n_seqs` sequences that grow by a token per step.  wqkv: Weight of
     (n_heads + 2 n_kv_heads) head_dim rows, wo: Weight of n_heads head_dim columns.  A sequence
     that reaches `limit` cached tokens is brought down to `keep` of them (the first `sink`, the
-    last `recent`, and those that have gathered the most attention)."""
+    last `recent`, and those that have gathered the most attention).  norm: a HeadNorm, for models that
+    norm their query and key heads."""
 
     def __init__(self, wqkv, wo, n_seqs, n_heads, n_kv_heads, head_dim, limit, keep, sink=4,
-                 recent=16, kind=mq.Q8_0, page_size=16, bias=None, max_pos=32768, freq_base=1e6):
+                 recent=16, kind=mq.Q8_0, page_size=16, bias=None, max_pos=32768, freq_base=1e6,
+                 norm=None):
         if not 0 < keep < limit:
             raise ValueError(f"keep={keep} must leave room below limit={limit}")
         if sink < 0 or recent < 0 or sink + recent > keep:
             raise ValueError(f"sink={sink} and recent={recent} are more than keep={keep}")
-        self.wqkv, self.wo, self.n_heads, self.bias = wqkv, wo, n_heads, bias
+        self.wqkv, self.wo, self.n_heads, self.bias, self.norm = wqkv, wo, n_heads, bias, norm
         self.limit, self.keep, self.sink, self.recent = limit, keep, sink, recent
         self.width = -(-limit // page_size)
         spare = -(-keep // page_size)  # pages that one eviction needs at a time
@@ -78,7 +80,8 @@ class DecodeLayer:
     def attend(self, x):
         """The layer's device calls on x [n_seqs][K]: only launches, fit for a CUDA graph."""
         qkv = mq.matvec(self.wqkv, x)
-        q = mq.rope_store(self.cache, self.rope, qkv, self.pos, self.slot, self.n_heads, bias=self.bias)
+        q = mq.rope_store(self.cache, self.rope, qkv, self.pos, self.slot, self.n_heads, bias=self.bias,
+                          norm=self.norm)
         o = mq.attn_decode(self.cache, q, self.pages, self.lens, self.limit, track=True, ws=self.ws)
         return mq.matvec(self.wo, o.flatten(1))
 
