@@ -150,6 +150,9 @@ mq_status rope_store(const char *site, const mq_kv_cache *cache, const mq_rope *
   if (T && !(T == 1 && q == qkv) &&
       overlap(q, T * n_heads * cache->head_dim * esize, qkv, uint64_t((T - 1) * ld + width) * esize))
     return fail(MQ_ERR_ARG, "%s: q=%p overlaps qkv=%p (only one token's may, from the row's start)", site, q, qkv);
+  const uint64_t q_bytes = uint64_t(T) * n_heads * cache->head_dim * esize, norm_bytes = 4 * uint64_t(cache->head_dim);
+  if (norm && (overlap(q, q_bytes, norm->q, norm_bytes) || overlap(q, q_bytes, norm->k, norm_bytes)))
+    return fail(MQ_ERR_ARG, "%s: q=%p overlaps the norms' weights", site, q);
   DeviceState *st = nullptr;
   if ((s = current_state(&st, site)) != MQ_OK) return s;
   if (T == 0) return MQ_OK;

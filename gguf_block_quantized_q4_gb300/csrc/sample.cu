@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (greedy) {  // the first token with the maximum: of its rank the first warp's
     if (rank != winner) return;
     int w = 0;
-    while (sh.warp_key[w] != top_key) ++w;
+    while (w < kWarps - 1 && sh.warp_key[w] != top_key) ++w;
     if (w != warp) return;
     uint32_t index = 0xffffffffu;
     each_at_leisure(s.top, [&](const float (&x)[kSide], int g) {
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const u64 lead = sum_of_ranks(rank), all = sum_of_ranks(ranks), at = target(all);
     if (at < lead || at >= lead + sh.sum) return;
     before = lead;
-    while (at >= before + sh.warp_sum[run]) before += sh.warp_sum[run++];
+    while (run < kWarps - 1 && at >= before + sh.warp_sum[run]) before += sh.warp_sum[run++];
     // the group: that warp alone through a few, or all warps add up a share of them each (in the bins' place)
     u64 *const sums = &sh.list[0][0];
     auto group_sum = [&](const float (&x)[kSide], int g) { return of_warp(amount(x, g, nothing)); };
@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
     int g = 0;
     for (;; g += 32) {
+      if (g >= groups) return;  // (only where the logits were written to meanwhile)
       const u64 upto = upto_lane(g + lane < groups ? sums[g + lane] : 0);
       const unsigned past = __ballot_sync(0xffffffffu, at < before + upto);
       if (past) {
@@ -758,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           at = place_by_weight(sh, s, counts ? k : listed, counts ? 0 : above, {counts ? 0 : wanted, p});
           share_left = false;
         }
+        at = min(max(at, 0), kList - 1);  // (in the list, whatever was written to the logits meanwhile)
         cut = logit_of((uint32_t)(sh.list[1][at] >> 32)), cut_index = (int)~(uint32_t)sh.list[1][at];
         held = whole && !share_left ? at + 1 : 0;
         break;

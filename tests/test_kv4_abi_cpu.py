@@ -40,6 +40,16 @@ def test_norm_arguments(L):
         assert got[0] == status and got[1].startswith("mq_norm_rope_store: "), got
 
 
+def test_queries_over_the_norms_weights_are_refused(L):
+    """(other blocks still read them)"""
+    c, r = cache(), rope()
+    for q, k in ((4096 + 28 * 128 * 4 - 4, 1 << 20), (1 << 20, 4096 - 508)):
+        norm = mq._HeadNormStruct(q, k, 1e-6)
+        st = L.mq_norm_rope_store(ctypes.byref(c), ctypes.byref(r), ctypes.byref(norm), 0, ctypes.c_void_p(1 << 30), 36 * 128, None, None,
+                                  None, ctypes.c_void_p(4096), 1, 28, None)
+        assert mq.STATUS[st] == "MQ_ERR_ARG" and "overlaps the norms" in L.mq_last_error().decode()
+
+
 def test_norm_structure_matches_the_header():
     names = [f for f, _ in mq._HeadNormStruct._fields_]
     src = '#include <stdio.h>\n#include <stddef.h>\n#include "mq.h"\nint main(void) {\n'
