@@ -85,9 +85,9 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 
 struct Scale {
   float top, hi, lo;  // m (finite); log2(e) / T in two parts
-  // Weights are in units of 2^-unit: 44, or 34 in rows of 2^14 tokens or more whose groups of 128 tokens have
-  // maxima of 2^-8 of the largest weight or more on average (their sums are far above that one).  A weight has less than 32
-  // bits from y = unit - 30 (`deep`) on.
+  // Weights are in units of 2^-unit: 44, or, in rows of 2^14 tokens or more whose groups of 128 have maxima of
+  // 2^-16 or 2^-8 of the largest weight or more on average, 38 or 34 (their sums are far above that
+  // one).  A weight has less than 32 bits from y = unit - 29 (`deep`) on.
   int unit;
   float deep;
 };
@@ -131,17 +131,19 @@ struct Weights {
       float r;
       asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
       // r in [0.70, 1.42] as a whole number of 2^-22, in the low bits of its sum with 2^23; to the left by 8 and
-      // to the right by n - (unit - 30).  (Past 31 the shift leaves zero: all of y from 45 on,
-      // infinities and NaN, whose m are larger or no numbers.)
+      // to the right by n - (unit - 30), rounded (cut off, 150 thousand tokens would lose half a unit each).
+      // (Past 32 the shift leaves zero: all of y from unit + 1 on, infinities and NaN, whose m are larger
+      // or no numbers.)
       v[q] = __float_as_uint(__fmaf_rn(r, 0x1p22f, 0x1p23f)) << 8;
       by[q] = __float_as_uint(m) - (kMagicBits + (uint32_t)(s.unit - 30));
-      w[q] = __funnelshift_rc(v[q], 0u, by[q]);
+      w[q] = (__funnelshift_rc(v[q], 0u, by[q] - 1) + 1) >> 1;
       any |= y < s.deep;
     }
   }
   __device__ __forceinline__ u64 whole(const Scale &s, const float (&x)[kSide], int q) const {
     const float y = depth(s, x[q]);
-    return y < fminf(s.deep, 8.f) ? precise(s.top, s.hi, s.lo, x[q], s.unit) : y < s.deep ? (u64)v[q] << -by[q] : w[q];
+    if (y < fminf(s.deep, 8.f)) return precise(s.top, s.hi, s.lo, x[q], s.unit);
+    return y < s.deep ? (u64)v[q] << 8 >> (8 + (int)by[q]) : w[q];
   }
 };
 __device__ __noinline__ u64 weight(const Scale &s, float x) {
@@ -296,19 +298,40 @@ __device__ __noinline__ int sort_lists(Shared &sh, int rank) {
     __syncthreads();
     return all;
   }
-  int size = 32;  // a power of two
+  // bitonic, a warp's 64 in registers where the places compared lie in them (a step of all threads takes
+  // 400 cycles, 1024 tokens by those alone 12 us)
+  int size = 64;  // a power of two
   while (size < all) size *= 2;
-  for (int i = tid; i < size; i += kThreads) sorted[i] = listed(i);
-  __syncthreads();
-  for (int len = 2; len <= size; len *= 2)  // bitonic
-    for (int gap = len / 2; gap; gap /= 2) {
+  const int lane = tid & 31, i0 = (tid & ~31) * 2 + lane, i1 = i0 + 32;
+  u64 x = i0 < all ? listed(i0) : 0, y = i1 < all ? listed(i1) : 0;
+  auto larger = [](int i, int gap, int len) { return ((i & len) == 0) == ((i & gap) == 0); };
+  auto within = [&](int gap, int len) {
+    for (; gap; gap /= 2) {
+      const bool inner = gap == 32;
+      const u64 ox = inner ? y : __shfl_xor_sync(0xffffffffu, x, gap), oy = inner ? x : __shfl_xor_sync(0xffffffffu, y, gap);
+      x = larger(i0, gap, len) ? max(x, ox) : min(x, ox);
+      y = larger(i1, gap, len) ? max(y, oy) : min(y, oy);
+    }
+  };
+  for (int len = 2; len <= 64; len *= 2) within(len / 2, len);
+  for (int len = 128; len <= size; len *= 2) {
+    __syncthreads();
+    if (i0 < size) sorted[i0] = x, sorted[i1] = y;
+    __syncthreads();
+    for (int gap = len / 2; gap >= 64; gap /= 2) {
       for (int t = tid; t < size / 2; t += kThreads) {
         const int i = 2 * t - (t & (gap - 1)), j = i + gap;
-        const u64 x = sorted[i], y = sorted[j];
-        if ((x < y) == ((i & len) == 0)) sorted[i] = y, sorted[j] = x;
+        const u64 u = sorted[i], v = sorted[j];
+        if ((u < v) == ((i & len) == 0)) sorted[i] = v, sorted[j] = u;
       }
       __syncthreads();
     }
+    if (i0 < size) x = sorted[i0], y = sorted[i1];
+    within(32, len);
+  }
+  __syncthreads();
+  if (i0 < size) sorted[i0] = x, sorted[i1] = y;
+  __syncthreads();
   return all;
 }
 
@@ -518,12 +541,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   top_key = sh.rank_key[0];
   for (int q = 1; q < ranks; ++q)
     if (sh.rank_key[q] > top_key) top_key = sh.rank_key[q], winner = q;
-  Scale s = {logit_of(top_key), c, c_lo, 44, 14.f};
+  Scale s = {logit_of(top_key), c, c_lo, 44, 15.f};
   if (looks) {
     look = 0;
     for (int q = 0; q < ranks; ++q) look += sh.rank_sum[q];
     const float mean = (float)((int64_t)look >> 20) / (float)(look & 0xfffff);
-    if (s.top * c * 16.f - mean < 8.f * 16.f) s.unit = 34, s.deep = 4.f;
+    const float y = s.top * c - mean * 0.0625f;
+    if (y < 16.f) s.unit = y < 8.f ? 34 : 38, s.deep = (float)(s.unit - 29);
   }
   auto finish = [&](int token, float logprob) {
     a.token[row] = token;
@@ -584,18 +608,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const Weights w(s, x);
     u64 sum = 0;
     const bool all = cut == -INFINITY;
-    if (!w.any) {
+    bool on[kSide];
 #pragma unroll
-      for (int q = 0; q < kSide; ++q) {
-        const uint32_t v = all || stays(x[q], first + g * kGroup + q) ? w.w[q] : 0;
-        one(q, v), sum += v;
-      }
-    } else {
+    for (int q = 0; q < kSide; ++q) on[q] = all || stays(x[q], first + g * kGroup + q);
 #pragma unroll
-      for (int q = 0; q < kSide; ++q) {
-        const u64 v = all || stays(x[q], first + g * kGroup + q) ? w.whole(s, x, q) : 0;
-        one(q, v), sum += v;
-      }
+    for (int q = 0; q < kSide; ++q) {
+      const uint32_t v = on[q] && !(depth(s, x[q]) < s.deep) ? w.w[q] : 0;
+      one(q, v), sum += v;
+    }
+    if (w.any) {
+#pragma unroll
+      for (int q = 0; q < kSide; ++q)
+        if (on[q] && depth(s, x[q]) < s.deep) {
+          const u64 v = w.whole(s, x, q);
+          one(q, v), sum += v;
+        }
     }
     return sum;
   };
@@ -664,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     float x[kSide];
     u64 w[kSide];
     decode(fetch(g), g, x);
-    const u64 own = amount(x, g, [&](int q, auto v) { w[q] = v; });
+    const u64 own = amount(x, g, [&](int q, auto v) { w[q] = v; });  // (a token's last is its weight)
     u64 from = before + upto_lane(own) - own;
 #pragma unroll
     for (int q = 0; q < kSide; ++q) {
@@ -828,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // ln w - ln(sum): the sum is the largest weight and what is beside it
     const u64 rest = all - min(all, u64(1) << s.unit);
     const float l = x == s.top ? 0.f : -__fdiv_rn(__fsub_rn(s.top, x), T);
-    finish(i, l - log1pf((float)rest * (s.unit == 44 ? 0x1p-44f : 0x1p-34f)));
+    finish(i, l - log1pf((float)rest * __uint_as_float((uint32_t)(127 - s.unit) << 23)));
   };
   if (held && held <= kCounted) {
     // every block has all that stays: each token's sum of the weights before it, by its index
