@@ -1,5 +1,5 @@
 """Python binding of libmq, the GB300 GGUF block-quantised matmul library, with the paged
-key-value cache and decode attention between its products.
+key-value cache and decode attention between its products and the sampling after the last.
 
 Argument marshalling only: every step of the computation runs in libmq's CUDA
 kernels.  PyTorch provides device memory and streams.  The C ABI
@@ -789,7 +789,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
         None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
         None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(),
         token.data_ptr(), logprob.data_ptr(),
-        _raw_current_stream(logits.device.index) if stream is None else stream.cuda_stream)
+        _raw_current_stream(logits.device.index or 0) if stream is None else stream.cuda_stream)
     if status:
         _check(status)
     return token, logprob

@@ -6,7 +6,7 @@
 // unnormalised o, which pieces of the length join as
 //     M = max m_i,  L = sum l_i exp2(m_i - M),  o = sum o_i exp2(m_i - M) / L.
 //
-// What bounds it: the bytes of K and V.  A group of up to 16 query heads (8 for heads of 192 and
+// What bounds it: the bytes of K and V (over Q4_0 rows the issue slots, below).  A group of up to 16 query heads (8 for heads of 192 and
 // 256) shares one reading of them; a larger one is several row groups, each a unit of its own that
 // reads them again (38 x 8192, F16: 96/4 heads of 128 207 us, 64/4 107; 64/4 heads of 256 405, 8/4
 // 206).  A group's rows share the keys, so
@@ -21,7 +21,8 @@
 // table (a page may end anywhere; a row past the end is filled with zeros, nothing is read for
 // it), so no barrier stands between the loads and the products and about 128 KB are in flight
 // per SM; 44 KB cover the memory's latency.  ldmatrix, transposing for V, reads the operands;
-// rows are padded by 16 bytes, which puts the eight rows of a matrix on different banks.
+// rows are padded by 16 bytes (those of 64 bytes have their chunks exchanged by the key), which puts
+// the eight rows of a matrix on different banks.
 //
 // Work: (sequence, kv head, row group) units of tiles of TK keys, laid end to end; thread block b
 // of the `parts` that have work takes the steps [b T / parts, (b + 1) T / parts) of all T.  The
@@ -44,13 +45,25 @@
 // select per logit cost nothing at 38 x 8192 (28/4 heads of 128) and up to 0.5 us where a block has
 // few tiles (16 x 4096, 16/1 heads of 128, F16: 18.3 -> 18.6 us).
 //
+// Q4_0 rows have half the bytes of Q8_0's and as many products, so that the instructions bound them.
+// A word holds the dims j and 16 + j of four keys' or dims' pairs; the query's rows (and the dims of o)
+// are put in that order instead of the quants.  n - 8 is exact in f16 (a LOP3 and an addition or an fma
+// per pair); the keys' scales multiply their block's sum in binary32, and the values' scales the f16
+// parts of the weights, whose rest the fma keeps.  So the weights' reference may not be raised with a
+// tile's largest scale for nothing: it is kept up to 2^8 below the largest weight (kSlack), which spares
+// the maxima over the lanes and the factors of o in nearly all tiles, and the weights stand at up to
+// 2^7 (kUnit) before the scales; where a tile has a scale of 1 or more a power of two takes it below 1.
+//
 // Measured (28/4 heads of 128; from one card to another 3% apart): 38 x 8192 keys f16 104.5 to 108 us
 // (5.9 to 6.1 TB/s, 88 to 91% of a plain copy's rate), bf16 104.7 to 108, Q8_0 67 (5.1 TB/s, 76%: not
 // the bytes, and no pipe full: half of the issue slots stay empty, two warps per scheduler waiting
 // on fixed latencies of conversions, shared memory and products; its copies alone take 55); 131072
 // bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start, the first rows and the
 // join); 64 ragged sequences up to 8192, f16 97 to 100 us, Q8_0 67.5; one sequence of 37 keys, 14/2
-// heads of 64, 5.1.
+// heads of 64, 5.1.  Q4_0: those 64 sequences 55.2 us (41% of a plain copy's rate; the copies alone take 36.5,
+// all but the copies 55, without the second product 46, with half of the products' instructions
+// 47.4, without the conversion of the quants 52.6, without the scales of V 55.3; 12 warps of 16 or 32
+// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part each) 29.1 us (38%); 37 keys 5.4.
 #pragma once
 
 #include <algorithm>

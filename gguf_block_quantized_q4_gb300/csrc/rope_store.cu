@@ -1,9 +1,10 @@
-// rope_store.cu -- mq_rope_store: bias, rotary positions with several axes, and the store of
-// keys and values into the paged cache.
+// rope_store.cu -- mq_rope_store and mq_norm_rope_store: bias, norms of the query and key heads, rotary
+// positions with several axes, and the store of keys and values into the paged cache.
 //
 // Mathematics: pair i of a head turns by the angle of table[pos[axis[i]]][i] = (c, s),
 //     r0 = a0 c - a1 s,   r1 = a0 s + a1 c,
-// every step rounded on its own (no contraction), so that the result is defined bit for bit.
+// every step rounded on its own (no contraction), so that the result is defined bit for bit.  With norms
+// a0 and a1 are first multiplied by g = 1 / sqrt(mean(a^2) + eps) of their head and by their weights.
 //
 // What bounds it: the bytes of qkv, q and the rows stored, each moved once.  A thread keeps one
 // place in the head, four pairs (two groups of four dims, 16 bytes of f32 each), for all heads
@@ -13,13 +14,21 @@
 // axes and divisions for each: 652 instructions a warp, 131 us for 16384 bf16 tokens); few tokens
 // are spread over more blocks, a round of heads each.  Q8_0 rows: the largest magnitude of a
 // 32-element block meets in shared memory as an integer maximum (the halves of a partial rotation
-// may end inside a block, so no fixed lanes share one), then the quants as in quant_row.cuh.
+// may end inside a block, so no fixed lanes share one), then the quants as in quant_row.cuh.  Q4_0 rows:
+// the largest element keeps its sign, and a block's 32 numbers meet in shared memory, from which every thread
+// packs four bytes of the row.  A norm's two sums (`squares`) are added over the lanes of a head where they are a
+// power of two, else in shared memory by fours; the kernels with norms are made for each head size
+// and go round by round (NP = 1), so that five blocks of 256 threads are on an SM: they are bound by their
+// instructions, not by the bytes.
 // Measured (28/4 heads of 128): 16384 tokens f32 to f16 98 us (5.9 TB/s, 89% of a plain copy's
 // rate), to Q8_0 93 us (90%; three rounds at once spill 8 bytes a thread), bf16 to f16 64 us (72%: one
 // token's loads are in flight per block, fewer bytes than cover the latency); 4096 tokens f32 to
 // f16, three axes, 25.2 us (86%); 1023 tokens bf16 to Q8_0, 32/8 heads, half of a head rotated, 9.9 us
 // (2.8 times its bytes' time: a block has one or two whole tokens, so the shares are uneven); 8
-// tokens 2.1 us.
+// tokens 2.1 us.  4096 tokens, 32/8 heads of 128, f32 to Q4_0: 31.7 us without norms, 45.0 with them (57% of
+// a plain copy's rate; with pairs of sums 63, by whole numbers 50.7, by rounds 47.9, by head size 45.0; four
+// blocks an SM 49.0, six 44.8); 1023 of 12/12 heads of 96, bf16 to bf16, with norms 9.1 us (5.6
+// without); 8 of 16/8 heads of 128 2.8 us.
 #include <algorithm>
 #include <type_traits>
 

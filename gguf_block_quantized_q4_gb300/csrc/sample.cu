@@ -7,7 +7,7 @@
 // last (logit, index) that stays.  The token is the first, in the order of the indexes, at which the
 // running sum of the weights that stay passes u times their sum.
 //
-// What bounds it: the logits are read once (64 rows of 151936: 5.8 us); then latency.  A thread block
+// What bounds it: the logits are read once (64 rows of 151936: 5.7 us); then latency.  A thread block
 // cluster has a row, a run of consecutive tokens per block and of those one per warp, read 128 at a time:
 // such a group's maximum stays in shared memory.  What follows the maximum (one exchange over the
 // cluster) reads only the groups that can matter: a cut's tokens, or what a cut or min-p has left, are in
@@ -15,10 +15,12 @@
 // and flat rows read all logits again, then from the L2 cache.
 //
 // Weights are whole numbers in units of 2^-44 (44 bits for the largest; a token 2^-45 below it weighs
-// nothing, and fewer than 2^19 tokens fit a 64-bit sum).  Sums of whole numbers do not depend on their
-// order, so neither do results: not on the cluster's size, nor on the atomics.  The exponential
-// (weight) is right to about 2^-27 of itself: binary32's own 2^-24 would move the running sum
-// enough to name another token in one of a few hundred rows of flat logits.
+// nothing, and fewer than 2^19 tokens fit a 64-bit sum), of 2^-38 or 2^-34 in flat rows, whose deep
+// weights then fit 32 bits, which a shared atomic adds in 10 cycles a warp (64 bits take 25).  Sums of whole
+// numbers do not depend on their order, so neither do results: not on the cluster's size, nor on the
+// atomics.  The exponential is right to 2^-27 of itself down to 2^-8 of the largest weight: binary32's own
+// 2^-24 would move the running sum enough to name another token in one of a few hundred rows of
+// flat logits.  Below that it is the hardware's (2^-21, the errors of either sign).
 //
 // A cut: the groups' maxima are counted in 2048 bins of y (45 to each halving), which the cluster's blocks
 // add up; a scan names the bin down to which k of them lie.  There are at least k tokens down to that
@@ -27,6 +29,14 @@
 // the bins; the few tokens of the bin that holds the cut are listed then.  Where they are more than
 // a list holds (nearly equal logits) the bin is divided in 2048 once more, and where that does not do
 // (equal ones) three rounds of bins, of the logit's bits, name the logit and a count of equals the index.
+//
+// Measured (f32): one row of 151936 with top-k 40 and top-p 12.9 us, greedy 3.9, the temperature alone 10, top-p of
+// a flat row 22 to 32; 64 such rows with limits of their own 57.6 us (ten times their bytes' time: rows of
+// top-p pass over their logits three times, four blocks each, and all rows are one wave); 256 with min-p
+// 59.0 us (39% of a plain copy's rate); 16 rows of 32003 bf16 logits, most of them masked, top-p 19.2 us.
+// (First form 25.0, 76.2, 155.4 and 23.3 us.)  Of the 50 thousand cycles of a flat top-p row the
+// histogram takes 7, the choice of its bin 7, the lists 7, their sort 8, the last sums 10: barriers of the
+// cluster in each.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -52,7 +62,7 @@ constexpr int kCounted = kThreads / 2;                // listed tokens that are 
 constexpr int kFew = 4;                               // groups that a warp goes through alone
 constexpr int kMaxRanks = 16;
 constexpr float kBinsPerHalving = 45.f;
-constexpr int kLastBin = kBins - 1;  // (2025 and up weigh nothing)
+constexpr int kLastBin = kBins - 1;  // (2026 and up weigh nothing)
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added to a number, it leaves the nearest integer in the low bits
 constexpr uint32_t kMagicBits = 0x4b400000u;
 
@@ -358,7 +368,7 @@ __device__ __noinline__ int place_by_weight(Shared &sh, const Scale &s, int most
   return (int)sh.bin;
 }
 
-// per_rank: tokens of a block; groups: of a warp (their tokens are consecutive).
+// groups: of a warp (their tokens are consecutive, and the warps' in a block, the blocks' in a cluster).
 template <int IO>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int groups) {
   extern __shared__ __align__(16) uint32_t totals[];  // the cluster's bins of this rank's run; the groups' maxima
@@ -966,7 +976,7 @@ mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *
   // Blocks of a cluster: as many as are resident at once for all rows (two to an SM), with 2048 logits or more
   // each.  Twice as many where top-p without top-k, or min-p, can make some rows far longer than others,
   // whose few blocks would be left alone at the end (64 rows of 151936 with settings of their own 71 us, 57
-  // by twice as many; 256 with min-p 85, 70; but 64 with top-k and top-p 22, 36).
+  // by twice as many; 256 with min-p 69, 60; but 64 with top-k and top-p 22, 36).
   const int per_sm = a.min_p || (a.top_p && !a.top_k) ? 4 : 2;
   int r = 0;
   while (r < 4 && a.B << (r + 1) <= per_sm * st->sms && a.V >> (r + 1) >= 2048 && st->sample_clusters[r + 1]) ++r;

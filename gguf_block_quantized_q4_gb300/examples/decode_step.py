@@ -34,7 +34,7 @@ class DecodeStep:
     def decode(self):
         """The step's device calls, from self.token to the next one: only launches, fit for a CUDA
         graph."""
-        x = self.embedding.index_select(0, self.token)
+        x = self.embedding.index_select(0, self.token.clamp(min=0))  # (-1: a row whose logits were no numbers)
         for layer in self.layers:
             x = x + layer.attend(x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6))
         logits = mq.matvec(self.head, x)

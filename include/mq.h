@@ -18,8 +18,10 @@
  *                   mq_mmq_fused does both in one kernel.
  *
  * Between the products of a decoding step: a paged key-value cache, with rotary positions and
- * the store of keys and values (mq_rope_store), attention of one new token per sequence
- * (mq_attn_decode) and eviction by gathered attention weight (mq_kv_evict).
+ * the store of keys and values (mq_rope_store; with norms of the query and key heads
+ * mq_norm_rope_store), attention of one new token per sequence (mq_attn_decode) and eviction by
+ * gathered attention weight (mq_kv_evict).  At its end: the next token from the LM head's logits
+ * (mq_sample).
  *
  * Conventions ("CUDA Backend Design" §4.9 GPU safety; "GPU Safety" CUDA
  * rules): every invariant violation returns an error status and never falls
@@ -439,12 +441,16 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * least, a weight to 2^-40 of the largest before it; weights of Q8_0 values are multiplied by the
  * value's scale first and held to 2^-39 of the largest scale among the keys taken together (16 or
  * 32), so that values 2^20 below a neighbour's lose accuracy where theirs is the larger weight.
+ * Q4_0 keys (exact in f16) meet an f32 query as two f16 parts, a 16-bit one as one (bf16 queries held to
+ * 2^-38 of their row's largest element); the weights are two f16 parts, for bf16 outputs one (11 bits),
+ * multiplied by the value's scale (by a power of two below 1, where the keys taken together have one of 1 or
+ * more) and then held to 2^-32 of the largest weight before them.
  * Infinities and NaN in rows that are read (mq_rope_store rounds to them what F16 does not hold):
  * an infinite value makes its dim of o infinite (NaN beside one of the other sign, or where its
  * weight is below 2^-126), a NaN makes it NaN; a key whose logit is minus infinity weighs
  * nothing (if none weighs anything, o = 0); a logit that is plus infinity or NaN makes the head's o
  * NaN.  (To an infinite F16 key a query element below 2^-39 of its row's largest is a zero.)  The
- * scales of Q8_0 keys must not be infinite; those that mq_rope_store writes are not.
+ * scales of Q8_0 and Q4_0 keys must not be infinite; those that mq_rope_store writes are not.
  *   q, o    device [S][n_heads*head_dim] of type io (MQ_F32, MQ_F16, MQ_BF16), 16-byte aligned;
  *           o may be q itself, but not overlap it otherwise
  *   len     device int32 [S], the rows to read, the new token's own among them; <= max_len
@@ -506,9 +512,12 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages, int64_t pa
  * infinite logit gives token -1, logprob minus infinity.
  * u, temperature, top_p, min_p: device f32 [B]; top_k: device int32 [B]; each but u may be NULL
  * (T = 1, no limit).  token: device int32 [B], logprob: device f32 [B], written; apart from the inputs
- * and each other.  1 <= V < 2^19.  B = 0 does nothing.
- * Weights are held to 2^-27 of themselves and in units of 2^-44 of the largest (a token below that is
- * never drawn), sums of them exactly: results do not depend on the order of execution. */
+ * and each other.  1 <= V < 2^19, B < 2^16.  B = 0 does nothing.
+ * Weights are whole numbers of 2^-44 of the largest (a token 2^-45 below it is never drawn), right to 2^-27 of
+ * themselves down to 2^-8 of the largest (2^-4 in the flattest rows) and to 2^-21 below; in rows of 2^14
+ * tokens or more of which groups of 128 tokens have largest weights of 2^-16 or 2^-8 of the row's on average
+ * (the logarithms' mean), the unit is 2^-38 or 2^-34.  Sums of them are exact: results do not depend on the
+ * order of execution. */
 mq_status mq_sample(mq_type io, const void *logits, int64_t ld, int64_t B, int64_t V, const float *u,
                     const float *temperature, const int32_t *top_k, const float *top_p,
                     const float *min_p, int32_t *token, float *logprob, mq_stream stream);

@@ -1,6 +1,8 @@
 """A decoding step's operators as they run together: QKV product, norms with the rotation and the store into
 a Q4_0 cache, attention with weight sums, eviction, output product, LM head and sampling, against a
 model in 64 bits; call by call and replayed as a graph."""
+import math
+
 import numpy as np
 import pytest
 
@@ -121,3 +123,20 @@ def test_the_example_runs(capsys):
     decode_step.main(steps=40)
     out = capsys.readouterr().out
     assert "40 steps" in out and "as a graph" in out
+
+
+def test_a_sequence_without_a_token_goes_on(capsys):
+    """Logits that are all NaN give token -1; the next step takes the first row of the embedding for it."""
+    S, K, V, dim = 2, 256, 300, 64
+    layer = decode_layer.DecodeLayer(
+        mq.register_weight(mq.Q4_K, synth.weights(synth.Q4_K, 4 * dim, K, 10), 4 * dim, K),
+        mq.register_weight(mq.Q8_0, synth.weights(synth.Q8_0, K, 2 * dim, 20), K, 2 * dim), S, 2, 1, dim, 64, 32, kind=mq.Q4_0)
+    embedding = torch.randn((V, K), generator=torch.Generator().manual_seed(1)).cuda()
+    embedding[7] = math.nan
+    model = decode_step.DecodeStep(embedding, [layer], mq.register_weight(mq.Q6_K, synth.weights(synth.Q6_K, V, K, 30), V, K))
+    model.token[1] = 7
+    assert torch.isnan(model.step()[1]).all()
+    assert int(model.token[1]) == -1 and float(model.logprob[1]) == -math.inf and int(model.token[0]) >= 0
+    assert torch.equal(model.embedding.index_select(0, model.token.clamp(min=0))[1], embedding[0])
+    model.step()
+    mq.stream_status()

@@ -1,5 +1,7 @@
 """mq_sample against the 64-bit definition: every token equal, but where a running sum lies so near a
 border that 2^-24 of the sum decides."""
+import math
+
 import numpy as np
 import pytest
 
@@ -11,8 +13,11 @@ from gguf_block_quantized_q4_gb300 import build as mqbuild  # noqa: E402
 from oracle.sampling import sample  # noqa: E402
 from tests.kv_cases import IO, numpy_of  # noqa: E402
 
-# A weight is right to 2^-27 of itself, so running sums and shares of them to 2^-26 of the sum; tokens
-# below 2^-45 of the largest, at most 2^19 of them, add nothing where they should add up to 2^-26.
+# A weight is right to 2^-27 of itself down to 2^-8 of the largest, so running sums and shares of those to 2^-26
+# of the sum.  Below that it is right to 2^-21 with errors of either sign (mean -8e-9, 2^-27): 64 unlike
+# logits or more leave 2^-21 / 8 of their share at most but rarely.  Rounding to units of 2^-44 (2^-38 or 2^-34
+# in flat rows) adds half a unit of either sign a token, 2^-35 * sqrt(2^19) < 2^-25 in all; tokens below half a
+# unit, at most 2^19 of them, add nothing where they should add up to 2^-26.
 NEAR = 2.0 ** -24
 
 
@@ -217,3 +222,31 @@ def test_draws_follow_the_shares():
     assert (token[1:] >= token[:-1]).all()
     none = mq.sample(x[:0], x[:0, 0])
     assert none[0].shape == (0,)
+
+
+@pytest.mark.parametrize("down", [6.0, 9.0, 14.4, 20.0, 30.0])
+@pytest.mark.parametrize("V", [2049, 151936])
+def test_one_token_above_equal_ones(V, down):
+    """All other tokens 2^-down of the first: their errors are all alike.  An exponential's 2^-21, and half a unit of
+    2^-44 of the largest each (of 2^-38 or 2^-34 in flat rows: less than 2^-20 of the sum over 2^19 tokens, the
+    second only where the sum is above 2^-15 of their number): 2^-19 in a place or a share."""
+    bound = 2.0 ** -19
+    B = 16
+    l = torch.full((B, V), -down * math.log(2.0))
+    l[:, V // 3] = 0.0
+    u = (torch.arange(B) + 0.5) / B
+    token, logprob = mq.sample(l.cuda(), u.cuda())
+    mq.stream_status()
+    w = np.exp(numpy_of(l)[0].astype(np.float64))
+    run = np.cumsum(w) / w.sum()
+    for b in range(B):
+        i = int(token[b])
+        before = run[i - 1] if i else 0.0
+        assert before - bound <= float(u[b]) <= run[i] + bound, (b, i)
+        # (a difference of logits, a logarithm and their sum are rounded to binary32 below 2^5)
+        assert abs(float(logprob[b]) - math.log(w[i] / w.sum())) < 2 * bound + 3 * 2.0 ** -20
+
+
+def test_logits_on_the_host_are_refused():
+    with pytest.raises(mq.MQError, match="logits"):
+        mq.sample(torch.zeros((2, 50)), torch.zeros(2, device="cuda"))
