@@ -25,10 +25,10 @@
 // token's loads are in flight per block, fewer bytes than cover the latency); 4096 tokens f32 to
 // f16, three axes, 25.2 us (86%); 1023 tokens bf16 to Q8_0, 32/8 heads, half of a head rotated, 9.9 us
 // (2.8 times its bytes' time: a block has one or two whole tokens, so the shares are uneven); 8
-// tokens 2.1 us.  4096 tokens, 32/8 heads of 128, f32 to Q4_0: 31.7 us without norms, 45.0 with them (57% of
-// a plain copy's rate; with pairs of sums 63, by whole numbers 50.7, by rounds 47.9, by head size 45.0; four
-// blocks an SM 49.0, six 44.8); 1023 of 12/12 heads of 96, bf16 to bf16, with norms 9.1 us (5.6
-// without); 8 of 16/8 heads of 128 2.8 us.
+// tokens 2.1 us.  4096 tokens, 32/8 heads of 128, f32 to Q4_0: 31.7 us without norms, 44.4 with them (58% of a
+// plain copy's rate; with pairs of sums 63, by whole numbers 50.7, by rounds 47.9, by head size 45.0,
+// magnitudes compared as numbers instead of bits 44.4; four blocks an SM 49.0, six 44.8); 1023 of 12/12
+// heads of 96, bf16 to bf16, with norms 8.9 us (5.6 without); 8 of 16/8 heads of 128 2.8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -57,6 +57,10 @@ __device__ __forceinline__ void turn(float &a, float &b, float2 cs) {
 __device__ __forceinline__ uint32_t top4(float4 v) {  // (a NaN's bits exceed every number's)
   return max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
              max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+}
+// The largest magnitude, a NaN if there is one.
+__device__ __forceinline__ float magnitude4(float4 v) {
+  return max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
 }
 // The scale of a block whose largest magnitude has the bits `top`, and the quants of four of its
 // elements.
@@ -269,7 +273,7 @@ rope_store_kernel(const __grid_constant__ RopeArgs a, int per_pass, int passes) 
         if constexpr ((W & (W - 1)) == 0) {
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
-            uint32_t top = max(top4(x[k]), top4(y[k]));
+            uint32_t top = __float_as_uint(max_nan(magnitude4(x[k]), magnitude4(y[k])));
 #pragma unroll
             for (int i = 1; i < W; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
             const Unit unit = unit_of(top, least);
@@ -286,7 +290,7 @@ rope_store_kernel(const __grid_constant__ RopeArgs a, int per_pass, int passes) 
           uint32_t top[NP];
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
-            top[k] = max(top4(x[k]), top4(y[k]));
+            top[k] = __float_as_uint(max_nan(magnitude4(x[k]), magnitude4(y[k])));
             for (int i = 1; i < 4; i <<= 1) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], i));
             if (threadIdx.x % 4 == 0) quad_top[NORM ? k : 0][threadIdx.x / 4] = top[k];
           }
