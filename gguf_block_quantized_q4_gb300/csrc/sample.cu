@@ -31,9 +31,9 @@
 // (equal ones) three rounds of bins, of the logit's bits, name the logit and a count of equals the index.
 //
 // Measured (f32): one row of 151936 with top-k 40 and top-p 12.9 us, greedy 3.9, the temperature alone 10, top-p of
-// a flat row 22 to 32; 64 such rows with limits of their own 57.6 us (ten times their bytes' time: rows of
-// top-p pass over their logits three times, four blocks each, and all rows are one wave); 256 with min-p
-// 59.0 us (39% of a plain copy's rate); 16 rows of 32003 bf16 logits, most of them masked, top-p 19.2 us.
+// a flat row 22 to 32; 64 such rows with limits of their own 52.5 us (nine times their bytes' time: rows of
+// top-p pass over their logits three times, eight blocks each); 256 with min-p 59.0 us (39% of a plain copy's
+// rate); 16 rows of 32003 bf16 logits, most of them masked, top-p 19.3 us.
 // (First form 25.0, 76.2, 155.4 and 23.3 us.)  Of the 50 thousand cycles of a flat top-p row the
 // histogram takes 7, the choice of its bin 7, the lists 7, their sort 8, the last sums 10: barriers of the
 // cluster in each.
@@ -368,6 +368,28 @@ __device__ __noinline__ int place_by_weight(Shared &sh, const Scale &s, int most
   return (int)sh.bin;
 }
 
+// The row of the cluster `y`: first the rows that pass over all of their logits more than once (top-p without a
+// small top-k, large top-k), in their order, then the others.
+__device__ __noinline__ int row_of(Shared &sh, const SampleArgs &a, int y) {
+  const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
+  bool slow = false;
+  if (r < a.B) {
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const bool few = k > 0 && k <= kQuick;
+    slow = (!a.temperature || a.temperature[r] > 0.f) && !few && ((k > 0 && k < a.V) || (a.top_p && a.top_p[r] < 1.f));
+  }
+  const int n = __syncthreads_count(slow);
+  const bool in = r < a.B && slow == (y < n);
+  const unsigned who = __ballot_sync(0xffffffffu, in);
+  if (lane == 0) sh.warp_key[warp] = __popc(who);
+  __syncthreads();
+  int at = y < n ? y : y - n;
+  for (int w = 0; w < warp; ++w) at -= (int)sh.warp_key[w];
+  if (in && at == __popc(who & ((1u << lane) - 1))) sh.bin = r;
+  __syncthreads();
+  return (int)sh.bin;
+}
+
 // groups: of a warp (their tokens are consecutive, and the warps' in a block, the blocks' in a cluster).
 template <int IO>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int groups) {
@@ -376,7 +398,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.y;
   float *const maxima = reinterpret_cast<float *>(totals + (ranks > 1 ? 2 * kBins / ranks : 0));  // [kWarps][groups]
   float *const mine = maxima + warp * groups;
   auto zero = [&] {
@@ -388,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (tid == 0) sh.listed = 0;
   cluster.barrier_arrive();  // (every block's shared memory exists and is clear; waited for below)
   grid_dependency();
+  const int64_t row = a.slow_first ? row_of(sh, a, (int)blockIdx.y) : (int)blockIdx.y;
 
   const float T = a.temperature ? a.temperature[row] : 1.f;
   const int k = a.top_k ? a.top_k[row] : 0;
@@ -981,10 +1003,15 @@ mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *
   int r = 0;
   while (r < 4 && a.B << (r + 1) <= per_sm * st->sms && a.V >> (r + 1) >= 2048 && st->sample_clusters[r + 1]) ++r;
   const int ranks = 1 << r, groups = groups_of(a.V, ranks);
+  // Where not all clusters are resident at once and rows differ in their cuts (two settings or more are given), the
+  // slow ones begin first: those 64 rows 57.7 us without, 52.5 with; finding its row costs a cluster 1.5 us (64
+  // rows of top-p alone 73 us, 78 with it).
+  SampleArgs b = a;
+  b.slow_first = !!a.top_k + !!a.top_p + !!a.min_p > 1 && a.B <= kThreads && a.B << r > 2 * st->sms;
   auto *kernel = a.io == MQ_F32 ? sample_kernel<MQ_F32> : a.io == MQ_F16 ? sample_kernel<MQ_F16> : sample_kernel<MQ_BF16>;
   return launch_cluster("sample_kernel", kernel, dim3(ranks, (unsigned)a.B, 1), dim3(kThreads, 1, 1),
                         smem_of(groups, ranks),
-                        s, ranks, a, groups);
+                        s, ranks, b, groups);
 }
 
 }  // namespace mq

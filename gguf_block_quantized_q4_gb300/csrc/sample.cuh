@@ -14,6 +14,7 @@ struct SampleArgs {
   const float *top_p, *min_p;
   int32_t *token;
   float *logprob;
+  bool slow_first;  // the launcher's: the order of the rows
 };
 mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *st);
 mq_status init_sample(DeviceState *st);  // shared-memory opt-in, cluster sizes

@@ -250,3 +250,21 @@ def test_one_token_above_equal_ones(V, down):
 def test_logits_on_the_host_are_refused():
     with pytest.raises(mq.MQError, match="logits"):
         mq.sample(torch.zeros((2, 50)), torch.zeros(2, device="cuda"))
+
+
+@pytest.mark.parametrize("B", [64, 300, 512, 513])
+def test_many_rows_of_unlike_settings(B):
+    """More rows than are resident at once, whatever the order they are taken in: each has its own answer."""
+    g = torch.Generator().manual_seed(B)
+    V = 20000
+    x = torch.randn((B, V), generator=g) * 2
+
+    def pick(*values):
+        return [values[int(i)] for i in torch.randint(0, len(values), (B,), generator=g)]
+    given = dict(temperature=pick(0.0, 0.7, 1.5), top_k=pick(0, 0, 20, 900, V), top_p=pick(1.0, 0.6, 0.95),
+                 min_p=pick(0.0, 0.0, 0.05))
+    u = torch.rand(B, generator=g)
+    check(x, u, **given)
+    alike = {k: [v[0]] * B for k, v in given.items()}
+    alike["top_p"], alike["temperature"] = [0.8] * B, [1.0] * B
+    check(x[:64], u[:64], **{k: v[:64] for k, v in alike.items()})
