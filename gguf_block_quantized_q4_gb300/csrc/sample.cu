@@ -995,19 +995,25 @@ mq_status init_sample(DeviceState *st) {
 }
 
 mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *st) {
-  // Blocks of a cluster: as many as are resident at once for all rows (two to an SM), with 2048 logits or more
-  // each.  Twice as many where top-p without top-k, or min-p, can make some rows far longer than others,
-  // whose few blocks would be left alone at the end (64 rows of 151936 with settings of their own 71 us, 57
-  // by twice as many; 256 with min-p 69, 60; but 64 with top-k and top-p 22, 36).
-  const int per_sm = a.min_p || (a.top_p && !a.top_k) ? 4 : 2;
+  // Blocks of a cluster: as many as leave all rows resident at once (one row after the other costs twice the time: 16
+  // rows of 151936 with top-k and top-p 14.8 us by 8 blocks each, 27.2 by 16, of which 14 rows fit), with
+  // 2048 logits or more each.  Twice as many where rows may take unlike times and the few blocks of the slow ones
+  // would be left alone at the end: top-p with min-p, from 4 blocks down (64 rows with settings of their own 66 us,
+  // 52 by twice as many; of the same settings 18, 35); top-p alone, from 2 down (128 rows 105, 99; 256 203,
+  // 176; but 42 55, 61); min-p without it, from one (256 rows at T = 1 69, 59; of few tokens that stay 35, 44).
+  auto fits = [&](int ranks_log, int waves) {
+    return ranks_log <= 4 && a.V >> ranks_log >= 2048 && a.B <= int64_t(waves) * st->sample_clusters[ranks_log];
+  };
   int r = 0;
-  while (r < 4 && a.B << (r + 1) <= per_sm * st->sms && a.V >> (r + 1) >= 2048 && st->sample_clusters[r + 1]) ++r;
+  while (fits(r + 1, 1)) ++r;
+  const int most = a.top_p ? (a.min_p ? 2 : a.top_k ? -1 : 1) : a.min_p ? 0 : -1;
+  if (r <= most && fits(r + 1, 2)) ++r;
   const int ranks = 1 << r, groups = groups_of(a.V, ranks);
   // Where not all clusters are resident at once and rows differ in their cuts (two settings or more are given), the
   // slow ones begin first: those 64 rows 57.7 us without, 52.5 with; finding its row costs a cluster 1.5 us (64
   // rows of top-p alone 73 us, 78 with it).
   SampleArgs b = a;
-  b.slow_first = !!a.top_k + !!a.top_p + !!a.min_p > 1 && a.B <= kThreads && a.B << r > 2 * st->sms;
+  b.slow_first = !!a.top_k + !!a.top_p + !!a.min_p > 1 && a.B <= kThreads && a.B > st->sample_clusters[r];
   auto *kernel = a.io == MQ_F32 ? sample_kernel<MQ_F32> : a.io == MQ_F16 ? sample_kernel<MQ_F16> : sample_kernel<MQ_BF16>;
   return launch_cluster("sample_kernel", kernel, dim3(ranks, (unsigned)a.B, 1), dim3(kThreads, 1, 1),
                         smem_of(groups, ranks),
