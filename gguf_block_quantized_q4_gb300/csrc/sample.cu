@@ -77,6 +77,7 @@ struct Shared {
   uint32_t warp_key[kWarps];
   uint32_t rank_key[kMaxRanks], rank_n[kMaxRanks];
   u64 rank_sum[kMaxRanks];
+  u64 rank_look[kMaxRanks];  // (read without a barrier behind: a block that is ahead writes rank_sum meanwhile)
   u64 above, inside;  // of the bin that was chosen: what lies before it, and in it
   uint32_t bin, listed, cut_index;
   float least;
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cluster.barrier_wait();
   if (tid < ranks) {
     *cluster.map_shared_rank(&sh.rank_key[rank], tid) = top_key;
-    if (looks) *cluster.map_shared_rank(&sh.rank_sum[rank], tid) = sh.sum;
+    if (looks) *cluster.map_shared_rank(&sh.rank_look[rank], tid) = sh.sum;
   }
   cluster.sync();
   int winner = 0;  // the first rank with the row's maximum
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   Scale s = {logit_of(top_key), c, c_lo, 44, 15.f};
   if (looks) {
     look = 0;
-    for (int q = 0; q < ranks; ++q) look += sh.rank_sum[q];
+    for (int q = 0; q < ranks; ++q) look += sh.rank_look[q];
     const float mean = (float)((int64_t)look >> 20) / (float)(look & 0xfffff);
     const float y = s.top * c - mean * 0.0625f;
     if (y < 16.f) s.unit = y < 8.f ? 34 : 38, s.deep = (float)(s.unit - 29);
