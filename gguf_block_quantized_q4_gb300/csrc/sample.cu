@@ -921,6 +921,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   } else if (by_floor || by_count) {
     // few tokens of a group stay, and most of them are not deep: they are put side by side for their weights
     // (256 rows of 151936 with min-p: 67 us without)
+    __syncthreads();  // (the cut has been read from the list)
     float *const queue = reinterpret_cast<float *>(sh.list[1]) + warp * 64;
     int waiting = 0;
     each(cut, [&](const float (&x)[kSide], int g) {

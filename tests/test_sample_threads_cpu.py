@@ -38,3 +38,12 @@ def test_temperature_alone(f, V, ranks_log):
     """A block that is ahead has its sum ready while others still choose the weights' unit."""
     x, u = rows(2, V, 0)
     run(f, x, u, ranks_log, temperature=[0.8, 1.3])
+
+
+@pytest.mark.parametrize("ranks_log", [0, 1])
+@pytest.mark.parametrize("k", [257, 289, 321, 500, 700])
+def test_cuts_that_leave_more_than_are_counted(f, k, ranks_log):
+    """The cut is read from the sorted list by all threads before the list's place is used again."""
+    x, u = rows(1, 12001, k)
+    run(f, x, u, ranks_log, top_k=[k])
+    run(f, x, u, ranks_log, top_k=[k], top_p=[0.999])
