@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (lane == 0) mine[g] = best;
     top = fmaxf(top, best);
   });
+  __syncwarp();  // (lane 0's maxima are read by the others)
 
   // ---- the maximum ----
   uint32_t top_key = key_of(top);

@@ -47,3 +47,15 @@ def test_cuts_that_leave_more_than_are_counted(f, k, ranks_log):
     x, u = rows(1, 12001, k)
     run(f, x, u, ranks_log, top_k=[k])
     run(f, x, u, ranks_log, top_k=[k], top_p=[0.999])
+
+
+def test_unit_of_the_weights(f):
+    """What the unit is chosen by has every group's maximum: here their mean lies at 2^-7.93, and at
+    2^-8.03 without the last one of each warp; the other tokens, at 2^-36, count in the smaller unit only."""
+    V, ln2 = 16384, np.log(2.0)
+    x = np.full((1, V), -36 * ln2, np.float32)
+    x[0, 64::128] = -8.1 * ln2      # 128 groups, nine to a warp
+    x[0, 64 + 128 * 8::128 * 9] = -7.1 * ln2
+    x[0, 5] = 0
+    u = np.array([0.3], np.float32)
+    run(f, x, u, 0, temperature=[1.0])
