@@ -63,7 +63,7 @@
 // heads of 64, 5.1.  Q4_0: those 64 sequences 55.2 us (41% of a plain copy's rate; the copies alone take 36.5,
 // all but the copies 55, without the second product 46, with half of the products' instructions
 // 47.4, without the conversion of the quants 52.6, without the scales of V 55.3; 12 warps of 16 or 32
-// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part each) 29.1 us (38%); 37 keys 5.4.
+// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 31.2 us (36%); 37 keys 5.4.
 #pragma once
 
 #include <algorithm>
@@ -214,11 +214,10 @@ struct Shape {
   static constexpr bool kScaled = kQ8 || kQ4;   // blocks of 32 dims with a scale each
   static constexpr bool kBf = TYPE == MQ_BF16;  // operands bf16, else f16
   // parts of the query and of the weights.  Q4_0: 16-bit queries are one f16 part (f16 exact, bf16 to 2^-38 of
-  // the row's largest), and for bf16 outputs so are the weights, whose 11 bits are eight times finer than
-  // an output's: mma.sync holds the issue port for 8.6 cycles here, and its instructions were 37% of the
-  // time of a tile (131072 keys, bf16: 32.9 us with two parts each)
+  // the row's largest), as mma.sync holds the issue port for 8.6 cycles here and its instructions are 37%
+  // of the time of a tile.
   static constexpr int kQueryParts = kBf ? 3 : kQ4 && IO != MQ_F32 ? 1 : 2;
-  static constexpr int kParts = kBf ? 3 : kQ4 && IO == MQ_BF16 ? 1 : 2;
+  static constexpr int kParts = kBf ? 3 : 2;
   static constexpr int kRow = kQ4 ? D / 2 : kQ8 ? D : 2 * D;  // bytes of a key row
   static constexpr int kNG = D / 32;            // groups of 32 dims
   static constexpr int kMT = kRow <= 128 ? 2 : 1;  // 16-key groups a warp takes at a time

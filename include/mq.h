@@ -442,7 +442,7 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * value's scale first and held to 2^-39 of the largest scale among the keys taken together (16 or
  * 32), so that values 2^20 below a neighbour's lose accuracy where theirs is the larger weight.
  * Q4_0 keys (exact in f16) meet an f32 query as two f16 parts, a 16-bit one as one (bf16 queries held to
- * 2^-38 of their row's largest element); the weights are two f16 parts, for bf16 outputs one (11 bits),
+ * 2^-38 of their row's largest element); the weights are two f16 parts,
  * multiplied by the value's scale (by a power of two below 1, where the keys taken together have one of 1 or
  * more) and then held to 2^-32 of the largest weight before them.
  * Infinities and NaN in rows that are read (mq_rope_store rounds to them what F16 does not hold):

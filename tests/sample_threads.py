@@ -30,7 +30,7 @@ def build(folder):
         with open(os.path.join(folder, name), "w") as f:
             f.write(body)
     lib = os.path.join(folder, "sample_host.so")
-    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-ffp-contract=off", "-I", HERE, "-I", folder,
+    subprocess.run(["g++", "-O2", "-U_FORTIFY_SOURCE", "-std=c++17", "-shared", "-fPIC", "-ffp-contract=off", "-I", HERE, "-I", folder,
                     f'-DSAMPLE_CU="{os.path.join(folder, "sample.cu")}"', os.path.join(HERE, "sample_host.cpp"), "-o", lib],
                    check=True, capture_output=True, text=True)
     f = ctypes.CDLL(lib).sample_host

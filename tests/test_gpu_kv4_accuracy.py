@@ -1,0 +1,60 @@
+"""Attention over Q4_0 rows keeps what two f16 parts of a weight hold, whatever the activations' type and however
+small the values' scales: bounds without a term for weights of fewer bits."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import gguf_block_quantized_q4_gb300 as mq  # noqa: E402
+from gguf_block_quantized_q4_gb300 import build as mqbuild  # noqa: E402
+from oracle import kv  # noqa: E402
+from tests.kv4_cases import Paged4, attn_bound4  # noqa: E402
+from tests.kv_cases import IO, numpy_of, tiny  # noqa: E402
+
+BITS = {"f32": 24, "f16": 11, "bf16": 8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    mqbuild.build()
+    mq.init(0)
+    yield
+
+
+def check(p, q, io, scale):
+    o = mq.attn_decode(p.cache, q.cuda(), p.pages, p.lens, p.max_len, scale=scale)
+    mq.stream_status()
+    ref, mass, reach, _ = kv.attn_decode(p.host, p.page_size, numpy_of(q), p.pages_host, p.lens_list, scale, 0)
+    _, rel = attn_bound4(p, numpy_of(q), ref, mass, reach, scale, 0, io)
+    # What f16 holds of small weights: a weight (2^15 for the largest) and its product with a scale d below 1 end in three
+    # roundings to steps of 2^-24, half a step each: a key with a number of at most 8 loses 8 * 3 * 2^-25 of
+    # 2^15 in units of `unit`, a power of two up to twice the largest scale (2^-15 at least: smaller scales are
+    # brought up by 2^15).
+    unit = max(2.0 ** -15, 2 * float(np.nanmax(np.abs(p.host["v_scale"].astype(np.float64)))))
+    floor = np.array([24 * n * 2.0 ** -40 * unit for n in p.lens_list])[:, None, None]
+    near = floor + np.expm1(rel)[..., None] * mass
+    # the rounding to the output's type: half a step of the binade that the value lies in
+    step = np.exp2(np.floor(np.log2(np.abs(ref) + near + 1e-300))) * 2.0 ** -BITS[io]
+    err = np.abs(numpy_of(o).astype(np.float64) - ref)
+    bound = near + step + tiny(io)
+    assert (err <= bound).all(), f"worst err/bound {np.max(err / bound):.3g}, {np.mean(err > bound):.3g} of all"
+
+
+def queries(S, hq, dim, io, seed, size=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn((S, hq, dim), generator=g) * size).to(IO[io])
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_rounded_once(dim, io):
+    """Few keys, so that the errors of their weights do not cancel: the output's rounding is the only one of its
+    size."""
+    lens = [1, 2, 2, 3, 3, 5, 9, 17, 33] * 4
+    p = Paged4(lens, 2, dim, 16, seed=dim)
+    check(p, queries(len(lens), 14, dim, io, dim), io, dim ** -0.5)

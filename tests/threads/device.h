@@ -10,6 +10,7 @@
 // that block has ended, a launch that the stand-in does not know.
 #pragma once
 
+#include <setjmp.h>
 #include <ucontext.h>
 
 #include <algorithm>
@@ -70,7 +71,9 @@ struct Block {
   size_t fixed_bytes = 0, dynamic_bytes = 0;
 };
 struct Fiber {
-  ucontext_t at;
+  ucontext_t start;
+  jmp_buf at;  // (a swap of contexts would call the system each time)
+  bool begun = false;
   std::unique_ptr<char[]> stack;
   unsigned cluster_phase = 0, votes = 0, exchanges = 0;
   Block *block;
@@ -88,7 +91,7 @@ struct Machine {
   Barrier cluster;
   std::set<std::pair<int, Fiber *>> ready;
   Fiber *now = nullptr;
-  ucontext_t home;
+  jmp_buf home;
   void (*body)(void *);
   void *arg;
 };
@@ -99,6 +102,9 @@ inline Fiber &self() { return *machine->now; }
   std::exit(3);
 }
 
+inline void leave(Fiber &f) {
+  if (_setjmp(f.at) == 0) _longjmp(machine->home, 1);
+}
 inline void Barrier::look() {
   if (arrived == 0 || arrived < expected) return;
   arrived = 0, ++phase;
@@ -110,7 +116,7 @@ inline void wait(Barrier &b, unsigned phase) {
   Fiber &f = self();
   if (b.phase == phase) b.waiting.push_back(&f);
   else machine->ready.insert({f.place, &f});
-  swapcontext(&f.at, &machine->home);
+  leave(f);
 }
 inline void sync(Barrier &b) { wait(b, b.arrive()); }
 
@@ -142,7 +148,7 @@ inline void entry() {
   f.done = true;
   --f.block->left;
   f.warp->all.drop(), f.block->all.drop(), m->cluster.drop();
-  swapcontext(&f.at, &m->home);
+  leave(f);
 }
 
 // One cluster of `ranks` blocks: body(arg) in every thread.  order[i]: the i-th thread (rank * block + thread) that
@@ -171,10 +177,10 @@ inline void run_cluster(int ranks, int block, dim3 first, size_t fixed, size_t d
     f.thread = i % block, f.rank = i / block;
     f.block_index = dim3(first.x + f.rank, first.y, first.z);
     f.stack = std::unique_ptr<char[]>(new char[kStack]);
-    getcontext(&f.at);
-    f.at.uc_stack.ss_sp = f.stack.get(), f.at.uc_stack.ss_size = kStack;
-    f.at.uc_link = nullptr;
-    makecontext(&f.at, entry, 0);
+    getcontext(&f.start);
+    f.start.uc_stack.ss_sp = f.stack.get(), f.start.uc_stack.ss_size = kStack;
+    f.start.uc_link = nullptr;
+    makecontext(&f.start, entry, 0);
   }
   for (int i = 0; i < n; ++i) {
     Fiber &f = m.fibers[order[i]];
@@ -185,7 +191,11 @@ inline void run_cluster(int ranks, int block, dim3 first, size_t fixed, size_t d
   while (!m.ready.empty()) {
     m.now = m.ready.begin()->second;
     m.ready.erase(m.ready.begin());
-    swapcontext(&m.home, &m.now->at);
+    if (_setjmp(m.home) == 0) {
+      if (m.now->begun) _longjmp(m.now->at, 1);
+      m.now->begun = true;
+      setcontext(&m.now->start);
+    }
     left -= m.now->done;
   }
   if (left) fail("threads wait for one another");
