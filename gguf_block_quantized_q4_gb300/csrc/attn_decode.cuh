@@ -49,10 +49,9 @@
 // A word holds the dims j and 16 + j of four keys' or dims' pairs; the query's rows (and the dims of o)
 // are put in that order instead of the quants.  n - 8 is exact in f16 (a LOP3 and an addition or an fma
 // per pair); the keys' scales multiply their block's sum in binary32, and the values' scales the f16
-// parts of the weights, whose rest the fma keeps.  So the weights' reference may not be raised with a
-// tile's largest scale for nothing: it is kept up to 2^8 below the largest weight (kSlack), which spares
-// the maxima over the lanes and the factors of o in nearly all tiles, and the weights stand at up to
-// 2^7 (kUnit) before the scales; where a tile has a scale of 1 or more a power of two takes it below 1.
+// parts of the weights, whose rest the fma keeps; where a tile has a scale of 1 or more a power of two takes it
+// below 1.  A tile without a logit above its row's largest so far, as most are, spares the maxima over the
+// lanes.
 //
 // Measured (28/4 heads of 128; from one card to another 3% apart): 38 x 8192 keys f16 104.5 to 108 us
 // (5.9 to 6.1 TB/s, 88 to 91% of a plain copy's rate), bf16 104.7 to 108, Q8_0 67 (5.1 TB/s, 76%: not
@@ -60,10 +59,10 @@
 // on fixed latencies of conversions, shared memory and products; its copies alone take 55); 131072
 // bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start, the first rows and the
 // join); 64 ragged sequences up to 8192, f16 97 to 100 us, Q8_0 67.5; one sequence of 37 keys, 14/2
-// heads of 64, 5.1.  Q4_0: those 64 sequences 55.2 us (41% of a plain copy's rate; the copies alone take 36.5,
+// heads of 64, 5.1.  Q4_0: those 64 sequences 56.4 us (41% of a plain copy's rate; the copies alone take 36.5,
 // all but the copies 55, without the second product 46, with half of the products' instructions
 // 47.4, without the conversion of the quants 52.6, without the scales of V 55.3; 12 warps of 16 or 32
-// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 31.2 us (36%); 37 keys 5.4.
+// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 31.9 us (35%); 37 keys 5.4.
 #pragma once
 
 #include <algorithm>
@@ -252,9 +251,7 @@ struct Shape {
   // the f16 parts hold weights in (0, 2^15], so that the second part of all but negligible weights is
   // a normal f16.  (Multiplied in after the exponential: added to its argument it would round that
   // to 2^-21 where s - m itself is nearly exact.)
-  // Q4_0: their reference may lie up to kSlack (halvings) below the largest.
-  static constexpr float kSlack = 8.f;
-  static constexpr float kUnit = kBf ? 1.f : kQ4 ? 0x1p7f : 0x1p15f;
+  static constexpr float kUnit = kBf ? 1.f : 0x1p15f;
 };
 
 struct Params {
@@ -1027,8 +1024,8 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int w = 0; w < 4; ++w) s[m][n][w] *= fac[n][w & 1];
-        // Q4_0: weights against a reference that is at most kSlack below the largest logit so far, so that most
-        // tiles need no maximum over the lanes (three shuffles one after the other)
+        // Q4_0: a tile without a logit above its row's largest so far, as most are, needs no maximum over the lanes
+        // (three shuffles one after the other)
         bool renew = !C::kQ4;
         if (here != kAll) {
 #pragma unroll
@@ -1062,7 +1059,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
               float top = -INFINITY;
 #pragma unroll
               for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][w], s[m][n][w + 2]));
-              renew |= top > mx[n][w] + C::kSlack;  // (any logit, where there is no reference yet)
+              renew |= top > mx[n][w];
             }
           renew = __any_sync(0xffffffffu, renew);
         }

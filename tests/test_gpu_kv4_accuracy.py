@@ -58,3 +58,27 @@ def test_rounded_once(dim, io):
     lens = [1, 2, 2, 3, 3, 5, 9, 17, 33] * 4
     p = Paged4(lens, 2, dim, 16, seed=dim)
     check(p, queries(len(lens), 14, dim, io, dim), io, dim ** -0.5)
+
+
+@pytest.mark.parametrize("size", [0.7])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_light_keys_beside_a_heavy_one(dim, size):
+    """The heavy key's value is zero: what is left are weights of 2^-16 to 2^-36 of the largest."""
+    S, hq = 2, 14
+    p = Paged4([2, 3], 1, dim, 16, seed=1)
+    kn, vn = ((p.host[x] + 8).astype(np.uint8) for x in ("k", "v"))
+    ks, vs = (p.host[x + "_scale"].copy() for x in ("k", "v"))
+    for s in range(S):
+        page, slot = kv.place(p.pages_host[s], 16, np.arange(p.lens_list[s]))
+        kn[page, 0, slot] = 8                       # logits of zero ...
+        kn[page[0], 0, slot[0]] = 15                # ... but for the first key's
+        ks[page, 0, slot] = 0.125
+        vn[page[0], 0, slot[0]] = 8
+        vs[page, 0, slot] = size
+    p.set("k", kv.pack4(kn), ks)
+    p.set("v", kv.pack4(vn), vs)
+    p.cache = p.wrap()
+    # logit = scale * sum q k = q dim 0.875 scale: (16 + 20 i / hq) ln 2
+    want = torch.tensor([(16 + 20 * i / hq) * math.log(2) for i in range(hq)])
+    q = (want / (dim * 0.875 * dim ** -0.5))[None, :, None].expand(S, hq, dim).contiguous()
+    check(p, q, "f32", dim ** -0.5)
