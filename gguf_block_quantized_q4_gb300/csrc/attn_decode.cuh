@@ -49,9 +49,10 @@
 // A word holds the dims j and 16 + j of four keys' or dims' pairs; the query's rows (and the dims of o)
 // are put in that order instead of the quants.  n - 8 is exact in f16 (a LOP3 and an addition or an fma
 // per pair); the keys' scales multiply their block's sum in binary32, and the values' scales the f16
-// parts of the weights, whose rest the fma keeps; where a tile has a scale of 1 or more a power of two takes it
-// below 1.  A tile without a logit above its row's largest so far, as most are, spares the maxima over the
-// lanes.
+// parts of the weights, whose rest the fma keeps.  A power of two puts a tile's largest value scale between 1/2 and 1:
+// downwards it divides the weights (at 2^15, f16 has no room above them), upwards it multiplies the scales.  (Only
+// for tiles outside [2^-4, 1): 57.7 to 59.6 us, by where it stands, at the 64 sequences below.)  A tile
+// without a logit above its row's largest so far, as most are, spares the maxima over the lanes (59.1 -> 58.2).
 //
 // Measured (28/4 heads of 128; from one card to another 3% apart): 38 x 8192 keys f16 104.5 to 108 us
 // (5.9 to 6.1 TB/s, 88 to 91% of a plain copy's rate), bf16 104.7 to 108, Q8_0 67 (5.1 TB/s, 76%: not
@@ -59,10 +60,10 @@
 // on fixed latencies of conversions, shared memory and products; its copies alone take 55); 131072
 // bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start, the first rows and the
 // join); 64 ragged sequences up to 8192, f16 97 to 100 us, Q8_0 67.5; one sequence of 37 keys, 14/2
-// heads of 64, 5.1.  Q4_0: those 64 sequences 56.4 us (41% of a plain copy's rate; the copies alone take 36.5,
+// heads of 64, 5.1.  Q4_0: those 64 sequences 58.2 us (39% of a plain copy's rate; the copies alone take 36.5,
 // all but the copies 55, without the second product 46, with half of the products' instructions
 // 47.4, without the conversion of the quants 52.6, without the scales of V 55.3; 12 warps of 16 or 32
-// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 31.9 us (35%); 37 keys 5.4.
+// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 32.6 us (34%); 37 keys 5.4.
 #pragma once
 
 #include <algorithm>
@@ -871,20 +872,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             for (int j = 0; j < SW; ++j) w[j] = __funnelshift_r(w[j], j + 1 < SW ? w[(j + 1) % SW] : 0, shift);
           }
         };
-        bool scales_known = !C::kScaled;  // (the power of two: 1)
-        if (C::kQ4) {  // scales below 1 are multiplied as they are stored: a look at whether one is not
-          uint32_t high = 0;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t w[SW];
-            scales_of(w, 1, 16 * m + (lane & 15));
-            if (NG & 1) w[SW - 1] &= 0xffffu;
-#pragma unroll
-            for (int j = 0; j < SW; ++j) high |= (w[j] & 0x7fff7fffu) + 0x44004400u;  // (bit 15 from 0x3c00 on)
-          }
-          scales_known = !__any_sync(0xffffffffu, high & 0x80008000u);
-        }
-        if (!scales_known) {  // a power of two that V's largest scale of the tile is below
+        if (C::kScaled) {  // a power of two that V's largest scale of the tile is below
           uint32_t top = 0;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -896,9 +884,10 @@ attn_decode_kernel(const __grid_constant__ Params p) {
               top = max(top, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
           }
           top = __reduce_max_sync(0xffffffffu, top);
-          const int e = top == 0 || top >= 0x7c00u
-                            ? 126
-                            : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+          int e = top == 0 || top >= 0x7c00u
+                      ? 126
+                      : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+          if (C::kQ4) e = max(e, 111);  // (up by 2^15 at most: a factor in f16)
           tile_unit = __uint_as_float(uint32_t(e + 1) << 23), per_unit = __uint_as_float(uint32_t(253 - e) << 23);
         }
         // ---- S^T = K Q^T ----
@@ -1089,7 +1078,7 @@ attn_decode_kernel(const __grid_constant__ Params p) {
             if (C::kQ4) sum *= C::kUnit;
             ls[n][w] = fmaf(ls[n][w], al[n][w], sum);
           }
-        const float weight_unit = C::kUnit * per_unit;  // Q4_0
+        const float weight_unit = C::kUnit * fminf(per_unit, 1.f);  // Q4_0
         // the weights transposed: lane (g, t) gets row g's of the keys 2t, 2t + 1, 2t + 8, 2t + 9;
         // their parts, or for Q8_0 (whose blocks' scales come first) as binary32 in two halves
         uint32_t pw[MT][NT][2][C::kParts];
@@ -1124,6 +1113,18 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int q = 0; q < 4; ++q) scales_of(vscale[m][q], 1, 16 * m + 8 * (q >> 1) + 2 * t + (q & 1));
+        if (C::kQ4 && per_unit > 1.f) {  // (exact)
+          const __half2 up = __float2half2_rn(per_unit);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int j = 0; j < SW; ++j) {
+                const __half2 d = __hmul2_rn(*reinterpret_cast<const __half2 *>(&vscale[m][q][j]), up);
+                vscale[m][q][j] = *reinterpret_cast<const uint32_t *>(&d);
+              }
+        }
 #pragma unroll
         for (int j0 = 0; j0 < NG; j0 += 2) {  // (two groups of 32 dims, four chains)
           float c[2][2][NT][4] = {};

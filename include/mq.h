@@ -442,9 +442,9 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *cache, int64_t S, int n_heads,
  * value's scale first and held to 2^-39 of the largest scale among the keys taken together (16 or
  * 32), so that values 2^20 below a neighbour's lose accuracy where theirs is the larger weight.
  * Q4_0 keys (exact in f16) meet an f32 query as two f16 parts, a 16-bit one as one (bf16 queries held to
- * 2^-38 of their row's largest element); the weights are two f16 parts,
- * multiplied by the value's scale (by a power of two below 1, where the keys taken together have one of 1 or
- * more) and then held to 2^-40 of the largest weight before them.
+ * 2^-38 of their row's largest element); the weights are two f16 parts, multiplied by the value's scale and
+ * held to 2^-39 of the largest weight before them times the largest scale among the keys taken together (16
+ * or 32; to 2^-39 of 2^-15 where that scale is smaller).
  * Infinities and NaN in rows that are read (mq_rope_store rounds to them what F16 does not hold):
  * an infinite value makes its dim of o infinite (NaN beside one of the other sign, or where its
  * weight is below 2^-126), a NaN makes it NaN; a key whose logit is minus infinity weighs

@@ -60,7 +60,7 @@ def test_rounded_once(dim, io):
     check(p, queries(len(lens), 14, dim, io, dim), io, dim ** -0.5)
 
 
-@pytest.mark.parametrize("size", [0.7])
+@pytest.mark.parametrize("size", [0.7, 2.0 ** -4, 2.0 ** -9, 2.0 ** -14, 2.0 ** -20])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_light_keys_beside_a_heavy_one(dim, size):
     """The heavy key's value is zero: what is left are weights of 2^-16 to 2^-36 of the largest."""
@@ -82,3 +82,29 @@ def test_light_keys_beside_a_heavy_one(dim, size):
     want = torch.tensor([(16 + 20 * i / hq) * math.log(2) for i in range(hq)])
     q = (want / (dim * 0.875 * dim ** -0.5))[None, :, None].expand(S, hq, dim).contiguous()
     check(p, q, "f32", dim ** -0.5)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -8, 2.0 ** -12, 2.0 ** -16, 2.0 ** -20])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_small_scales(size, dim):
+    p = Paged4([300, 33, 70, 5], 1, dim, 16, seed=8)
+    sc = (np.random.default_rng(3).standard_normal(p.host["v_scale"].shape) * size).astype(np.float16)
+    sc[np.isnan(p.host["v_scale"])] = np.nan
+    p.set("v", kv.pack4((p.host["v"] + 8).astype(np.uint8)), sc)
+    p.cache = p.wrap()
+    check(p, queries(4, 8, dim, "f32", 2), "f32", dim ** -0.5)
+
+
+def test_tiles_of_unlike_scales():
+    """Small scales, then large ones, then small ones: each tile's power of two is its own."""
+    p = Paged4([2000], 1, 128, 16, seed=9)
+    rng = np.random.default_rng(4)
+    sc = rng.standard_normal(p.host["v_scale"].shape)
+    page, slot = kv.place(p.pages_host[0], 16, np.arange(2000))
+    size = np.exp2(rng.integers(-20, 12, 2000 // 50).repeat(50).astype(np.float64))
+    sc[page, 0, slot] *= size[:, None]
+    sc = sc.astype(np.float16)
+    sc[np.isnan(p.host["v_scale"])] = np.nan
+    p.set("v", kv.pack4((p.host["v"] + 8).astype(np.uint8)), sc)
+    p.cache = p.wrap()
+    check(p, queries(1, 28, 128, "f32", 3), "f32", 128 ** -0.5)
