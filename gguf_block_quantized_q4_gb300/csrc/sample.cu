@@ -33,7 +33,7 @@
 // Measured (f32): one row of 151936 with top-k 40 and top-p 12.9 us, greedy 3.9, the temperature alone 10, top-p of
 // a flat row 22 to 32; 64 such rows with limits of their own 52.5 us (nine times their bytes' time: rows of
 // top-p pass over their logits three times, eight blocks each); 256 with min-p 59.0 us (39% of a plain copy's
-// rate); 16 rows of 32003 bf16 logits, most of them masked, top-p 19.3 us.
+// rate); 16 rows of 32003 bf16 logits, most of them masked, top-p 20.0 us.
 // (First form 25.0, 76.2, 155.4 and 23.3 us.)  Of the 50 thousand cycles of a flat top-p row the
 // histogram takes 7, the choice of its bin 7, the lists 7, their sort 8, the last sums 10: barriers of the
 // cluster in each.
@@ -391,6 +391,37 @@ __device__ __noinline__ int row_of(Shared &sh, const SampleArgs &a, int y) {
   return (int)sh.bin;
 }
 
+// What the unit of the weights is chosen by: of a warp's groups, counted from the row's first token on, the maxima
+// times `by` (rounded, in the upper bits) and their number.  The groups as they are read begin `off` tokens
+// earlier: their first tokens are the group's before, and where one of those may be the maximum, the group
+// is read again.
+template <int IO>
+__device__ __noinline__ u64 look_at(const void *from, int V, int off, int first, int groups, const float *maxima, float by) {
+  const int lane = threadIdx.x & 31;
+  u64 look = 0;
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int at = (first + g0 + lane) * kGroup;
+    const bool on = g0 + lane < groups && at < V;
+    float top = on ? maxima[g0 + lane] : -INFINITY;
+    if (off) {
+      bool again = false;
+      for (int i = at - off; i < at; ++i)
+        if (i >= 0 && top > -INFINITY) again |= load_io1(from, IO, i) >= top;
+      for (unsigned todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
+        const int who = __ffs(todo) - 1, start = (first + g0 + who) * kGroup;
+        float t = -INFINITY;
+        for (int i = start + lane; i < min(start + kGroup, V); i += 32) t = fmaxf(t, load_io1(from, IO, i));
+        t = logit_of(__reduce_max_sync(0xffffffffu, key_of(t)));
+        if (lane == who) top = t;
+      }
+      if (on)
+        for (int i = at + kGroup - off; i < min(at + kGroup, V); ++i) top = fmaxf(top, load_io1(from, IO, i));
+    }
+    if (top > -INFINITY) look += (u64)((int64_t)__float2int_rn(fminf(fmaxf(top * by, -1e9f), 1e9f)) << 20) + 1;
+  }
+  return look;
+}
+
 // groups: of a warp (their tokens are consecutive, and the warps' in a block, the blocks' in a cluster).
 template <int IO>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int groups) {
@@ -554,14 +585,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (tid == kThreads - 1 && by_floor) sh.floor_log = (double)T * log((double)fminf(floor_p, 1.f));
   // Rows without limits and top-p read all tokens again: for the unit of their weights, the mean of the groups'
   // maxima in sixteenths of y, as a sum and a number.  (Of the groups, not the warps or blocks, so that
-  // a row's results do not depend on their number.)
+  // a row's results do not depend on their number, nor on where the row lies.)
   const bool looks = !greedy && !by_count && !by_floor && V >= 1 << 14;
-  u64 look = 0;
-  if (looks) {
-    for (int g = lane; g < groups; g += 32)
-      if (mine[g] > -INFINITY) look += (u64)((int64_t)__float2int_rn(fminf(fmaxf(mine[g] * c * 16.f, -1e9f), 1e9f)) << 20) + 1;
-    scan(sh, look);
-  }
+  if (looks) scan(sh, look_at<IO>(from, V, off, (rank * kWarps + warp) * groups, groups, mine, c * 16.f));
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top_key = max(top_key, sh.warp_key[w]);
@@ -577,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (sh.rank_key[q] > top_key) top_key = sh.rank_key[q], winner = q;
   Scale s = {logit_of(top_key), c, c_lo, 44, 15.f};
   if (looks) {
-    look = 0;
+    u64 look = 0;
     for (int q = 0; q < ranks; ++q) look += sh.rank_look[q];
     const float mean = (float)((int64_t)look >> 20) / (float)(look & 0xfffff);
     const float y = s.top * c - mean * 0.0625f;

@@ -516,8 +516,8 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages, int64_t pa
  * Weights are whole numbers of 2^-44 of the largest (a token 2^-45 below it is never drawn), right to 2^-27 of
  * themselves down to 2^-8 of the largest (2^-4 in the flattest rows) and to 2^-21 below; in rows of 2^14
  * tokens or more of which groups of 128 tokens have largest weights of 2^-16 or 2^-8 of the row's on average
- * (the logarithms' mean), the unit is 2^-38 or 2^-34.  Sums of them are exact: results do not depend on the
- * order of execution. */
+ * (the logarithms' mean), the unit is 2^-38 or 2^-34.  Sums of them are exact: a row's results depend neither on the
+ * order of execution nor on the row's place in memory or in the batch. */
 mq_status mq_sample(mq_type io, const void *logits, int64_t ld, int64_t B, int64_t V, const float *u,
                     const float *temperature, const int32_t *top_k, const float *top_p,
                     const float *min_p, int32_t *token, float *logprob, mq_stream stream);

@@ -59,3 +59,26 @@ def test_unit_of_the_weights(f):
     x[0, 5] = 0
     u = np.array([0.3], np.float32)
     run(f, x, u, 0, temperature=[1.0])
+
+
+@pytest.mark.parametrize("io_rows", [1, 2])
+@pytest.mark.parametrize("ranks_log", [0, 1])
+def test_results_do_not_depend_on_the_address(f, ranks_log, io_rows):
+    """The same logits from any element of a 16-byte block on: groups of 128 are counted from the row's start.  Of every
+    second group the first and the last token are heavy (2^-7.2), so that groups counted from a block's start would
+    all have one, and their mean another unit, in which the tokens at 2^-36 do not count."""
+    V, ln2 = 16384 + 70, np.log(2.0)
+    x = np.full((io_rows, V), -36 * ln2, np.float32)
+    x[:, 0::256] = x[:, 127::256] = -7.2 * ln2
+    x[:, 7] = 0
+    x[1:, 9000:9050] = np.nan
+    u = np.array([0.3, 0.9][:io_rows], np.float32)
+    want = st.sample(f, x, u, ranks_log, temperature=[1.0] * io_rows)
+    for shift in range(4):
+        for ld in (V + 2, V + 3):
+            wide = np.full(io_rows * ld + 8, 50, np.float32)
+            start = -(wide.ctypes.data // 4) % 4 + shift
+            view = wide[start:start + io_rows * ld].reshape(io_rows, ld)[:, :V]
+            view[:] = x
+            token, logprob = st.sample(f, view, u, ranks_log, temperature=[1.0] * io_rows)
+            assert token.tolist() == want[0].tolist() and logprob.tobytes() == want[1].tobytes(), (shift, ld)
