@@ -41,6 +41,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 
 #include "kv.cuh"
 #include "sample.cuh"
@@ -988,6 +989,7 @@ size_t smem_of(int groups, int ranks) { return (ranks > 1 ? 2 * kBins / ranks * 
 
 mq_status init_sample(DeviceState *st) {
   cudaError_t e = cudaSuccess;
+  for (int &n : st->sample_clusters) n = INT_MAX;
   auto set_up = [&](auto *kernel) {
     if (e != cudaSuccess) return;
     cudaFuncAttributes fa;
@@ -1011,10 +1013,12 @@ mq_status init_sample(DeviceState *st) {
       attr.val.clusterDim.x = 1 << i, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&st->sample_clusters[i], kernel, &cfg) != cudaSuccess) {
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
-        st->sample_clusters[i] = 0;
+        n = 0;
       }
+      st->sample_clusters[i] = std::min(st->sample_clusters[i], n);  // (what every type's kernel can have)
     }
   };
   set_up(sample_kernel<MQ_F32>);
@@ -1030,6 +1034,10 @@ mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *
   // would be left alone at the end: top-p with min-p, from 4 blocks down (64 rows with settings of their own 66 us,
   // 52 by twice as many; of the same settings 18, 35); top-p alone, from 2 down (128 rows 105, 99; 256 203,
   // 176; but 42 55, 61); min-p without it, from one (256 rows at T = 1 69, 59; of few tokens that stay 35, 44).
+  // It goes by which settings are given, not by what they hold: 64 rows with all four given and none in effect take 34 us,
+  // 23 by half as many blocks.  And eight blocks a row would do for a few more than 72 rows of settings of their own
+  // (73 rows 57, by the rule's four 69; 80 64, 73; 96 81, 76; 128 100, 80), four for more than 144 (160 85, by
+  // two 124; 256 131, 140).
   auto fits = [&](int ranks_log, int waves) {
     return ranks_log <= 4 && a.V >> ranks_log >= 2048 && a.B <= int64_t(waves) * st->sample_clusters[ranks_log];
   };

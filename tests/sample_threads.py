@@ -33,7 +33,9 @@ def build(folder):
     subprocess.run(["g++", "-O2", "-U_FORTIFY_SOURCE", "-std=c++17", "-shared", "-fPIC", "-ffp-contract=off", "-I", HERE, "-I", folder,
                     f'-DSAMPLE_CU="{os.path.join(folder, "sample.cu")}"', os.path.join(HERE, "sample_host.cpp"), "-o", lib],
                    check=True, capture_output=True, text=True)
-    f = ctypes.CDLL(lib).sample_host
+    library = ctypes.CDLL(lib)
+    f = library.sample_host
+    f.library = library
     p, i64 = ctypes.c_void_p, ctypes.c_int64
     f.argtypes = [ctypes.c_int, p, i64, i64, i64, p, p, p, p, p, p, p, p, ctypes.c_int, ctypes.c_uint]
     return f

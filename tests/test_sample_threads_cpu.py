@@ -1,5 +1,7 @@
 """mq_sample's kernel run on the host, its threads going on in any order that its barriers allow: results are the
 definition's, and the same to the last bit, whichever thread, warp or block is behind."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -82,3 +84,12 @@ def test_results_do_not_depend_on_the_address(f, ranks_log, io_rows):
             view[:] = x
             token, logprob = st.sample(f, view, u, ranks_log, temperature=[1.0] * io_rows)
             assert token.tolist() == want[0].tolist() and logprob.tobytes() == want[1].tobytes(), (shift, ld)
+
+
+def test_clusters_that_every_type_can_have(f):
+    """The kernels of the three types have one table: what is resident at once of each of them."""
+    per_kernel = [[100, 50, 24, 10, 5], [90, 60, 24, 11, -1], [120, 70, 30, 12, 6]]
+    given, out = (ctypes.c_int * 15)(*sum(per_kernel, [])), (ctypes.c_int * 5)()
+    init = f.library.sample_host_init
+    init.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    assert init(given, out) == 0 and list(out) == [90, 50, 24, 10, 0]

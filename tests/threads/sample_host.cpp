@@ -17,7 +17,11 @@ struct cudaLaunchConfig_t {
 };
 template <class K> cudaError_t cudaFuncGetAttributes(cudaFuncAttributes *, K *) { return cudaSuccess; }
 template <class K> cudaError_t cudaFuncSetAttribute(K *, int, int) { return cudaSuccess; }
-template <class K> cudaError_t cudaOccupancyMaxActiveClusters(int *n, K *, cudaLaunchConfig_t *) { return *n = 1, cudaSuccess; }
+inline const int *resident = nullptr;  // of each kernel's set-up, size by size: clusters, or -1 for one that cannot run
+template <class K> cudaError_t cudaOccupancyMaxActiveClusters(int *n, K *, cudaLaunchConfig_t *) {
+  *n = *resident++;
+  return *n < 0 ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
 inline cudaError_t cudaGetLastError() { return cudaSuccess; }
 
 namespace mq {
@@ -66,4 +70,12 @@ extern "C" int sample_host(int io, const void *logits, int64_t ld, int64_t B, in
   threads::which_order = order, threads::order_seed = seed;
   mq::fixed_bytes = sizeof(mq::Shared);
   return mq::launch_sample(a, nullptr, &st);
+}
+
+extern "C" int sample_host_init(const int *clusters, int *out) {
+  mq::DeviceState st;
+  resident = clusters;
+  const int r = mq::init_sample(&st);
+  for (int i = 0; i < 5; ++i) out[i] = st.sample_clusters[i];
+  return r;
 }
