@@ -60,10 +60,10 @@
 // on fixed latencies of conversions, shared memory and products; its copies alone take 55); 131072
 // bf16 keys of one sequence 53 us (76%: 42 of streaming, the rest the start, the first rows and the
 // join); 64 ragged sequences up to 8192, f16 97 to 100 us, Q8_0 67.5; one sequence of 37 keys, 14/2
-// heads of 64, 5.1.  Q4_0: those 64 sequences 58.2 us (39% of a plain copy's rate; the copies alone take 36.5,
+// heads of 64, 5.1.  Q4_0: those 64 sequences 58.9 us (39% of a plain copy's rate; the copies alone take 36.5,
 // all but the copies 55, without the second product 46, with half of the products' instructions
 // 47.4, without the conversion of the quants 52.6, without the scales of V 55.3; 12 warps of 16 or 32
-// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 32.6 us (34%); 37 keys 5.4.
+// keys 63 to 66, 16 of 16 keys 74.5); 131072 keys, bf16 activations (one part of the queries) 32.4 us (34%); 37 keys 5.4.
 #pragma once
 
 #include <algorithm>
@@ -873,20 +873,26 @@ attn_decode_kernel(const __grid_constant__ Params p) {
           }
         };
         if (C::kScaled) {  // a power of two that V's largest scale of the tile is below
-          uint32_t top = 0;
+          // (f16 bits of magnitudes order as numbers; with 0x400 more, those of infinities and NaN are negative: beside
+          // one the other products must stay numbers.  Two at a time 58.8 us of Q4_0's 64 sequences above, one by
+          // one 59.5; of Q8_0's 66.4 and 65.6.)
+          int top = 0;
+          uint32_t tops = 0x04000400u;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             uint32_t w[SW];
             scales_of(w, 1, 16 * m + (lane & 15));
             if (NG & 1) w[SW - 1] &= 0xffffu;
 #pragma unroll
-            for (int j = 0; j < SW; ++j)  // (f16 bits of magnitudes order as numbers)
-              top = max(top, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
+            for (int j = 0; j < SW; ++j) {
+              const uint32_t x = (w[j] & 0x7fff7fffu) + 0x04000400u;
+              if (C::kQ4) tops = __vmaxs2(tops, x);
+              else top = max(top, max((int)x >> 16, (int)(int16_t)x));
+            }
           }
-          top = __reduce_max_sync(0xffffffffu, top);
-          int e = top == 0 || top >= 0x7c00u
-                      ? 126
-                      : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
+          if (C::kQ4) top = max(tops & 0xffffu, tops >> 16);
+          top = __reduce_max_sync(0xffffffffu, max(top - 0x400, 0));
+          int e = top == 0 ? 126 : (int)(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))) >> 23);
           if (C::kQ4) e = max(e, 111);  // (up by 2^15 at most: a factor in f16)
           tile_unit = __uint_as_float(uint32_t(e + 1) << 23), per_unit = __uint_as_float(uint32_t(253 - e) << 23);
         }
