@@ -40,7 +40,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <cfloat>
 #include <climits>
 
 #include "kv.cuh"
@@ -444,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   grid_dependency();
   const int64_t row = a.slow_first ? row_of(sh, a, (int)blockIdx.y) : (int)blockIdx.y;
 
-  const float T = a.temperature ? a.temperature[row] : 1.f;
+  float T = a.temperature ? a.temperature[row] : 1.f;
+  if (T > 0.f) T = fmaxf(T, 0x1p-127f);  // (so that log2(e) / T is finite)
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.f, floor_p = a.min_p ? a.min_p[row] : 0.f;
   const float u = a.u[row];
@@ -575,12 +575,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the maximum ----
   uint32_t top_key = key_of(top);
   if (lane == 0) sh.warp_key[warp] = top_key;
-  // log2(e) / T: the quotient (finite, so that the largest logit's y is 0), and its remainder over T
+  // log2(e) / T: the quotient, and its remainder over T
   float c = 0.f, c_lo = 0.f;
   if (!greedy) {
     constexpr float e_hi = 1.44269502162933349609375f, e_lo = 1.92596299112661746887e-8f;
-    c = fminf(__fdiv_rn(e_hi, T), FLT_MAX);
-    if (c > 0.f && c < FLT_MAX) c_lo = __fdiv_rn(__fmaf_rn(-c, T, e_hi) + e_lo, T);
+    c = __fdiv_rn(e_hi, T);
+    if (c > 0.f) c_lo = __fdiv_rn(__fmaf_rn(-c, T, e_hi) + e_lo, T);
   }
   // (of min-p the border is exact to 64 bits: in flat rows thousands of tokens lie near it)
   if (tid == kThreads - 1 && by_floor) sh.floor_log = (double)T * log((double)fminf(floor_p, 1.f));

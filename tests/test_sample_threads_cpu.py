@@ -93,3 +93,15 @@ def test_clusters_that_every_type_can_have(f):
     init = f.library.sample_host_init
     init.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     assert init(given, out) == 0 and list(out) == [90, 50, 24, 10, 0]
+
+
+@pytest.mark.parametrize("T", [2.0 ** -149, 1e-40, 2.0 ** -128])
+def test_temperatures_below_the_smallest(f, T):
+    """A temperature below 2^-127, whose inverse binary32 does not hold, is taken as that: weights and logprob alike."""
+    x = np.array([[0.0, -1.0, -2.0, -0.5, -200.0] * 3], np.float32) * np.float32(2.0 ** -127)
+    for u in (0.05, 0.3, 0.5, 0.8, 0.97):
+        token, logprob = st.sample(f, x, [u], 0, temperature=[T])
+        want, lp, margin = exact(x[0], float(np.float32(u)), temperature=2.0 ** -127)
+        assert margin > 1e-3 and token[0] == want and abs(logprob[0] - lp) < 1e-6, (u, token, logprob, want, lp)
+    token, logprob = st.sample(f, x * np.float32(2.0 ** 100), [0.9], 0, temperature=[T])
+    assert token[0] == 10 and abs(logprob[0] - np.log(1 / 3)) < 1e-6
