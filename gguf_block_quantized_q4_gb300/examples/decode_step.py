@@ -19,6 +19,12 @@ class DecodeStep:
     (Weight of as many rows); the requests' settings as mq.sample takes them, one per sequence."""
 
     def __init__(self, embedding, layers, head, **settings):
+        if not layers:
+            raise ValueError("a step needs layers")
+        if head.N != embedding.shape[0]:  # (a token without a row would be read past the embedding's end)
+            raise ValueError(f"the head's {head.N} rows are not the embedding's {embedding.shape[0]}")
+        if len({len(layer.held) for layer in layers}) > 1:
+            raise ValueError("the layers are of unlike numbers of sequences")
         self.embedding, self.layers, self.head, self.settings = embedding, layers, head, settings
         n = len(layers[0].held)
         self.token = torch.zeros(n, dtype=torch.int32, device="cuda")    # the last ones, and their logprobs
