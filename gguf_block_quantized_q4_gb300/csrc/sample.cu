@@ -65,6 +65,7 @@ constexpr float kBinsPerHalving = 45.f;
 constexpr int kLastBin = kBins - 1;  // (2026 and up weigh nothing)
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added to a number, it leaves the nearest integer in the low bits
 constexpr uint32_t kMagicBits = 0x4b400000u;
+constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;  // log2(e) in two parts
 
 struct Shared {
   // the block's bins, low and high words; while a cut's tokens are sorted: its own list, all lists
@@ -160,6 +161,21 @@ struct Weights {
 __device__ __noinline__ u64 weight(const Scale &s, float x) {
   const float in[kSide] = {x, -INFINITY, -INFINITY, -INFINITY};
   return Weights(s, in).whole(s, in, 0);
+}
+
+// -(top - x) / T - ln(sum 2^-unit), rounded once: each in two parts.  The sum is the largest weight (2^unit) and what is
+// beside it; its logarithm y has the second part sum 2^-unit e^-y - 1 (one step of Newton's).
+__device__ __noinline__ float log_share(float top, float x, float T, u64 sum, int unit) {
+  const float d = __fsub_rn(top, x), b = __fsub_rn(d, top);
+  const float e = __fsub_rn(__fsub_rn(top, __fsub_rn(d, b)), __fadd_rn(x, b));  // top - x - d
+  const float l = __fdiv_rn(d, T), l_lo = l > 0.f ? __fdiv_rn(__fmaf_rn(-l, T, d) + e, T) : 0.f;
+  const float rest = (float)(sum - min(sum, u64(1) << unit));
+  const float y = log1pf(rest * __uint_as_float((uint32_t)(127 - unit) << 23));
+  const u64 one = __umul64hi(sum, precise(y, kLog2e, kLog2eLow, 0.f, 62));  // 2^(unit - 2), nearly
+  const float y_lo = (float)(int64_t)(one - (u64(1) << (unit - 2))) * __uint_as_float((uint32_t)(129 - unit) << 23);
+  const float s = __fadd_rn(l, y), v = __fsub_rn(s, l);
+  const float s_lo = __fadd_rn(__fsub_rn(l, __fsub_rn(s, v)), __fsub_rn(y, v));
+  return __fsub_rn(0.f, __fadd_rn(s, __fadd_rn(s_lo, __fadd_rn(l_lo, y_lo))));
 }
 
 // floor(x v) for 0 < x < 1, and whether x v is more than that.
@@ -578,9 +594,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // log2(e) / T: the quotient, and its remainder over T
   float c = 0.f, c_lo = 0.f;
   if (!greedy) {
-    constexpr float e_hi = 1.44269502162933349609375f, e_lo = 1.92596299112661746887e-8f;
-    c = __fdiv_rn(e_hi, T);
-    if (c > 0.f) c_lo = __fdiv_rn(__fmaf_rn(-c, T, e_hi) + e_lo, T);
+    c = __fdiv_rn(kLog2e, T);
+    if (c > 0.f) c_lo = __fdiv_rn(__fmaf_rn(-c, T, kLog2e) + kLog2eLow, T);
   }
   // (of min-p the border is exact to 64 bits: in flat rows thousands of tokens lie near it)
   if (tid == kThreads - 1 && by_floor) sh.floor_log = (double)T * log((double)fminf(floor_p, 1.f));
@@ -913,10 +928,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return !(u > 0.f) ? u64(0) : u < 1.f ? part_of(u, all, more) : all - 1;
   };
   auto drawn = [&](int i, float x, u64 all) {
-    // ln w - ln(sum): the sum is the largest weight and what is beside it
-    const u64 rest = all - min(all, u64(1) << s.unit);
-    const float l = x == s.top ? 0.f : -__fdiv_rn(__fsub_rn(s.top, x), T);
-    finish(i, l - log1pf((float)rest * __uint_as_float((uint32_t)(127 - s.unit) << 23)));
+    finish(i, log_share(s.top, x, T, all, s.unit));
   };
   if (held && held <= kCounted) {
     // every block has all that stays: each token's sum of the weights before it, by its index

@@ -105,3 +105,22 @@ def test_temperatures_below_the_smallest(f, T):
         assert margin > 1e-3 and token[0] == want and abs(logprob[0] - lp) < 1e-6, (u, token, logprob, want, lp)
     token, logprob = st.sample(f, x * np.float32(2.0 ** 100), [0.9], 0, temperature=[T])
     assert token[0] == 10 and abs(logprob[0] - np.log(1 / 3)) < 1e-6
+
+
+@pytest.mark.parametrize("V,size", [(1000, 1.0), (5000, 0.1), (16384, 2.0), (3, 5.0)])
+def test_log_probabilities_are_rounded_once(f, V, size):
+    """To binary32's nearest, but for the sum's own error (2^-26 of it) and what two parts of a quotient and a logarithm
+    leave (2^-28 of each)."""
+    g = np.random.default_rng(V)
+    B = 24
+    x = (g.standard_normal((B, V)) * size).astype(np.float32)
+    u = g.random(B).astype(np.float32)
+    for kw in ({"temperature": [0.9 + 0.1 * b for b in range(B)]}, {"top_k": [100] * B, "temperature": [1.7] * B}, {"min_p": [0.01] * B}):
+        token, logprob = st.sample(f, x, u, 0, **kw)
+        for b in range(B):
+            want, lp, margin = exact(x[b], float(u[b]), **{k: v[b] for k, v in kw.items()})
+            if margin < 2.0 ** -24:
+                continue
+            assert int(token[b]) == want
+            step = 2.0 ** (np.floor(np.log2(abs(lp) + 1e-30)) - 24)
+            assert abs(float(logprob[b]) - lp) <= step + 2.0 ** -26 + abs(lp) * 2.0 ** -27, (b, kw, logprob[b], lp)
