@@ -22,6 +22,7 @@
 #include <memory>
 #include <numeric>
 #include <set>
+#include <utility>
 #include <type_traits>
 #include <vector>
 
@@ -151,6 +152,9 @@ inline void entry() {
   leave(f);
 }
 
+constexpr size_t kGuard = 16;  // words behind (and, for alignment, before) a block's shared memory, which stay as they are
+inline uint8_t *aligned(const std::unique_ptr<uint64_t[]> &p) { return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p.get()) + 15) / 16 * 16); }
+
 // One cluster of `ranks` blocks: body(arg) in every thread.  order[i]: the i-th thread (rank * block + thread) that
 // goes on where it can.
 inline void run_cluster(int ranks, int block, dim3 first, size_t fixed, size_t dynamic, const std::vector<int> &order,
@@ -166,8 +170,10 @@ inline void run_cluster(int ranks, int block, dim3 first, size_t fixed, size_t d
   for (Block &b : m.blocks) {
     b.all.expected = b.left = block;
     b.fixed_bytes = fixed, b.dynamic_bytes = dynamic;
-    b.fixed = std::make_unique<uint64_t[]>(fixed / 8 + 2), b.dynamic = std::make_unique<uint64_t[]>(dynamic / 8 + 2);
-    std::memset(b.fixed.get(), 0xa5, fixed), std::memset(b.dynamic.get(), 0xa5, dynamic);
+    for (auto [at, bytes] : {std::pair(&b.fixed, fixed), std::pair(&b.dynamic, dynamic)}) {
+      *at = std::make_unique<uint64_t[]>(bytes / 8 + kGuard);
+      std::memset(at->get(), 0xa5, (bytes / 8 + kGuard) * 8);
+    }
   }
   machine = &m;
   constexpr size_t kStack = 64 << 10;
@@ -199,6 +205,10 @@ inline void run_cluster(int ranks, int block, dim3 first, size_t fixed, size_t d
     left -= m.now->done;
   }
   if (left) fail("threads wait for one another");
+  for (Block &b : m.blocks)
+    for (auto [at, bytes] : {std::pair(&b.fixed, fixed), std::pair(&b.dynamic, dynamic)})
+      for (size_t i = bytes; i < bytes + 8 * (kGuard - 2); ++i)
+        if (aligned(*at)[i] != 0xa5) fail("written behind shared memory");
   machine = nullptr;
 }
 
@@ -224,19 +234,17 @@ template <class T>
 T &shared() {
   Block &b = *self().block;
   if (sizeof(T) > b.fixed_bytes) fail("more shared memory than was laid out");
-  return *reinterpret_cast<T *>((reinterpret_cast<uintptr_t>(b.fixed.get()) + 15) / 16 * 16);
+  return *reinterpret_cast<T *>(aligned(b.fixed));
 }
-inline void *dynamic() { return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(self().block->dynamic.get()) + 15) / 16 * 16); }
+inline void *dynamic() { return aligned(self().block->dynamic); }
 template <class T>
 T *in_rank(T *p, int rank) {
   Fiber &f = self();
   Block &own = *f.block, &other = (&own - f.rank)[rank];
   if (other.left == 0) fail("shared memory of a block that has ended");
   const auto move = [&](std::unique_ptr<uint64_t[]> Block::*m, size_t bytes) -> T * {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = reinterpret_cast<uintptr_t>((own.*m).get());
-    if (at < base || at >= base + bytes + 16) return nullptr;
-    const uintptr_t a = (base + 15) / 16 * 16, to = (reinterpret_cast<uintptr_t>((other.*m).get()) + 15) / 16 * 16;
-    return reinterpret_cast<T *>(to + (at - a));
+    uint8_t *const at = reinterpret_cast<uint8_t *>(p), *const base = aligned(own.*m);
+    return at < base || at >= base + bytes ? nullptr : reinterpret_cast<T *>(aligned(other.*m) + (at - base));
   };
   if (T *q = move(&Block::fixed, own.fixed_bytes)) return q;
   if (T *q = move(&Block::dynamic, own.dynamic_bytes)) return q;
