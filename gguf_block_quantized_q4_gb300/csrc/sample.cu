@@ -18,7 +18,7 @@
 // nothing, and fewer than 2^19 tokens fit a 64-bit sum), of 2^-38 or 2^-34 in flat rows, whose deep
 // weights then fit 32 bits, which a shared atomic adds in 10 cycles a warp (64 bits take 25).  Sums of whole
 // numbers do not depend on their order, so neither do results: not on the cluster's size, nor on the
-// atomics.  The exponential is right to 2^-27 of itself down to 2^-8 of the largest weight: binary32's own
+// atomics, nor on the row's place.  The exponential is right to 2^-27 of itself down to 2^-8 of the largest weight: binary32's own
 // 2^-24 would move the running sum enough to name another token in one of a few hundred rows of
 // flat logits.  Below that it is the hardware's (2^-21, the errors of either sign).
 //
@@ -30,11 +30,11 @@
 // a list holds (nearly equal logits) the bin is divided in 2048 once more, and where that does not do
 // (equal ones) three rounds of bins, of the logit's bits, name the logit and a count of equals the index.
 //
-// Measured (f32): one row of 151936 with top-k 40 and top-p 12.9 us, greedy 3.9, the temperature alone 10, top-p of
-// a flat row 22 to 32; 64 such rows with limits of their own 52.5 us (nine times their bytes' time: rows of
-// top-p pass over their logits three times, eight blocks each); 256 with min-p 59.0 us (39% of a plain copy's
-// rate); 16 rows of 32003 bf16 logits, most of them masked, top-p 20.0 us.
-// (First form 25.0, 76.2, 155.4 and 23.3 us.)  Of the 50 thousand cycles of a flat top-p row the
+// Measured (f32): one row of 151936 with top-k 40 and top-p 13.3 us, greedy 3.9, the temperature alone 10.3, top-p of
+// a flat row 23 to 32; 64 such rows with limits of their own 44 to 58 us over twelve draws of these, 51 on average
+// (nine times their bytes' time: rows of top-p pass over their logits three times, eight blocks each); 256
+// with min-p 59.2 us (39% of a plain copy's rate); 16 rows of 32003 bf16 logits, most of them masked, top-p
+// 20.2 us.  (First form 25.0, 76.2, 155.4 and 23.3 us.)  Of the 50 thousand cycles of a flat top-p row the
 // histogram takes 7, the choice of its bin 7, the lists 7, their sort 8, the last sums 10: barriers of the
 // cluster in each.
 #include <cooperative_groups.h>
@@ -1059,7 +1059,7 @@ mq_status launch_sample(const SampleArgs &a, cudaStream_t s, const DeviceState *
   if (r <= most && fits(r + 1, 2)) ++r;
   const int ranks = 1 << r, groups = groups_of(a.V, ranks);
   // Where not all clusters are resident at once and rows differ in their cuts (two settings or more are given), the
-  // slow ones begin first: those 64 rows 57.7 us without, 52.5 with; finding its row costs a cluster 1.5 us (64
+  // slow ones begin first: those 64 rows (of one draw) 57.7 us without, 52.5 with; finding its row costs a cluster 1.5 us (64
   // rows of top-p alone 73 us, 78 with it).
   SampleArgs b = a;
   b.slow_first = !!a.top_k + !!a.top_p + !!a.min_p > 1 && a.B <= kThreads && a.B > st->sample_clusters[r];
