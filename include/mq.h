@@ -507,9 +507,10 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, const int32_t *pages, int64_t pa
  *           last token that weighs something)
  *   logprob ln(w_token / that sum); may be NULL
  * T that is not above 0 (NaN too) is greedy: the token with the largest logit, the first of equal
- * ones, logprob 0.  T below 2^-127 counts as 2^-127; T infinite: all finite logits weigh alike.  A
- * NaN logit counts as minus infinity, which weighs nothing; infinite ones share all weight among
- * themselves; a row with no finite or infinite logit gives token -1, logprob minus infinity.
+ * ones, logprob 0.  T below 2^-127 counts as 2^-127; T infinite: all finite logits weigh alike (but for
+ * ones whose distance to the largest is beyond binary32, which weigh nothing at any T).  A NaN logit counts
+ * as minus infinity, which weighs nothing; infinite ones share all weight among themselves; a row with no
+ * finite or infinite logit gives token -1, logprob minus infinity.
  * u, temperature, top_p, min_p: device f32 [B]; top_k: device int32 [B]; each but u may be NULL
  * (T = 1, no limit).  token: device int32 [B], logprob: device f32 [B], written; apart from the inputs
  * and each other.  1 <= V < 2^19, B < 2^16.  B = 0 does nothing.

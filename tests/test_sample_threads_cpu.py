@@ -124,3 +124,12 @@ def test_log_probabilities_are_rounded_once(f, V, size):
             assert int(token[b]) == want
             step = 2.0 ** (np.floor(np.log2(abs(lp) + 1e-30)) - 24)
             assert abs(float(logprob[b]) - lp) <= step + 2.0 ** -26 + abs(lp) * 2.0 ** -27, (b, kw, logprob[b], lp)
+
+
+def test_distances_beyond_binary32(f):
+    """What the header says of logits that lie further apart than binary32 reaches, at any temperature."""
+    x = np.array([[3e38, -3e38, 2.9e38, 0.0]], np.float32)
+    for u, T, want in ((0.5, np.inf, 2), (0.99, np.inf, 3), (0.1, 1e38, 0), (0.99, 1e38, 3)):
+        token, logprob = st.sample(f, x, [u], 0, temperature=[T])
+        w = np.exp((x[0, [0, 2, 3]].astype(np.float64) - 3e38) / T)
+        assert token[0] == want and abs(logprob[0] - np.log(w[[0, 2, 3].index(want)] / w.sum())) < 1e-6
